@@ -281,7 +281,7 @@ def run(s):
                               interleaved=s["case"]["pairs"], out=s["q"])
             return s["q"], s["recent"]
         if op == "attention":
-            return w12.w12_kv_attention(cache, 0, s["q"], s["row_off"], s["case"]["rows"], slot=s["slot"], parent=s["parent"], out=s["out"])
+            return w12.w12_kv_attention(cache, 0, s["q"], s["row_off"], slot=s["slot"], parent=s["parent"], out=s["out"])
         w12.w12_kv_commit(cache, s["row_off"], s["accept_len"], path=s["path"], slot=s["slot"], length_out=s["length_out"])
         return s["codes"], s["scales"], s["recent"], s["length_out"]
     return {"append": _append, "attention": _attention, "commit": _commit, "sampled": _sampled}[op](s)
