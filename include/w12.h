@@ -348,6 +348,163 @@ w12_status tree_accept(int32_t num_trees, const int32_t *node_off,
                        int32_t *accept_len, int32_t *path, int32_t *bonus,
                        hipStream_t stream);
 
+/*
+ * KV cache of the verify pass. [S1] 4.3: a pass runs the target over draft
+ * trees and keeps one root path of each; [S1] 4.4: prompts share the pass,
+ * their rows a chain. The cache holds, per layer:
+ *   pages   [layers][num_pages][kv_heads][2 (K, V)][page_tokens * head_dim]
+ *           8-bit codes of whole blocks of page_tokens committed tokens,
+ *           W12_KV_E4M3 (OCP e4m3) or W12_KV_INT8;
+ *   scales  [layers][num_pages][kv_heads][2] fp32: a code stands for
+ *           code * scale, one scale per block, head and K or V;
+ *   recent  [layers][slots][kv_heads][2][recent_rows * head_dim] bf16: the
+ *           committed tokens of a sequence's unfinished block (its first
+ *           len % page_tokens rows), then the rows of the current step.
+ * and for all layers:
+ *   page_table [slots][max_pages] int32: page of each block of a sequence;
+ *   len        [slots] int32: committed tokens of each sequence.
+ * A block is quantised once, when its last token is committed, from bf16: the
+ * pages depend on the accepted tokens only, not on rejected drafts or on how
+ * tokens were grouped into steps.
+ * Order inside a block and inside the recent rows: keys of 32 tokens x 32
+ * dims lie as [2 halves of 16 dims][32 tokens][16 dims], values as [2][32
+ * dims][16 tokens], half h holding tokens 8 i + 4 h + j (i, j < 4) at 4 i + j;
+ * such fragments are ordered by 32 tokens, then by 32 dims.
+ * Sizes: page_tokens 32, 64, 96 or 128; head_dim 64, 128 or 256; recent_rows
+ * a multiple of 32 in [page_tokens, 1024]; kv_heads <= 256; slots <= 2^20;
+ * max_pages * page_tokens <= 2^30. pages and recent 16-byte, scales 8-byte
+ * aligned.
+ *
+ * A step's calls share its rows: sequence s owns rows [row_off[s],
+ * row_off[s + 1]) of total_rows (at most 512, at most 512 sequences), a tree
+ * with tree-local parents as in tree_accept, or, with parent NULL, a chain
+ * (row i follows row i - 1: prompts, plain decoding, chains of drafts). slot
+ * [num_seq] names each sequence's slot (NULL: its own index). Rows of no
+ * sequence are left as they are.
+ */
+typedef enum { W12_KV_E4M3 = 0, W12_KV_INT8 = 1 } w12_kvtype;
+
+typedef struct w12_kv_cache {
+  int32_t kvtype, layers, num_pages, kv_heads, page_tokens, head_dim, slots, recent_rows, max_pages;
+  uint8_t *pages;
+  float *scales;
+  uint16_t *recent;
+  const int32_t *page_table;
+  int32_t *len;
+} w12_kv_cache;
+
+/*
+ * w12_kv_append -- rotates a step's queries and keys by their positions and
+ * puts keys and values behind the sequence's committed tokens, as rows that
+ * w12_kv_attention sees and w12_kv_commit keeps or drops. len is not changed:
+ * appending again overwrites the step's rows.
+ *   qkv  [total_rows][(q_heads + 2 kv_heads) * head_dim] fp32 or bf16
+ *        (qkv_type a w12_ydtype): query heads, key heads, value heads, as the
+ *        fused Wq|Wk|Wv product writes them.
+ *   rope [positions][rot_dim] fp32: cosines of the rot_dim / 2 angles of a
+ *        position, then their sines. The row at depth d of its tree has
+ *        position len + d. The first rot_dim dims (even) of each query and
+ *        key head turn in pairs (i, i + rot_dim / 2), or (2 i, 2 i + 1) if
+ *        interleaved; computed in fp32, rounded to bf16 once.
+ *   q    [total_rows][q_heads][head_dim] bf16 out: the rotated queries.
+ * Device-detected, reported as NaN queries: an invalid tree, a slot outside
+ * [0, slots) or of an earlier sequence of the call, a length outside the
+ * page table, more rows than recent_rows - len % page_tokens (nothing of such
+ * a sequence is written to the cache); a position outside [0, positions)
+ * (that row's query, and its key's rotated dims).
+ */
+w12_status w12_kv_append(const w12_kv_cache *cache, int32_t layer, int32_t num_seq, const int32_t *slot,
+                         const int32_t *row_off, int32_t total_rows, const int32_t *parent, const void *qkv,
+                         int qkv_type, int32_t q_heads, const float *rope, int32_t positions, int32_t rot_dim,
+                         int32_t interleaved, uint16_t *q, hipStream_t stream);
+
+/* Workspace bytes w12_kv_attention needs (host output). */
+w12_status w12_kv_attention_workspace(const w12_kv_cache *cache, int32_t num_seq, int32_t total_rows, int32_t q_heads,
+                                      size_t *bytes);
+
+/*
+ * w12_kv_attention -- attention of a step's rows: row i attends to its
+ * sequence's committed tokens and to its own ancestors among the step's rows,
+ * itself included,
+ *   out[i, h] = softmax(scale q[i, h] . K) V,  kv head h / (q_heads / kv_heads),
+ * with fp32 scores, sums and accumulation; probabilities and 8-bit codes
+ * enter the matrix products as bf16 (the codes exactly). Infinities and NaN
+ * in rows that a row does not see never reach it. The split of long
+ * sequences over workgroups is in a fixed order: results are bitwise
+ * reproducible.
+ *   q    [total_rows][q_heads][head_dim] bf16 (w12_kv_append's output).
+ *   out  [total_rows][q_heads * head_dim] bf16: the x of the Wo product.
+ *   ws   zero-filled workspace of >= w12_kv_attention_workspace bytes, 256-byte
+ *        aligned; left zero-filled where it must be.
+ * Device-detected, reported as NaN outputs of the sequence: what w12_kv_append
+ * lists (a slot named twice is allowed here), and a page id outside
+ * [0, num_pages). A block with a NaN scale reads as NaN.
+ */
+w12_status w12_kv_attention(const w12_kv_cache *cache, int32_t layer, int32_t num_seq, const int32_t *slot,
+                            const int32_t *row_off, int32_t total_rows, const int32_t *parent, const uint16_t *q,
+                            int32_t q_heads, float scale, uint16_t *out, void *ws, size_t ws_bytes,
+                            hipStream_t stream);
+
+/*
+ * w12_kv_commit -- keeps the accepted rows of a step, in all layers at once:
+ * row path[0 .. accept_len] of each sequence (tree_accept's outputs: path
+ * [total_rows], tree-local and ascending from the root; NULL: the first
+ * accept_len + 1 rows) join its committed tokens in order. Every block that
+ * becomes full is quantised into its page (page_table[slot][len / page_tokens
+ * ...] must name pages for them): scale = the smallest power of two with
+ * amax <= 448 scale (e4m3, at least 2^-126) or amax / 127 (int8), 1 for a block
+ * of zeros; code = value / scale, rounded to nearest even. A block that holds
+ * an infinity or NaN gets scale NaN. The rows left move to the front of the
+ * recent rows.
+ *   len_out [slots] out: the new length of each sequence's slot, other
+ *           entries left as they are; may be the cache's own len.
+ * accept_len -1 (a refused tree) keeps nothing. Device-detected, reported as
+ * length -1 with nothing written: what w12_kv_append lists (trees aside), an
+ * accept_len or path outside the sequence's rows or not ascending from row 0,
+ * a page id outside [0, num_pages), no room in the page table.
+ */
+w12_status w12_kv_commit(const w12_kv_cache *cache, int32_t num_seq, const int32_t *slot, const int32_t *row_off,
+                         int32_t total_rows, const int32_t *accept_len, const int32_t *path, int32_t *len_out,
+                         hipStream_t stream);
+
+/* Workspace bytes tree_accept_sampled needs (host output). */
+w12_status tree_accept_sampled_workspace(int32_t num_trees, int32_t total_nodes, int32_t vocab, size_t *bytes);
+
+/*
+ * tree_accept_sampled -- tree verification of sampling requests: drafted
+ * tokens against the target's probabilities, from given random numbers ([S3]
+ * speculative sampling: accept with min(1, p / q), else draw from max(0, p -
+ * q)). Trees as in tree_accept (at most 1024 nodes each, total_nodes and
+ * num_trees at most 65535); row i of logits belongs to node i,
+ *   p = softmax(logits[i] / temperature[tree]).
+ * From the root, a node's children are tried in index order against what
+ * the rejections so far have left of p: child c with token x is accepted, and
+ * the walk goes on from it, if u_accept[c] q(x) < p(x); otherwise p becomes
+ * max(p - q, 0), normalised. q = draft[i] (the distribution that node i's
+ * children were drawn from), or, with draft NULL, one at x (drafts that were
+ * chosen, not drawn). Where no child is accepted the walk ends, and the bonus
+ * token is the lowest t whose cumulative sum of p exceeds u_bonus[tree] times
+ * the whole sum (the last token with p > 0 if none does). The tokens that come
+ * out are distributed as if drawn from the target alone.
+ * Probabilities, sums and comparisons are held in 64 bits.
+ *   logits  [total_nodes][vocab] fp32 or bf16 (logits_type a w12_ydtype),
+ *           w12_gemm's y of the head; vocab <= 2^28.
+ *   temperature [num_trees] fp32 > 0, or NULL (1); draft [total_nodes][vocab]
+ *           fp32 or NULL (rows of nodes without children are not read);
+ *   u_accept [total_nodes], u_bonus [num_trees] fp32 in [0, 1).
+ *   accept_len, path, bonus: as tree_accept's.
+ *   ws      workspace, 16-byte aligned, content ignored.
+ * Device-detected, reported as accept_len = bonus = -1 and a path of -1: what
+ * tree_accept lists, a drafted token outside [0, vocab), more than 1024
+ * nodes, a temperature that is not positive and finite, and a row on the walk
+ * whose logits hold NaN, +inf or nothing but -inf.
+ */
+w12_status tree_accept_sampled(int32_t num_trees, const int32_t *node_off, int32_t total_nodes, const int32_t *parent,
+                               const int32_t *token, const void *logits, int logits_type, int32_t vocab,
+                               const float *temperature, const float *draft, const float *u_accept,
+                               const float *u_bonus, int32_t *accept_len, int32_t *path, int32_t *bonus, void *ws,
+                               size_t ws_bytes, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,539 @@
+"""GPU parity of the KV cache (w12_kv_append, w12_kv_attention, w12_kv_commit,
+through the C ABI) against the 64-bit oracle. Committed bytes and scales match
+exactly; rotated rows and attention outputs within the roundings that the
+tolerances count."""
+import numpy as np
+import pytest
+
+import synth
+from oracle import kv_cache as KV
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+
+
+def say(*a):
+    print("[kv]", *a, flush=True)
+
+
+@pytest.fixture(scope="module")
+def w12():
+    import torch
+    import w12_weight_streaming_amd as w
+    assert torch.cuda.is_available()
+    w.lib()
+    return w
+
+
+def i32(a):
+    import torch
+    return None if a is None else torch.tensor(np.asarray(a), dtype=torch.int32, device=DEV)
+
+
+def f64(t):
+    return t.float().cpu().numpy().astype(np.float64)
+
+
+def bf16(a):
+    """numpy -> bf16 tensor on the GPU, and the values it holds."""
+    import torch
+    t = torch.tensor(np.asarray(a), dtype=torch.float32).bfloat16()
+    return t.to(DEV), f64(t)
+
+
+def rope_table(positions, rot):
+    ang = np.arange(positions)[:, None] * 10000.0 ** (-np.arange(0, rot, 2) / rot)
+    return np.concatenate([np.cos(ang), np.sin(ang)], 1).astype(np.float32)
+
+
+def random_parents(rng, n):
+    return np.array([-1] + [int(rng.randint(max(0, i - 6), i)) for i in range(1, n)], np.int32)
+
+
+class Serving:
+    """A cache on the GPU and the oracle's state of it, driven step by step."""
+
+    def __init__(self, w12, seqs, kv, group, dim, page, int8=False, layers=1, step_rows=64, blocks=24, seed=0,
+                 rot=None, interleaved=False, positions=4096):
+        import torch
+        self.w12, self.seqs, self.kv, self.group, self.dim, self.page, self.layers = w12, seqs, kv, group, dim, page, layers
+        self.rng = np.random.RandomState(seed)
+        self.slots = seqs + 2
+        self.slot = self.rng.permutation(self.slots)[:seqs].astype(np.int32)
+        pages = seqs * blocks + 3
+        self.cache = w12.kv_cache(layers, kv, dim, pages, self.slots, blocks, page, step_rows, int8, DEV)
+        ids = self.rng.permutation(pages)[:seqs * blocks].reshape(seqs, blocks)
+        table = np.full((self.slots, blocks), -7, np.int32)
+        table[self.slot] = ids
+        self.table = table
+        self.cache.page_table.copy_(i32(table))
+        # what no token wrote yet must never matter
+        self.cache.recent.fill_(float("nan"))
+        self.cache.scales.fill_(float("nan"))
+        self.int8, self.rot, self.interleaved = int8, rot or dim, interleaved
+        self.rope = rope_table(positions, self.rot)
+        self.rope_t = torch.tensor(self.rope, device=DEV)
+        self.state = [[[KV.Sequence(page, int8, dim) for _ in range(kv)] for _ in range(seqs)] for _ in range(layers)]
+
+    def step(self, rows, parents=None, f32=False, check=True, commit=None, paths=None, qkv=None):
+        """Append and attend in every layer, then commit. rows: rows of each
+        sequence; parents: per sequence or None (chains); commit: accept_len
+        of each (default: all rows of a chain, a root path of a tree)."""
+        import torch
+        w12, off = self.w12, np.concatenate([[0], np.cumsum(rows)]).astype(np.int32)
+        total, heads = int(off[-1]), self.kv * self.group
+        par = None if parents is None else i32(np.concatenate(parents))
+        each = parents if parents is not None else [KV.chain(n) for n in rows]
+        width = (heads + 2 * self.kv) * self.dim
+        drafted = []
+        for layer in range(self.layers):
+            x = self.rng.randn(total, width).astype(np.float32) if qkv is None else qkv
+            xt = torch.tensor(x, device=DEV)
+            xt = xt if f32 else xt.bfloat16()
+            xv = f64(xt).reshape(total, -1, self.dim)
+            q = w12.w12_kv_append(self.cache, layer, xt, i32(off), self.rope_t, heads, slot=i32(self.slot), parent=par,
+                                  interleaved=self.interleaved)
+            out = w12.w12_kv_attention(self.cache, layer, q, i32(off), slot=i32(self.slot), parent=par)
+            torch.cuda.synchronize()
+            got_q, got = f64(q), f64(out).reshape(total, heads, self.dim)
+            rec = f64(self.cache.recent[layer])
+            per_seq = []
+            for s in range(self.seqs):
+                a, b = off[s], off[s + 1]
+                if a == b:
+                    per_seq.append(None)
+                    continue
+                length = self.state[layer][s][0].length
+                pos = length + KV.depths(each[s])
+                turned, size = KV.rotate(xv[a:b, :heads + self.kv], pos, self.rope, self.interleaved)
+                # one rounding to bf16, and three in fp32 of |x cos| + |y sin|
+                tol = 2.0 ** -8 * np.abs(turned) + 4 * 2.0 ** -24 * size
+                tail = length % self.page
+                at = np.arange(tail, tail + b - a)
+                k = np.stack([rec[self.slot[s], h, 0][KV.key_places(tail + b - a, self.dim)[at]] for h in range(self.kv)], 1)
+                v = np.stack([rec[self.slot[s], h, 1][KV.value_places(tail + b - a, self.dim)[at]] for h in range(self.kv)], 1)
+                if check:
+                    assert (np.abs(got_q[a:b] - turned[:, :heads]) <= tol[:, :heads]).all(), ("q", layer, s)
+                    assert (np.abs(k - turned[:, heads:]) <= tol[:, heads:]).all(), ("k", layer, s)
+                    want_v = xv[a:b, heads + self.kv:]
+                    assert (np.abs(v - want_v) <= 2.0 ** -8 * np.abs(want_v)).all(), ("v", layer, s)
+                    for h in range(self.kv):
+                        seq = self.state[layer][s][h]
+                        see = np.concatenate([np.ones((b - a, length), bool), KV.ancestors(each[s])], 1)
+                        ref, av, sz = KV.attention(got_q[a:b, h * self.group:(h + 1) * self.group],
+                                                   np.concatenate([seq.k, k[:, h]]), np.concatenate([seq.v, v[:, h]]), see,
+                                                   self.dim ** -0.5)
+                        lim = KV.attention_tolerance(ref, av, sz, length + b - a, self.dim)
+                        err = np.abs(got[a:b, h * self.group:(h + 1) * self.group] - ref)
+                        assert (err <= lim).all(), ("attention", layer, s, h, float((err / lim).max()))
+                per_seq.append((k, v))
+            drafted.append(per_seq)
+        acc, path = [], []
+        for s in range(self.seqs):
+            n = rows[s]
+            if parents is None:
+                a = n - 1 if commit is None else commit[s]
+                way = np.arange(n)
+            else:
+                node = int(self.rng.randint(n))
+                way = [node]
+                while each[s][way[0]] >= 0:
+                    way.insert(0, int(each[s][way[0]]))
+                a = len(way) - 1
+                if commit is not None:
+                    a = min(a, commit[s])
+            acc.append(a)
+            path.append(np.concatenate([np.asarray(way, np.int32)[:a + 1], np.full(n - min(a + 1, n), -1, np.int32)]))
+        w12.w12_kv_commit(self.cache, i32(off), i32(acc), path=None if parents is None else i32(np.concatenate(path)),
+                          slot=i32(self.slot))
+        for layer in range(self.layers):
+            for s in range(self.seqs):
+                if acc[s] >= 0:
+                    k, v = drafted[layer][s]
+                    for h in range(self.kv):
+                        self.state[layer][s][h].commit(k[path[s][:acc[s] + 1], h], v[path[s][:acc[s] + 1], h])
+        if check:
+            self.check()
+        return acc
+
+    def check(self):
+        """Lengths, pages, scales and the recent tail are the oracle's, bit for bit."""
+        length = self.cache.length.cpu().numpy()
+        codes = self.cache.pages.float().cpu().numpy()
+        scales = self.cache.scales.cpu().numpy()
+        for layer in range(self.layers):
+            rec = f64(self.cache.recent[layer])
+            for s in range(self.seqs):
+                assert length[self.slot[s]] == self.state[layer][s][0].length
+                for h in range(self.kv):
+                    seq = self.state[layer][s][h]
+                    for b, blk in enumerate(seq.blocks):
+                        pid = self.table[self.slot[s], b]
+                        for v in (0, 1):
+                            assert np.array_equal(scales[layer, pid, h, v], blk[2 * v + 1], equal_nan=True), (layer, s, h, b, v)
+                            if blk[2 * v] is not None:
+                                got = codes[layer, pid, h, v][KV.places(v, self.page, self.dim)]
+                                assert np.array_equal(got, blk[2 * v]), ("codes", layer, s, h, b, v)
+                    tail = seq.length % self.page
+                    if tail:
+                        for v, x in ((0, seq.k), (1, seq.v)):
+                            got = rec[self.slot[s], h, v][KV.places(v, tail, self.dim)]
+                            assert np.array_equal(got, x[seq.length - tail:], equal_nan=True), ("tail", layer, s, h, v)
+
+
+# (seqs, kv heads, group, dim, page, int8, rows of the steps)
+CASES = [
+    (1, 1, 1, 64, 32, False, [1, 1, 31, 1, 64, 3]),
+    (3, 2, 6, 128, 64, False, [40, 24, 1, 64, 63, 2]),
+    (2, 4, 6, 256, 64, False, [64, 33, 30, 1, 1]),
+    (2, 3, 5, 64, 96, True, [64, 31, 1, 1, 64]),
+    (4, 1, 8, 128, 128, True, [64, 63, 1, 5, 64, 60]),
+    (2, 2, 12, 256, 32, True, [17, 47, 32, 1]),
+    (5, 8, 1, 128, 64, False, [3, 60, 1, 1]),
+]
+
+
+@pytest.mark.parametrize("seqs,kv,group,dim,page,int8,steps", CASES)
+def test_chains(w12, seqs, kv, group, dim, page, int8, steps):
+    say("chains", seqs, kv, group, dim, page, int8)
+    sv = Serving(w12, seqs, kv, group, dim, page, int8, seed=dim + page)
+    for i, n in enumerate(steps):
+        rows = [max(1, n - 5 * s) for s in range(seqs)]
+        sv.step(rows, f32=i % 2 == 1)
+
+
+@pytest.mark.parametrize("seqs,kv,group,dim,page,int8,steps", CASES)
+def test_trees_keep_one_path(w12, seqs, kv, group, dim, page, int8, steps):
+    say("trees", seqs, kv, group, dim, page, int8)
+    sv = Serving(w12, seqs, kv, group, dim, page, int8, seed=dim + page + 1, layers=2 if dim < 256 else 1)
+    sv.step([page - 3 if page < 65 else 61] * seqs)
+    for i in range(6):
+        rows = [int(sv.rng.randint(1, 33)) for _ in range(seqs)]
+        sv.step(rows, parents=[random_parents(sv.rng, n) for n in rows])
+
+
+@pytest.mark.parametrize("rot,interleaved", [(128, False), (64, False), (32, True), (2, False), (2, True), (30, False), (126, True)])
+def test_rotations(w12, rot, interleaved):
+    say("rotation", rot, interleaved)
+    sv = Serving(w12, 2, 2, 3, 128, 32, seed=rot, rot=rot, interleaved=interleaved)
+    sv.step([40, 7])
+    rows = [9, 20]
+    sv.step(rows, parents=[random_parents(sv.rng, n) for n in rows], f32=True)
+
+
+@pytest.mark.parametrize("dim,group", [(64, 6), (128, 2)])
+def test_prompt_of_512_rows(w12, dim, group):
+    say("prompt 512", dim)
+    sv = Serving(w12, 1, 1, group, dim, 64, step_rows=512, seed=dim)
+    sv.step([45])
+    sv.step([512])
+    sv.step([1])
+
+
+def test_long_context_is_split_and_joined(w12):
+    """A sequence long enough that many workgroups share an item, next to
+    short and empty ones."""
+    say("long")
+    sv = Serving(w12, 3, 2, 4, 64, 32, step_rows=512, blocks=200, seed=4, positions=8192)
+    for n in range(10):
+        sv.step([490, 20, 1], check=n in (0, 9), commit=[489, -1, 0])  # 511 rows: a step holds 512
+    rows = [32, 5, 1]
+    sv.step(rows, parents=[random_parents(sv.rng, n) for n in rows])
+
+
+def test_512_sequences_of_one_row(w12):
+    say("512 sequences")
+    sv = Serving(w12, 512, 1, 2, 64, 32, step_rows=8, blocks=2, seed=5)
+    for _ in range(2):
+        sv.step([1] * 512)
+
+
+def test_pages_do_not_depend_on_grouping(w12):
+    """The same tokens in one prompt, or one by one behind rejected drafts,
+    leave the same pages and tail."""
+    import torch
+    say("grouping")
+    rng = np.random.RandomState(6)
+    kv, dim, n = 2, 128, 70
+    x = rng.randn(n, 4 * dim).astype(np.float32)
+    junk = rng.randn(n, 4 * dim).astype(np.float32)
+    rope = torch.tensor(rope_table(200, dim), device=DEV)
+    caches = []
+    for one_by_one in (False, True):
+        c = w12.kv_cache(1, 1, dim, 4, 1, 4, 32, 96, False, DEV)
+        c.page_table.copy_(i32([[0, 1, 2, 3]]))
+        if not one_by_one:
+            w12.w12_kv_append(c, 0, torch.tensor(x, device=DEV), i32([0, n]), rope, 2)
+            w12.w12_kv_commit(c, i32([0, n]), i32([n - 1]))
+        else:
+            for i in range(n):  # a row, with two drafts behind it that are dropped
+                rows = np.stack([x[i], junk[i], junk[i] * 100])
+                w12.w12_kv_append(c, 0, torch.tensor(rows, device=DEV), i32([0, 3]), rope, 2, parent=i32([-1, 0, 0]))
+                w12.w12_kv_commit(c, i32([0, 3]), i32([0]), path=i32([0, -1, -1]))
+        assert c.length.item() == n
+        caches.append(c)
+    a, b = caches
+    assert torch.equal(a.pages.view(torch.uint8)[:, :2], b.pages.view(torch.uint8)[:, :2])
+    assert torch.equal(a.scales[:, :2], b.scales[:, :2])
+    for v in (0, 1):
+        at = torch.tensor(KV.places(v, n % 32, dim).ravel(), device=DEV)
+        assert torch.equal(a.recent[0, 0, 0, v][at], b.recent[0, 0, 0, v][at])
+
+
+def test_special_values_close_blocks(w12):
+    """Zeros, one large value, tiny values, an infinity and a NaN in a block."""
+    import torch
+    say("special blocks")
+    for int8 in (False, True):
+        dim, page = 64, 32
+        sv = Serving(w12, 1, 1, 1, dim, page, int8, seed=8, step_rows=256)
+        x = np.zeros((6 * page, 3 * dim), np.float32)
+        r = np.random.RandomState(9)
+        x[page:2 * page] = r.randn(page, 3 * dim) * 2.0 ** -120
+        x[2 * page:3 * page] = r.randn(page, 3 * dim)
+        x[2 * page + 5, dim + 3] = 3e38
+        x[3 * page:4 * page] = r.randn(page, 3 * dim)
+        x[3 * page + 1, 2 * dim + 7] = np.inf
+        x[4 * page:5 * page] = r.randn(page, 3 * dim)
+        x[4 * page + 1, 2 * dim + 9] = np.nan
+        x[5 * page:] = 448 * r.choice([-1, 1], (page, 3 * dim))
+        # each block in one step from row 0, so that rotation leaves its first row alone
+        off, q = i32([0, 6 * page]), None
+        rope = torch.tensor(np.concatenate([np.ones((256, dim // 2)), np.zeros((256, dim // 2))], 1), dtype=torch.float32, device=DEV)
+        w12.w12_kv_append(sv.cache, 0, torch.tensor(x, device=DEV), off, rope, 1, slot=i32(sv.slot))
+        w12.w12_kv_commit(sv.cache, off, i32([6 * page - 1]), slot=i32(sv.slot))
+        _, vals = bf16(x)
+        with np.errstate(invalid="ignore"):
+            sv.state[0][0][0].commit(vals[:, dim:2 * dim], vals[:, 2 * dim:])
+        sv.check()
+
+
+def test_nan_and_inf_reach_only_rows_that_see_them(w12):
+    """Siblings' infinities and NaN, in keys and values, and garbage behind
+    the rows, stay out of a row's output; its own ancestors' come through."""
+    import torch
+    say("nan")
+    kv, group, dim, page, n = 1, 3, 128, 32, 40
+    sv = Serving(w12, 1, kv, group, dim, page, seed=10)
+    sv.step([29])
+    parent = np.array([-1] + [0] * 10 + list(range(10, 39)), np.int32)  # ten leaves, then a chain from the tenth
+    rng = np.random.RandomState(11)
+    x = rng.randn(n, (kv * group + 2 * kv) * dim).astype(np.float32)
+    outs = []
+    for dirty in (False, True):
+        y = x.copy()
+        if dirty:
+            y[1, group * dim + 5] = np.inf                # leaf 1's key
+            y[2, (group + 1) * dim:] = np.nan             # leaf 2's value
+            y[3, (group + 1) * dim + 7] = -np.inf         # leaf 3's value
+            y[39, (group + 1) * dim + 100] = np.inf       # the chain's last row
+        q = w12.w12_kv_append(sv.cache, 0, torch.tensor(y, device=DEV), i32([0, n]), sv.rope_t, group, slot=i32(sv.slot),
+                              parent=i32(parent))
+        outs.append(f64(w12.w12_kv_attention(sv.cache, 0, q, i32([0, n]), slot=i32(sv.slot), parent=i32(parent))))
+    clean, dirty = outs
+    same = [i for i in range(n) if i not in (1, 2, 3, 39)]
+    assert np.array_equal(clean[same], dirty[same])
+    d = dirty.reshape(n, group, dim)
+    assert np.isnan(d[1]).all() and np.isnan(d[2]).all()
+    assert (d[3, :, 7] == -np.inf).all() and np.isfinite(np.delete(d[3], 7, axis=1)).all()
+    assert (d[39, :, 100] == np.inf).all() and np.array_equal(np.delete(d[39], 100, axis=1), np.delete(clean.reshape(n, group, dim)[39], 100, axis=1))
+
+
+def attend(w12, sv, q, off, **kw):
+    import torch
+    out = torch.full((q.shape[0] + 2, q.shape[1] * q.shape[2]), 7.0, dtype=torch.bfloat16, device=DEV)
+    w12.w12_kv_attention(sv.cache, 0, q, i32(off), out=out, **kw)
+    torch.cuda.synchronize()
+    return f64(out)
+
+
+def test_device_detected_errors_poison_only_their_sequence(w12):
+    import torch
+    say("refused sequences")
+    sv = Serving(w12, 4, 2, 2, 64, 32, seed=12)
+    sv.step([40, 40, 40, 40])
+    off = [0, 3, 6, 9, 12]
+    q, _ = bf16(sv.rng.randn(12, 4, 64))
+    good = attend(w12, sv, q, off, slot=i32(sv.slot))
+    assert np.isfinite(good).all() and (good[12:] == 7).all()
+
+    def only(seq, got, where):
+        rows = np.arange(off[seq], off[seq + 1])
+        rest = np.setdiff1d(np.arange(14), rows)
+        assert np.isnan(got[rows]).all(), where
+        assert np.array_equal(got[rest], good[rest]), where
+    par = [np.array([-1, 0, 1]) for _ in range(4)]
+    assert np.array_equal(attend(w12, sv, q, off, slot=i32(sv.slot), parent=i32(np.concatenate(par))), good)
+    for bad in ([0, 0, 1], [-1, 1, 1], [-1, 0, 2], [-1, -1, 0], [-1, 0, 9999], [-2, 0, 1]):
+        p = [x.copy() for x in par]
+        p[2] = np.array(bad)
+        only(2, attend(w12, sv, q, off, slot=i32(sv.slot), parent=i32(np.concatenate(p))), bad)
+    for bad_slot in (-1, sv.slots, 1 << 30):
+        sl = sv.slot.copy()
+        sl[1] = bad_slot
+        only(1, attend(w12, sv, q, off, slot=i32(sl)), bad_slot)
+    for bad_len in (-1, 24 * 32 + 1, 1 << 30):
+        keep = sv.cache.length.clone()
+        sv.cache.length[int(sv.slot[3])] = bad_len
+        only(3, attend(w12, sv, q, off, slot=i32(sv.slot)), bad_len)
+        sv.cache.length.copy_(keep)
+    for bad_page in (-1, sv.cache.pages.shape[1], -(1 << 31), (1 << 31) - 1):
+        keep = sv.cache.page_table.clone()
+        sv.cache.page_table[int(sv.slot[0]), 0] = bad_page
+        only(0, attend(w12, sv, q, off, slot=i32(sv.slot)), bad_page)
+        sv.cache.page_table.copy_(keep)
+    # offsets: sequences whose rows are no range have no rows; the others' stand
+    got = attend(w12, sv, q, [0, 3, 99, 9, 12], slot=i32(sv.slot))
+    assert np.array_equal(got[:3], good[:3]) and (got[3:9] == 7).all() and np.array_equal(got[9:], good[9:])
+    # more rows than the recent rows hold: 40 % 32 + 96 > 96
+    big, _ = bf16(np.ones((96, 4, 64)))
+    assert np.isnan(attend(w12, sv, big, [0, 96], slot=i32(sv.slot[:1]))[:96]).all()
+
+
+def test_append_and_commit_refuse_on_the_device(w12):
+    import torch
+    say("append, commit refused")
+    sv = Serving(w12, 3, 1, 1, 64, 32, seed=13, positions=64)
+    sv.step([30, 30, 30])
+    before = [t.clone() for t in (sv.cache.pages.view(torch.uint8), sv.cache.scales, sv.cache.recent)]
+    off = i32([0, 4, 8, 12])
+    x = torch.ones(12, 3 * 64, device=DEV)
+
+    def untouched():
+        return all(torch.equal(a.view(torch.uint8) if a.dtype != torch.uint8 else a, b.contiguous().view(torch.uint8))
+                   for a, b in zip(before, (sv.cache.pages.view(torch.uint8), sv.cache.scales, sv.cache.recent)))
+    # a slot named twice, one outside, a broken tree: only that sequence is refused
+    sl = np.array([sv.slot[0], sv.slot[0], sv.slots], np.int32)
+    q = w12.w12_kv_append(sv.cache, 0, x, off, sv.rope_t, 1, slot=i32(sl), parent=i32([-1, 0, 1, 2] * 3))
+    assert torch.isfinite(q[:4]).all() and torch.isnan(q[4:]).all()
+    sv.cache.recent.copy_(before[2])
+    q = w12.w12_kv_append(sv.cache, 0, x, off, sv.rope_t, 1, slot=i32(sv.slot), parent=i32([0, 0, 1, 2] + [-1, 0, 1, 4] + [-1, 0, 0, 3 - 4]))
+    assert torch.isnan(q).all() and untouched()
+    # positions past the table: the rows beyond it
+    sv.cache.length[int(sv.slot[0])] = 62
+    q = w12.w12_kv_append(sv.cache, 0, x[:4], i32([0, 4]), sv.rope_t, 1, slot=i32(sv.slot[:1]))
+    assert torch.isfinite(q[:2]).all() and torch.isnan(q[2:]).all()
+    sv.cache.length[int(sv.slot[0])] = 30
+    sv.cache.recent.copy_(before[2])
+    # commits
+    for acc, path in (([4, 0, 0], None), ([-2, 0, 0], None), ([2, 0, 0], [0, 2, 1, -1]), ([1, 0, 0], [1, 2, -1, -1]),
+                      ([2, 0, 0], [0, 1, 4, -1]), ([1, 0, 0], [0, 0, -1, -1])):
+        p = None if path is None else i32(path + [0, -1, -1, -1] * 2)
+        got = w12.w12_kv_commit(sv.cache, off, i32(acc), path=p, slot=i32(sv.slot), length_out=sv.cache.length.clone())
+        assert got[sv.slot].tolist() == [-1, 31, 31], (acc, path)
+        assert untouched()
+    # no room in the page table, a page that is none
+    keep = sv.cache.page_table.clone()
+    for bad in (-1, sv.cache.pages.shape[1]):
+        sv.cache.page_table[int(sv.slot[1]), 0] = bad
+        got = w12.w12_kv_commit(sv.cache, off, i32([0, 3, 0]), slot=i32(sv.slot), length_out=sv.cache.length.clone())
+        assert got[sv.slot].tolist() == [31, -1, 31] and untouched()
+    sv.cache.page_table.copy_(keep)
+    # a refused tree (accept_len -1) keeps nothing and is no error; a slot named twice is committed once
+    got = w12.w12_kv_commit(sv.cache, off, i32([-1, 0, 0]), slot=i32(sv.slot), length_out=sv.cache.length.clone())
+    assert got[sv.slot].tolist() == [30, 31, 31]
+    got = w12.w12_kv_commit(sv.cache, off, i32([0, 1, 0]), slot=i32([sv.slot[0], sv.slot[0], sv.slot[2]]),
+                            length_out=sv.cache.length.clone())
+    assert got[sv.slot].tolist() == [31, 30, 31]
+
+
+def test_repeats_are_bitwise_and_shapes_share_a_workspace(w12):
+    import torch
+    say("determinism")
+    first = {}
+    for rep in range(3):
+        for seqs, kv, group, dim, rows in ((1, 2, 6, 128, 3), (3, 1, 4, 64, 20), (2, 4, 6, 256, 9)):
+            sv = Serving(w12, seqs, kv, group, dim, 32, seed=14, step_rows=512, blocks=60)
+            for _ in range(2):
+                sv.step([400] * seqs if seqs == 1 else [150] * seqs, check=False)
+            q, _ = bf16(sv.rng.randn(rows * seqs, kv * group, dim))
+            off = np.arange(seqs + 1) * rows
+            for _ in range(3):
+                got = attend(w12, sv, q, off, slot=i32(sv.slot))
+                key = (seqs, dim)
+                assert np.array_equal(first.setdefault(key, got), got)
+
+
+def test_graph_replays_and_other_streams(w12):
+    """One step captured with its append, attention and commit; replayed with
+    eager calls of the same shapes in between, and calls on another stream."""
+    import torch
+    say("graphs")
+    sv = Serving(w12, 2, 2, 6, 128, 64, seed=15, step_rows=64, blocks=40)
+    sv.step([50, 64])
+    sv.step([64, 64])
+    rows, heads = 16, 12
+    off = i32([0, 8, 16])
+    x = torch.randn(rows, (heads + 4) * 128, device=DEV)
+    slot = i32(sv.slot)
+    length = sv.cache.length.clone()
+
+    def step():
+        q = w12.w12_kv_append(sv.cache, 0, x, off, sv.rope_t, heads, slot=slot)
+        out = w12.w12_kv_attention(sv.cache, 0, q, off, slot=slot)
+        w12.w12_kv_commit(sv.cache, off, i7, slot=slot, length_out=length)
+        return out
+    i7 = i32([3, 7])
+    want = []
+    inputs = [torch.randn_like(x) for _ in range(4)]
+    for y in inputs:
+        x.copy_(y)
+        want.append((step().clone(), length.clone()))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graphs = []
+    with torch.cuda.stream(side):
+        for _ in range(2):
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g, stream=side):
+                out = step()
+            graphs.append((g, out))
+    torch.cuda.synchronize()
+    for i, y in enumerate(inputs):
+        for g, out in graphs:
+            x.copy_(y)
+            out.zero_()
+            length.zero_()
+            g.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(out, want[i][0]) and torch.equal(length, want[i][1]), i
+            assert torch.equal(step(), want[i][0])  # eager, between replays
+    other = torch.cuda.Stream()
+    x.copy_(inputs[2])
+    torch.cuda.synchronize()
+    with torch.cuda.stream(other):
+        got = step()
+    other.synchronize()
+    assert torch.equal(got, want[2][0])
+
+
+def test_binding_refusals(w12):
+    import torch
+    say("binding")
+    c = w12.kv_cache(1, 2, 64, 4, 2, 2, 32, 16, False, DEV)
+    q = torch.zeros(4, 4, 64, dtype=torch.bfloat16, device=DEV)
+    off = i32([0, 4])
+    with pytest.raises(TypeError):
+        w12.w12_kv_attention(c, 0, q.float(), off)
+    with pytest.raises(ValueError):
+        w12.w12_kv_attention(c, 0, q[..., :32].contiguous(), off)
+    with pytest.raises(ValueError):
+        w12.w12_kv_attention(c, 0, q, off, parent=i32([-1, 0, 1]))
+    with pytest.raises(ValueError):
+        w12.w12_kv_attention(c, 0, q, off, slot=i32([0, 1]))
+    with pytest.raises(w12.W12Error):
+        w12.w12_kv_attention(c, 1, q, off)  # no such layer
+    with pytest.raises(w12.W12Error):
+        w12.w12_kv_attention(c, 0, q[:, :3].contiguous(), off)  # 3 query heads on 2 kv heads
+    with pytest.raises(w12.W12Error):
+        w12.w12_kv_attention(c, 0, q, off, ws=torch.zeros(256, dtype=torch.uint8, device=DEV))
+    with pytest.raises(ValueError):
+        w12.w12_kv_attention(c, 0, q, off, out=torch.zeros(3, 256, dtype=torch.bfloat16, device=DEV))
+    with pytest.raises(ValueError):
+        w12.w12_kv_append(c, 0, torch.zeros(4, 64, device=DEV), off, torch.zeros(8, 64, device=DEV), 4)
+    with pytest.raises(ValueError):
+        w12.w12_kv_commit(c, off, i32([0, 0]))
+    with pytest.raises(ValueError):
+        w12.KvCache(c.pages, c.scales[:, :3].contiguous(), c.recent, c.page_table, c.length, 64)
+    with pytest.raises(TypeError):
+        w12.KvCache(c.pages.view(torch.uint8), c.scales, c.recent, c.page_table, c.length, 64)

@@ -1,0 +1,183 @@
+"""GPU parity of tree_accept_sampled (through the C ABI) against the 64-bit
+oracle: accepted lengths, paths and bonus tokens are equal."""
+import numpy as np
+import pytest
+
+from oracle import tree_sampled as TS
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+
+
+def say(*a):
+    print("[sampled]", *a, flush=True)
+
+
+@pytest.fixture(scope="module")
+def w12():
+    import torch
+    import w12_weight_streaming_amd as w
+    assert torch.cuda.is_available()
+    w.lib()
+    return w
+
+
+def forest(seed, sizes, vocab, drafted, chain=False, f32=True, spread=3.0, clash=0.2):
+    """Trees whose drafts are drawn from (or are the likely tokens of) a
+    noisy copy of the target's rows; some siblings share a token."""
+    import torch
+    r = np.random.RandomState(seed)
+    off = np.concatenate([[0], np.cumsum(sizes)]).astype(np.int32)
+    total = int(off[-1])
+    logits = torch.tensor(r.randn(total, vocab) * spread, dtype=torch.float32)
+    logits = logits if f32 else logits.bfloat16()
+    lg = logits.float().numpy()
+    guess = lg + r.randn(total, vocab).astype(np.float32)
+    draft = np.exp(guess - guess.max(1, keepdims=True))
+    draft = (draft / draft.sum(1, keepdims=True)).astype(np.float32)
+    parent, token = [], []
+    for s, n in enumerate(sizes):
+        seen = {}
+        for i in range(n):
+            p = -1 if i == 0 else (i - 1 if chain else int(r.randint(max(0, i - 5), i)))
+            parent.append(p)
+            row = draft[off[s] + max(p, 0)].astype(np.float64)
+            k = seen.get(p, 0)
+            seen[p] = k + (0 if r.rand() < clash else 1)
+            token.append(int(r.choice(vocab, p=row / row.sum())) if drafted else int(np.argsort(-row)[k % vocab]))
+    temp = r.uniform(0.5, 1.3, len(sizes)).astype(np.float32)
+    u, ub = r.rand(total).astype(np.float32), r.rand(len(sizes)).astype(np.float32)
+    return dict(off=off, parent=np.array(parent, np.int32), token=np.array(token, np.int32), logits=logits, lg=lg, temp=temp,
+                draft=draft if drafted else None, u=u, ub=ub)
+
+
+def call(w12, f, **kw):
+    import torch
+    t = lambda a: None if a is None else torch.tensor(np.asarray(a), device=DEV)
+    out = w12.tree_accept_sampled(t(f["off"]), t(f["parent"]), t(f["token"]), f["logits"].to(DEV), t(f["u"]), t(f["ub"]),
+                                  temperature=t(f["temp"]), draft=t(f["draft"]), **kw)
+    return [o.cpu().numpy() for o in out]
+
+
+def both(w12, f):
+    got = call(w12, f)
+    ref = TS.forest(f["off"], f["parent"], f["token"], f["lg"], f["temp"], f["draft"], f["u"], f["ub"])
+    for g, r, nm in zip(got, ref, ("accept_len", "path", "bonus")):
+        assert np.array_equal(g, r), (nm, g, r)
+    return got
+
+
+@pytest.mark.parametrize("drafted", [False, True])
+@pytest.mark.parametrize("chain", [False, True])
+@pytest.mark.parametrize("vocab", [1, 2, 37, 1000, 4096, 4097, 20001])
+def test_forests(w12, vocab, chain, drafted):
+    say("forest", vocab, chain, drafted)
+    lens = []
+    for seed in range(3):
+        f = forest(100 * vocab + seed, [1, 9, 8, 17, 3, 32], vocab, drafted, chain, f32=seed != 1)
+        lens += both(w12, f)[0].tolist()
+    if vocab <= 1000:  # at more tokens these flat rows accept few drafts, by the oracle too
+        assert max(lens) >= 1
+
+
+@pytest.mark.parametrize("drafted", [False, True])
+def test_full_vocabulary(w12, drafted):
+    say("152064", drafted)
+    both(w12, forest(7, [9, 32], 152064, drafted, f32=True, spread=4.0))
+    both(w12, forest(8, [8] * 3, 152064, drafted, chain=True, f32=False, spread=4.0))
+
+
+def test_wide_and_large_trees(w12):
+    say("wide")
+    f = forest(9, [40], 300, True, spread=0.5)
+    f["parent"][1:] = 0  # one row of 39 children
+    both(w12, f)
+    f["draft"] = None
+    both(w12, f)
+    both(w12, forest(10, [1024, 700], 64, False, spread=1.0))
+
+
+def test_random_numbers_at_their_ends(w12):
+    say("ends")
+    for u, ub in ((0.0, 0.0), (1.0, 1.0), (np.float32(1) - np.float32(2.0 ** -24), np.float32(1) - np.float32(2.0 ** -24))):
+        for drafted in (False, True):
+            f = forest(11, [9, 8, 12], 501, drafted)
+            f["u"][:], f["ub"][:] = u, ub
+            both(w12, f)
+
+
+def test_masked_vocabularies_and_refused_rows(w12):
+    import torch
+    say("masks")
+    f = forest(12, [8, 8, 8, 8, 8, 8], 5000, False)
+    lg = f["lg"].copy()
+    lg[:, 100:4900] = -np.inf               # a constrained vocabulary
+    f["token"] = (f["token"] % 100).astype(np.int32)
+    lg[8] = -np.inf                          # tree 1's root: nothing to draw
+    lg[16, 4999] = np.nan                    # tree 2's root
+    lg[24, 0] = np.inf                       # tree 3's root
+    f["lg"], f["logits"] = lg, torch.tensor(lg)
+    f["u"][32:] = 1.0                        # trees 4, 5 stop at their roots: other rows do not matter
+    lg[33:40] = np.nan
+    f["logits"] = torch.tensor(lg)
+    got = both(w12, f)
+    assert got[0][1:4].tolist() == [-1, -1, -1] and got[2][4] >= 0
+
+
+def test_refused_trees(w12):
+    say("refused")
+    f = forest(13, [6] * 8, 100, False)
+    f["parent"][6] = 0
+    f["parent"][12 + 3] = 3
+    f["parent"][18 + 2] = -1
+    f["token"][24 + 1] = 100
+    f["token"][30 + 5] = -1
+    f["temp"][6] = 0.0
+    f["temp"][7] = np.nan
+    got = both(w12, f)
+    assert got[0][1:].tolist() == [-1] * 7 and got[0][0] >= 0
+    assert (got[1][6:] == -1).all()
+    f = forest(14, [6] * 4, 100, False)
+    f["off"][1:4] = [30, 12, 12]  # a range past the end, one that runs backwards, an empty one
+    got = call(w12, f)
+    assert got[0][:3].tolist() == [-1, -1, -1] and got[2][:3].tolist() == [-1, -1, -1]
+
+
+def test_without_temperature_on_a_stream_and_replayed(w12):
+    import torch
+    say("streams")
+    f = forest(15, [9, 9], 30000, True)
+    f["temp"] = None
+    want = both(w12, f)
+    t = lambda a: torch.tensor(np.asarray(a), device=DEV)
+    args = [t(f["off"]), t(f["parent"]), t(f["token"]), f["logits"].to(DEV), t(f["u"]), t(f["ub"])]
+    draft = t(f["draft"])
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        got = w12.tree_accept_sampled(*args, draft=draft)
+    s.synchronize()
+    assert all(np.array_equal(a.cpu().numpy(), b) for a, b in zip(got, want))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = w12.tree_accept_sampled(*args, draft=draft)
+    for _ in range(3):
+        for o in out:
+            o.fill_(77)
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(np.array_equal(a.cpu().numpy(), b) for a, b in zip(out, want))
+        w12.tree_accept_sampled(*args, draft=draft)
+
+
+def test_chosen_drafts_agree_with_tree_accept_at_low_temperature(w12):
+    """As the temperature falls the walk becomes greedy acceptance."""
+    import torch
+    say("greedy limit")
+    f = forest(16, [12, 8, 9], 4000, False, clash=0.0)
+    f["temp"][:] = 1e-3
+    acc, path, bonus = call(w12, f)
+    t = lambda a: torch.tensor(np.asarray(a, np.int32), device=DEV)
+    am = f["lg"].argmax(1)
+    ref = [x.cpu().numpy() for x in w12.tree_accept(t(f["off"]), t(f["parent"]), t(f["token"]), t(am))]
+    assert np.array_equal(acc, ref[0]) and np.array_equal(path, ref[1]) and np.array_equal(bonus, ref[2])

@@ -21,6 +21,7 @@ LIB_PATH = os.path.join(_HERE, "libw12.so")
 
 W12_OK, W12_EINVAL, W12_ENOSPC, W12_EHIP, W12_ECORRUPT = 0, -1, -2, -3, -4
 W12_Y_F32, W12_Y_BF16 = 0, 1
+W12_KV_E4M3, W12_KV_INT8 = 0, 1
 MFMA_MIN_ROWS = 5  # rows from which w12_gemm multiplies on the matrix cores (fewer: VALU path)
 MAX_ROWS = 512
 
@@ -44,6 +45,12 @@ class W12Cert8(ctypes.Structure):
                 ("q", ctypes.c_void_p), ("qexp", ctypes.c_void_p), ("cbound", ctypes.c_void_p)]
 
 
+class W12KvCache(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("kvtype", "layers", "num_pages", "kv_heads", "page_tokens", "head_dim",
+                                              "slots", "recent_rows", "max_pages")] + \
+               [(n, ctypes.c_void_p) for n in ("pages", "scales", "recent", "page_table", "len")]
+
+
 def lib() -> ctypes.CDLL:
     """The loaded libw12.so; raises if it has not been built."""
     global _lib
@@ -55,6 +62,7 @@ def lib() -> ctypes.CDLL:
         L = ctypes.CDLL(LIB_PATH)
         vp, i64, i32, sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t
         mp = ctypes.POINTER(W12Matrix)
+        kp = ctypes.POINTER(W12KvCache)
         sig = {
             "w12_strerror": (ctypes.c_char_p, [ctypes.c_int]),
             "w12_abi_version": (ctypes.c_int, []),
@@ -78,6 +86,15 @@ def lib() -> ctypes.CDLL:
             "w12_tree_build_workspace": (ctypes.c_int, [i32, i32, ctypes.POINTER(sz)]),
             "w12_tree_build": (ctypes.c_int, [i32, i32, i32, vp, vp, vp, vp, i32, vp, sz, vp, vp, vp, vp,
                                               vp, vp]),
+            "w12_kv_append": (ctypes.c_int, [kp, i32, i32, vp, vp, i32, vp, vp, ctypes.c_int, i32, vp, i32, i32, i32,
+                                             vp, vp]),
+            "w12_kv_attention_workspace": (ctypes.c_int, [kp, i32, i32, i32, ctypes.POINTER(sz)]),
+            "w12_kv_attention": (ctypes.c_int, [kp, i32, i32, vp, vp, i32, vp, vp, i32, ctypes.c_float, vp, vp, sz,
+                                                vp]),
+            "w12_kv_commit": (ctypes.c_int, [kp, i32, vp, vp, i32, vp, vp, vp, vp]),
+            "tree_accept_sampled_workspace": (ctypes.c_int, [i32, i32, i32, ctypes.POINTER(sz)]),
+            "tree_accept_sampled": (ctypes.c_int, [i32, vp, i32, vp, vp, vp, ctypes.c_int, i32, vp, vp, vp, vp, vp, vp,
+                                                   vp, vp, sz, vp]),
         }
         for name, (res, args) in sig.items():
             f = getattr(L, name)
@@ -93,7 +110,9 @@ def exported_symbols():
             "w12_head_argmax_workspace", "w12_head_argmax", "w12_gemm_qpass",
             "w12_head_argmax_qpass", "tree_accept", "w12_tree_build_workspace", "w12_tree_build",
             "w12_gemm_noalloc", "w12_cert8_pack", "w12_head_argmax_certified_workspace",
-            "w12_head_argmax_certified"]
+            "w12_head_argmax_certified", "w12_kv_append", "w12_kv_attention_workspace",
+            "w12_kv_attention", "w12_kv_commit", "tree_accept_sampled_workspace",
+            "tree_accept_sampled"]
 
 
 def _ok(status: int, what: str):
@@ -396,3 +415,233 @@ def w12_tree_build(lp: torch.Tensor, tok: torch.Tensor, depth: torch.Tensor, roo
                              _ptr(score), _stream(dev)), "w12_tree_build")
     n = int(node_off[-1].item())
     return node_off, parent[:n], token[:n], ndepth[:n], score[:n]
+
+
+# ------------------------------------------------------------------ KV cache of the verify pass
+
+@dataclass
+class KvCache:
+    """Device-resident KV cache: the arrays of include/w12.h. pages is
+    [layers, num_pages, kv_heads, 2, page_tokens * head_dim] float8_e4m3fn or
+    int8, scales its fp32 [layers, num_pages, kv_heads, 2], recent
+    [layers, slots, kv_heads, 2, recent_rows * head_dim] bfloat16, page_table
+    [slots, max_pages] int32, length [slots] int32."""
+    pages: torch.Tensor
+    scales: torch.Tensor
+    recent: torch.Tensor
+    page_table: torch.Tensor
+    length: torch.Tensor
+    head_dim: int
+
+    def __post_init__(self):
+        if not isinstance(self.pages, torch.Tensor) or self.pages.dtype not in (torch.float8_e4m3fn, torch.int8):
+            raise TypeError("pages must be a float8_e4m3fn or int8 tensor")
+        for t, dt, nm, nd in ((self.pages, self.pages.dtype, "pages", 5), (self.scales, torch.float32, "scales", 4),
+                              (self.recent, torch.bfloat16, "recent", 5), (self.page_table, torch.int32, "page_table", 2),
+                              (self.length, torch.int32, "length", 1)):
+            _need(t, dt, nm, nd)
+            if t.device != self.pages.device:
+                raise ValueError("the cache's arrays must be on one GPU")
+        layers, num_pages, kv, two, page = self.pages.shape
+        slots = self.length.numel()
+        if (two != 2 or page % self.head_dim or tuple(self.scales.shape) != (layers, num_pages, kv, 2)
+                or self.recent.shape[:4] != (layers, slots, kv, 2) or self.recent.shape[4] % self.head_dim
+                or self.page_table.shape[0] != slots):
+            raise ValueError("the cache's arrays differ in shape")
+        self._desc = W12KvCache(W12_KV_E4M3 if self.pages.dtype == torch.float8_e4m3fn else W12_KV_INT8, layers,
+                                num_pages, kv, page // self.head_dim, self.head_dim, slots,
+                                self.recent.shape[4] // self.head_dim, self.page_table.shape[1],
+                                self.pages.data_ptr(), self.scales.data_ptr(), self.recent.data_ptr(),
+                                self.page_table.data_ptr(), self.length.data_ptr())
+
+    def desc(self) -> W12KvCache:
+        return self._desc
+
+    @property
+    def device(self):
+        return self.pages.device
+
+    @property
+    def kv_heads(self) -> int:
+        return self.pages.shape[2]
+
+    def nbytes(self) -> int:
+        return sum(t.numel() * t.element_size()
+                   for t in (self.pages, self.scales, self.recent, self.page_table, self.length))
+
+
+def kv_cache(layers: int, kv_heads: int, head_dim: int, num_pages: int, slots: int, max_pages: int,
+             page_tokens: int = 64, step_rows: int = MAX_ROWS, int8: bool = False, device="cuda") -> KvCache:
+    """An empty KV cache for steps of up to step_rows rows per sequence."""
+    rows = -(-(page_tokens - 1 + step_rows) // 32) * 32
+    dt = torch.int8 if int8 else torch.float8_e4m3fn
+    return KvCache(
+        torch.zeros(layers, num_pages, kv_heads, 2, page_tokens * head_dim, dtype=torch.uint8, device=device).view(dt),
+        torch.ones(layers, num_pages, kv_heads, 2, dtype=torch.float32, device=device),
+        torch.zeros(layers, slots, kv_heads, 2, rows * head_dim, dtype=torch.bfloat16, device=device),
+        torch.zeros(slots, max_pages, dtype=torch.int32, device=device),
+        torch.zeros(slots, dtype=torch.int32, device=device), head_dim)
+
+
+def _on(dev: torch.device):
+    """The device of a call made current while its kernels are launched."""
+    return torch.cuda.device(dev)
+
+
+def _step(cache: KvCache, row_off, slot, rows: int, **more):
+    """Checks the step's arrays; returns the number of sequences."""
+    _need(row_off, torch.int32, "row_off", 1)
+    seqs = row_off.numel() - 1
+    for nm, t, n in (("slot", slot, seqs), *((nm, t, rows) for nm, t in more.items())):
+        if t is not None:
+            _need(t, torch.int32, nm, 1)
+            if t.numel() != n:
+                raise ValueError(f"{nm} must have {n} entries (got {t.numel()})")
+    for t in (row_off, slot, *more.values()):
+        if t is not None and t.device != cache.device:
+            raise ValueError("the step's arrays must be on the cache's GPU")
+    return seqs
+
+
+def w12_kv_append(cache: KvCache, layer: int, qkv: torch.Tensor, row_off: torch.Tensor, rope: torch.Tensor,
+                  q_heads: int, slot: torch.Tensor | None = None, parent: torch.Tensor | None = None,
+                  interleaved: bool = False, out: torch.Tensor | None = None) -> torch.Tensor:
+    """Rotates q and k of qkv [rows, (q_heads + 2 kv_heads) * head_dim] (fp32
+    or bf16) and appends k, v as the step's rows. rope [positions, rot_dim]
+    fp32 holds cosines, then sines. Returns q [rows, q_heads, head_dim] bf16."""
+    if not isinstance(qkv, torch.Tensor) or qkv.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("qkv must be a float32 or bfloat16 tensor")
+    _need(qkv, qkv.dtype, "qkv", 2)
+    _need(rope, torch.float32, "rope", 2)
+    rows = qkv.shape[0]
+    if qkv.shape[1] != (q_heads + 2 * cache.kv_heads) * cache.head_dim:
+        raise ValueError(f"qkv has {qkv.shape[1]} columns, {q_heads} + 2 * {cache.kv_heads} heads of "
+                         f"{cache.head_dim} need {(q_heads + 2 * cache.kv_heads) * cache.head_dim}")
+    seqs = _step(cache, row_off, slot, rows, parent=parent)
+    if out is None:
+        out = torch.empty(rows, q_heads, cache.head_dim, dtype=torch.bfloat16, device=qkv.device)
+    _need(out, torch.bfloat16, "out")
+    if out.numel() < rows * q_heads * cache.head_dim:
+        raise ValueError("out must hold [rows, q_heads, head_dim]")
+    if any(t.device != cache.device for t in (qkv, rope, out)):
+        raise ValueError("qkv, rope and out must be on the cache's GPU")
+    d = cache.desc()
+    with _on(cache.device):
+        _ok(lib().w12_kv_append(ctypes.byref(d), layer, seqs, _ptr(slot), _ptr(row_off), rows, _ptr(parent), _ptr(qkv),
+                                W12_Y_F32 if qkv.dtype == torch.float32 else W12_Y_BF16, q_heads, _ptr(rope),
+                                rope.shape[0], rope.shape[1], int(interleaved), _ptr(out), _stream(cache.device)),
+            "w12_kv_append")
+    return out
+
+
+def _call_workspace(nbytes: int, device: torch.device, tag: str) -> torch.Tensor:
+    """workspace(), but a zero-filled one of its own for a call that is being
+    captured: the graph's replays and eager calls, or two graphs, may overlap
+    in time, and must not share arrival counters."""
+    if torch.cuda.is_current_stream_capturing():
+        return torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=device)
+    return workspace(nbytes, device, tag)
+
+
+def w12_kv_attention(cache: KvCache, layer: int, q: torch.Tensor, row_off: torch.Tensor,
+                     slot: torch.Tensor | None = None, parent: torch.Tensor | None = None, scale: float | None = None,
+                     out: torch.Tensor | None = None, ws: torch.Tensor | None = None) -> torch.Tensor:
+    """Attention of the step's rows q [rows, q_heads, head_dim] bf16 over the
+    cache; returns [rows, q_heads * head_dim] bf16. scale defaults to
+    head_dim ** -0.5."""
+    _need(q, torch.bfloat16, "q", 3)
+    rows, q_heads, dim = q.shape
+    if dim != cache.head_dim:
+        raise ValueError(f"q has head_dim {dim}, the cache {cache.head_dim}")
+    seqs = _step(cache, row_off, slot, rows, parent=parent)
+    if out is None:
+        out = torch.empty(rows, q_heads * dim, dtype=torch.bfloat16, device=q.device)
+    _need(out, torch.bfloat16, "out")
+    if out.numel() < rows * q_heads * dim:
+        raise ValueError("out must hold [rows, q_heads * head_dim]")
+    if q.device != cache.device or out.device != cache.device:
+        raise ValueError("q and out must be on the cache's GPU")
+    d = cache.desc()
+    need = ctypes.c_size_t(0)
+    with _on(cache.device):
+        _ok(lib().w12_kv_attention_workspace(ctypes.byref(d), seqs, rows, q_heads, ctypes.byref(need)),
+            "w12_kv_attention_workspace")
+        if ws is None:
+            ws = _call_workspace(need.value, cache.device, "kv")
+        _ok(lib().w12_kv_attention(ctypes.byref(d), layer, seqs, _ptr(slot), _ptr(row_off), rows, _ptr(parent), _ptr(q),
+                                   q_heads, dim ** -0.5 if scale is None else scale, _ptr(out), _ptr(ws), ws.numel(),
+                                   _stream(cache.device)), "w12_kv_attention")
+    return out
+
+
+def w12_kv_commit(cache: KvCache, row_off: torch.Tensor, accept_len: torch.Tensor, path: torch.Tensor | None = None,
+                  slot: torch.Tensor | None = None, length_out: torch.Tensor | None = None) -> torch.Tensor:
+    """Keeps the accepted rows of the step (tree_accept's accept_len and
+    path; path None: each sequence's first accept_len + 1 rows) in every
+    layer. Writes the new lengths into length_out [slots] (the cache's own by
+    default) and returns it."""
+    if path is not None:
+        _need(path, torch.int32, "path", 1)
+        rows = path.numel()
+    else:
+        rows = MAX_ROWS
+    seqs = _step(cache, row_off, slot, rows, path=path)
+    _need(accept_len, torch.int32, "accept_len", 1)
+    if accept_len.numel() != seqs:
+        raise ValueError(f"accept_len must have {seqs} entries (got {accept_len.numel()})")
+    if length_out is None:
+        length_out = cache.length
+    _need(length_out, torch.int32, "length_out", 1)
+    if length_out.numel() != cache.length.numel():
+        raise ValueError("length_out must have one entry per slot")
+    if accept_len.device != cache.device or length_out.device != cache.device:
+        raise ValueError("accept_len and length_out must be on the cache's GPU")
+    d = cache.desc()
+    with _on(cache.device):
+        _ok(lib().w12_kv_commit(ctypes.byref(d), seqs, _ptr(slot), _ptr(row_off), rows, _ptr(accept_len), _ptr(path),
+                                _ptr(length_out), _stream(cache.device)), "w12_kv_commit")
+    return length_out
+
+
+def tree_accept_sampled(node_off: torch.Tensor, parent: torch.Tensor, token: torch.Tensor, logits: torch.Tensor,
+                        u_accept: torch.Tensor, u_bonus: torch.Tensor, temperature: torch.Tensor | None = None,
+                        draft: torch.Tensor | None = None, ws: torch.Tensor | None = None):
+    """Tree acceptance of sampling requests: logits [nodes, vocab] fp32 or
+    bf16 (a row per node), random numbers u_accept [nodes] and u_bonus
+    [trees], temperature [trees] or None (1), draft [nodes, vocab] fp32 or
+    None (chosen drafts). Returns (accept_len, path, bonus) as tree_accept."""
+    if not isinstance(logits, torch.Tensor) or logits.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("logits must be a float32 or bfloat16 tensor")
+    _need(logits, logits.dtype, "logits", 2)
+    total, vocab = logits.shape
+    for t, nm in ((node_off, "node_off"), (parent, "parent"), (token, "token")):
+        _need(t, torch.int32, nm, 1)
+    T = node_off.numel() - 1
+    for t, nm, n in ((u_accept, "u_accept", total), (u_bonus, "u_bonus", T), (temperature, "temperature", T)):
+        if t is not None:
+            _need(t, torch.float32, nm, 1)
+            if t.numel() != n:
+                raise ValueError(f"{nm} must have {n} entries (got {t.numel()})")
+    if draft is not None:
+        _need(draft, torch.float32, "draft", 2)
+        if draft.shape != logits.shape:
+            raise ValueError("draft and logits differ in shape")
+    if T < 0 or parent.numel() != total or token.numel() != total:
+        raise ValueError("tree_accept_sampled: inconsistent array sizes")
+    dev = logits.device
+    if any(t is not None and t.device != dev for t in (node_off, parent, token, u_accept, u_bonus, temperature, draft)):
+        raise ValueError("tree_accept_sampled: tensors on different devices")
+    acc = torch.empty(max(T, 0), dtype=torch.int32, device=dev)
+    path = torch.empty(total, dtype=torch.int32, device=dev)
+    bonus = torch.empty(max(T, 0), dtype=torch.int32, device=dev)
+    need = ctypes.c_size_t(0)
+    with _on(dev):
+        _ok(lib().tree_accept_sampled_workspace(T, total, vocab, ctypes.byref(need)), "tree_accept_sampled_workspace")
+        if ws is None:
+            ws = torch.empty(need.value, dtype=torch.uint8, device=dev)
+        _ok(lib().tree_accept_sampled(T, _ptr(node_off), total, _ptr(parent), _ptr(token), _ptr(logits),
+                                      W12_Y_F32 if logits.dtype == torch.float32 else W12_Y_BF16, vocab,
+                                      _ptr(temperature), _ptr(draft), _ptr(u_accept), _ptr(u_bonus), _ptr(acc),
+                                      _ptr(path), _ptr(bonus), _ptr(ws), ws.numel(), _stream(dev)),
+            "tree_accept_sampled")
+    return acc, path, bonus

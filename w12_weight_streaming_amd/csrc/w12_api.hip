@@ -7,6 +7,7 @@
 #include <atomic>
 
 #include "../../include/w12.h"
+#include "kv_internal.h"
 #include "w12_internal.h"
 
 namespace {
@@ -156,6 +157,8 @@ w12_status head_entry(const w12_matrix* head, const uint16_t* x, int64_t m, int3
 }
 
 }  // namespace
+
+int w12::device_cu_count() { return num_cu(); }
 
 extern "C" {
 
