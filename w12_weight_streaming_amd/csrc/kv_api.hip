@@ -112,11 +112,10 @@ w12_status w12_kv_attention(const w12_kv_cache* cache, int32_t layer, int32_t nu
   a.scale = scale;
   a.out = out;
   char* base = static_cast<char*>(ws);
-  a.cnt = reinterpret_cast<uint32_t*>(base);
+  a.items = base;
   a.part = reinterpret_cast<float*>(base + p.off_part);
   a.part_ml = reinterpret_cast<float*>(base + p.off_ml);
   a.G = p.G;
-  a.max_items = p.max_items;
   return st(w12::launch_kv_attention(a, stream));
 }
 

@@ -13,21 +13,27 @@
 // bf16 is exact (at most 8 significant bits). The block's scales multiply the
 // scores and the probabilities in fp32.
 //
-// Work split: an item is (sequence, kv head, tile of 32 query rows); its
-// units are groups of 32 tokens, pages first, then the recent rows. The units
-// of all items in order are cut into equal runs, one for each workgroup, so
-// ragged batches balance; within a run the four waves take units in turn. An
-// item that several workgroups share is joined by the last of them to arrive,
-// in workgroup order: results are bitwise reproducible.
+// Work split: a sequence's query rows (row x head of the group) are cut into
+// tiles of 32, a block is the tiles of WR = 1, 2, 4 or 8 waves, and the
+// workgroup's eight waves walk 8 / WR groups of 32 tokens at a time (a step). An item is (sequence, kv head,
+// block), its steps run over the pages, then the recent rows. The steps of all
+// items in order are cut into equal runs, one for each workgroup, so ragged
+// batches balance. Items that several workgroups share leave partial sums,
+// which a second launch joins in workgroup order: results are bitwise
+// reproducible.
 #include "kv_internal.h"
 #include "w12_device.h"
 
 namespace w12 {
 namespace {
 
-constexpr int kThreads = 256, kWaves = 4;
-constexpr int kTile = 32;        // query rows of an item
-constexpr int kUnitsPerWg = 4;   // fewest units worth a workgroup of their own
+constexpr int kThreads = 512, kWaves = 8;  // one workgroup a CU, two waves a SIMD
+constexpr int kTile = 32;        // query rows of a tile
+constexpr int kPartFloats = 16384;  // floats of one partial sum: a block's rows x dims, at most
+// steps that an item's beginning and end are worth (queries, the first pages'
+// chain of loads, recent rows, the join of the waves): they count as its last
+// steps, in which nothing is done
+constexpr int kItemSteps = 6;
 constexpr float kLog2e = 1.44269504088896340736f;
 // a new maximum is taken when a score passes the running one by this much
 // (in powers of two): until then probabilities may reach 2^8, which neither
@@ -36,21 +42,12 @@ constexpr float kSlack = 8.0f;
 constexpr float kFloor = -3.402823466e38f;  // running maximum before the first score
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-typedef __amdgpu_buffer_rsrc_t rsrc_t;
-constexpr int kRawBufferWord3 = 0x00020000;
-constexpr int kDeviceScope = 16;  // sc1: coherent across XCDs
 
-__device__ __forceinline__ rsrc_t make_rsrc(const void* base, uint32_t bytes) {
-  const uint64_t b = reinterpret_cast<uint64_t>(base);
-  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)b);
-  const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(b >> 32));
-  void* ub = reinterpret_cast<void*>(((uint64_t)hi << 32) | lo);
-  return __builtin_amdgcn_make_buffer_rsrc(ub, (short)0, (int)__builtin_amdgcn_readfirstlane(bytes), kRawBufferWord3);
-}
-
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
-  const __bf16 x = (__bf16)a, y = (__bf16)b;
-  return (uint32_t)__builtin_bit_cast(uint16_t, x) | ((uint32_t)__builtin_bit_cast(uint16_t, y) << 16);
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {  // one v_cvt_pk_bf16_f32
+  bf16x2 v;
+  v[0] = (__bf16)a;
+  v[1] = (__bf16)b;
+  return __builtin_bit_cast(uint32_t, v);
 }
 __device__ __forceinline__ bf16x8 as_operand(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   return __builtin_bit_cast(bf16x8, u32x4{a, b, c, d});
@@ -59,6 +56,9 @@ __device__ __forceinline__ bf16x8 as_operand(uint32_t a, uint32_t b, uint32_t c,
 // Four 8-bit codes as bf16 pairs, exactly.
 template <int KIND>
 __device__ __forceinline__ void codes4(uint32_t x, uint32_t& lo, uint32_t& hi) {
+  // opaque: else the compiler carries loaded codes from one step to the next
+  // byte by byte, in a register each
+  asm("" : "+v"(x));
   if constexpr (KIND == 0) {
     lo = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x, 1.0f, false));
     hi = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x, 1.0f, true));
@@ -78,467 +78,660 @@ __device__ __forceinline__ void codes16(const u32x4 x, bf16x8& a, bf16x8& b) {
   b = as_operand(w[4], w[5], w[6], w[7]);
 }
 
+// All ones where bit b of x is set (masks as values: as conditions they would
+// take a pair of scalar registers each).
+__device__ __forceinline__ uint32_t bit_mask(uint32_t x, int b) { return (uint32_t)((int32_t)(x << (31 - b)) >> 31); }
+
+// The larger of a lane's value and that of its other half.
+__device__ __forceinline__ float exchange_max(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+
+// U groups of 32 scores per row, x = sc * c in powers of two (only where
+// `see` has the token's bit, if MASK; a group that `valid` leaves out counts
+// for nothing). The probabilities come out times the value scale 2^lv, as the
+// product's operands; their sum without it (times rv = 2^-lv) joins l. The sum
+// is taken over the operands as rounded, two at a time.
+template <int NB, int U, bool MASK>
+__device__ __forceinline__ void softmax_step(f32x16 (&o)[NB], float& m, float& l, f32x16 (&sc)[U], const float (&c)[U],
+                                             const float (&lv)[U], const float (&rv)[U], const bool (&valid)[U],
+                                             uint32_t see, int half, bf16x8 (&pb)[U][2]) {
+  float mx = kFloor;
+  const uint32_t mine = see >> (half * 4);
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    float x = kFloor;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      if (MASK) {
+        const uint32_t keep = bit_mask(mine, (r >> 2) * 8 + (r & 3));
+        sc[u][r] = __uint_as_float((__float_as_uint(sc[u][r]) & keep) | (0xFF800000u & ~keep));
+      }
+      x = fmaxf(x, sc[u][r]);
+    }
+    if (valid[u]) mx = fmaxf(mx, x * c[u]);
+  }
+  mx = exchange_max(mx);
+  if (__any(mx > m + kSlack)) {
+    const float nm = fmaxf(m, mx);
+    const float al = __builtin_amdgcn_exp2f(m - nm);
+    m = nm;
+    l *= al;
+#pragma unroll
+    for (int i = 0; i < NB; ++i) o[i] *= al;
+  }
+  constexpr uint32_t kOnes = 0x3F803F80u;
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const float base = lv[u] - m;
+    uint32_t w[8];
+    float sum = 0.f;
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      w[r] = pack_bf16(__builtin_amdgcn_exp2f(__builtin_fmaf(sc[u][2 * r], c[u], base)),
+                       __builtin_amdgcn_exp2f(__builtin_fmaf(sc[u][2 * r + 1], c[u], base)));
+      sum = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, w[r]), __builtin_bit_cast(bf16x2, kOnes), sum, false);
+    }
+    l = __builtin_fmaf(sum, rv[u], l);
+    pb[u][0] = as_operand(w[0], w[1], w[2], w[3]);
+    pb[u][1] = as_operand(w[4], w[5], w[6], w[7]);
+  }
+}
+
+// Most tiles of a block: their queries take 32 KB of LDS.
 template <int DIM>
-struct Acc {
-  f32x16 o[DIM / 32];
-  float m, l;
+constexpr int kBlockTiles = 512 / DIM;
+
+// Waves along the rows for n tiles: as many as there are (the tokens are read
+// once for all of them) unless that leaves over a seventh of them idle.
+template <int MAX>
+__device__ __forceinline__ int waves_along_rows(int n) {
+  int wr = MAX;
+  while (wr > 1 && (n <= wr / 2 || ((n + wr - 1) / wr * wr - n) * 7 > n)) wr >>= 1;
+  return wr;
+}
+
+// What the join needs to know of the item that a workgroup begins and others
+// go on with.
+struct SplitItem {
+  int last;             // its last workgroup, -1: none
+  int rows;             // query rows
+  int row0, first_row;  // first row of the sequence; first query row of the item
+  int kvh, first_slot;  // partial slot of the first workgroup: 0 or 1
 };
 
-// One group of 32 scores per row: x = S * c (masked where `see` has no bit),
-// then the probabilities, and their operands scaled by `vs`.
+// A sequence as the scan found it.
+struct SeqInfo {
+  int len;     // -1: refused
+  int slot;
+  short row0, rows;
+};
+
 template <int DIM>
-__device__ __forceinline__ void softmax_step(Acc<DIM>& acc, const f32x16& sc, float c, float vs, uint32_t see, int half,
-                                             float (&p)[16], bf16x8 (&pb)[2]) {
-  float x[16], mx = kFloor;
-#pragma unroll
-  for (int r = 0; r < 16; ++r) {
-    x[r] = sc[r] * c;
-    if (!((see >> ((r >> 2) * 8 + half * 4 + (r & 3))) & 1)) x[r] = -__builtin_huge_valf();
-    mx = fmaxf(mx, x[r]);
-  }
-  mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
-  if (__any(mx > acc.m + kSlack)) {
-    const float nm = fmaxf(acc.m, mx);
-    const float al = __builtin_amdgcn_exp2f(acc.m - nm);
-    acc.m = nm;
-    acc.l *= al;
-#pragma unroll
-    for (int i = 0; i < DIM / 32; ++i) acc.o[i] *= al;
-  }
-  float sum = 0.f;
-#pragma unroll
-  for (int r = 0; r < 16; ++r) {
-    p[r] = __builtin_amdgcn_exp2f(x[r] - acc.m);
-    sum += p[r];
-  }
-  acc.l += sum;
-  uint32_t w[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) w[i] = pack_bf16(p[2 * i] * vs, p[2 * i + 1] * vs);
-  pb[0] = as_operand(w[0], w[1], w[2], w[3]);
-  pb[1] = as_operand(w[4], w[5], w[6], w[7]);
-}
-
-__device__ __forceinline__ int owner_of(int64_t u, int64_t total, int wgs) {
-  // the workgroup w with w * total / wgs <= u < (w + 1) * total / wgs
-  int w = (int)(((u + 1) * wgs - 1) / total);
-  return w;
-}
-
-template <int DIM, int KIND>
-__global__ __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) void kv_attention_kernel(AttentionArgs a) {
-  constexpr int NB = DIM / 32;
-  __shared__ int64_t s_first[kStepRows + 1];  // units before each sequence
-  __shared__ int64_t s_scan[kThreads];
-  __shared__ int s_parent[kStepRows];
-  __shared__ uint32_t s_anc[kTile][kStepRows / 32];
-  __shared__ float s_ml[kWaves][kTile][2];
-  __shared__ int s_bad, s_last;
-  __shared__ float s_o[2][kTile * DIM];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, col = lane & 31, half = lane >> 5;
-  const int group = a.q_heads / a.c.kv_heads;
-
-  // units of every sequence, then their running sum
-  auto tiles_of = [&](const SeqView& v) { return (v.rows * group + kTile - 1) / kTile; };
-  auto units_of = [&](const SeqView& v) {
-    return v.ok ? v.full * (a.c.page / kGroup) + (v.tail + v.rows + kGroup - 1) / kGroup : 1;
+struct Shared {
+  static constexpr int kRows = kBlockTiles<DIM> * kTile;
+  union {
+    uint4 q[kBlockTiles<DIM>][DIM / 32][2][64];  // query tiles as B operands
+    float o[kWaves / 2][4096];                   // sums of four waves while they join
   };
-  int64_t mine[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int s = tid * 2 + i;
-    mine[i] = 0;
-    if (s < a.st.num_seq) {
-      const SeqView v = seq_view(a.c, a.st, s);
-      mine[i] = (int64_t)tiles_of(v) * a.c.kv_heads * units_of(v);
-    }
-  }
-  s_scan[tid] = mine[0] + mine[1];
-  __syncthreads();
-  for (int o = 1; o < kThreads; o <<= 1) {
-    const int64_t x = tid >= o ? s_scan[tid - o] : 0;
-    __syncthreads();
-    s_scan[tid] += x;
-    __syncthreads();
-  }
+  uint32_t anc[kRows][kStepRows / 32];
+  int64_t first[kStepRows + 1];  // steps before each sequence
+  SeqInfo seq[kStepRows];
+  int parent[kStepRows];
+  float ml[kWaves][kTile][2];
+  int64_t scan[kWaves];
+  int bad, strange;
+};
+
+template <int DIM, int KIND, bool STREAM>
+__global__ __launch_bounds__(kThreads, 2) void kv_attention_kernel(AttentionArgs a) {
+  constexpr int NB = DIM / 32;
+  constexpr int kMaxWr = kBlockTiles<DIM>;
+  constexpr int U = DIM == 256 ? 1 : 2;       // groups of 32 tokens a wave takes at a time
+  constexpr bool kQueryRegs = DIM <= 128;     // its query operands stay in registers
+  __shared__ Shared<DIM> sh;
+  const int tid = threadIdx.x, lane = tid & 63, col = lane & 31, half = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int group = a.q_heads / a.c.kv_heads, per_page = a.c.page / kGroup;
+  SplitItem* split_item = static_cast<SplitItem*>(a.items) + blockIdx.x;
+
+  // steps of every sequence, then their running sum
+  struct Shape {
+    int wr, blocks, page_units, steps;
+  };
+  auto shape_of = [&](const SeqInfo& v) __attribute__((always_inline)) {
+    Shape h;
+    const int tiles = (v.rows * group + kTile - 1) / kTile;
+    h.wr = waves_along_rows<kMaxWr>(tiles);
+    h.blocks = (tiles + h.wr - 1) / h.wr;
+    const int full = v.len / a.c.page, tail = v.len - full * a.c.page;
+    h.page_units = v.len < 0 ? 0 : full * per_page;
+    const int units = v.len < 0 ? 1 : h.page_units + (tail + v.rows + kGroup - 1) / kGroup;
+    const int wt = kWaves / h.wr;
+    h.steps = (units + wt - 1) / wt + kItemSteps;
+    return h;
+  };
   {
-    const int64_t before = s_scan[tid] - mine[0] - mine[1];
-    s_first[tid * 2] = before;
-    s_first[tid * 2 + 1] = before + mine[0];
-    if (tid == kThreads - 1) s_first[kStepRows] = s_scan[tid];
+    static_assert(kThreads == kStepRows);
+    int64_t mine = 0;
+    if (tid < a.st.num_seq) {
+      const SeqView v = seq_view(a.c, a.st, tid);
+      SeqInfo n;
+      n.len = v.ok ? v.len : -1;
+      n.slot = v.slot;
+      n.row0 = (short)v.row0;
+      n.rows = (short)v.rows;
+      sh.seq[tid] = n;
+      const Shape h = shape_of(n);
+      mine = (int64_t)h.blocks * a.c.kv_heads * h.steps;
+    }
+    int64_t upto = mine;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const uint32_t lo = __shfl_up((uint32_t)upto, o, 64), hi = __shfl_up((uint32_t)((uint64_t)upto >> 32), o, 64);
+      if (lane >= o) upto += (int64_t)(((uint64_t)hi << 32) | lo);
+    }
+    if (lane == 63) sh.scan[wave] = upto;
+    __syncthreads();
+    for (int w = 0; w < wave; ++w) upto += sh.scan[w];
+    sh.first[tid] = upto - mine;
+    if (tid == kThreads - 1) sh.first[kStepRows] = upto;
   }
+  if (tid == 0) split_item->last = -1;
   __syncthreads();
-  const int64_t total = s_first[kStepRows];
-  if (total == 0) return;
-  const int wgs = (int)min((int64_t)a.G, (total + kUnitsPerWg - 1) / kUnitsPerWg);
+  const int64_t total = sh.first[kStepRows];
+  const int wgs = (int)min((int64_t)a.G, total);
   const int wg = blockIdx.x;
   if (wg >= wgs) return;
   const int64_t begin = total * wg / wgs, end = total * (wg + 1) / wgs;
 
-  int seq;  // the first sequence whose units reach past `begin`
+  int seq;  // the first sequence whose steps reach past `begin`
   {
     int lo = 0, hi = a.st.num_seq - 1;
     while (lo < hi) {
       const int mid = (lo + hi) >> 1;
-      if (s_first[mid + 1] > begin) hi = mid; else lo = mid + 1;
+      if (sh.first[mid + 1] > begin) hi = mid; else lo = mid + 1;
     }
     seq = lo;
   }
 
   for (int64_t at = begin; at < end;) {
-    while (s_first[seq + 1] <= at) ++seq;
-    const SeqView v = seq_view(a.c, a.st, seq);
-    const int tiles = tiles_of(v), units = units_of(v);
-    const int item = (int)((at - s_first[seq]) / units);
-    const int64_t item0 = s_first[seq] + (int64_t)item * units;  // the item's first unit
-    const int u0 = (int)(at - item0), u1 = (int)min((int64_t)units, end - item0);
-    const int kvh = item / tiles, tile = item % tiles;
-    const int first_row = tile * kTile, q_rows = v.rows * group;
-    const int my = first_row + col;  // the lane's query row: row my / group, head my % group
-    const bool on = my < q_rows && v.ok;
-    const int page_units = v.ok ? v.full * (a.c.page / kGroup) : 0;
-    bool poison = !v.ok;
+    while (sh.first[seq + 1] <= at) ++seq;
+    const SeqInfo v = sh.seq[seq];
+    const Shape h = shape_of(v);
+    const bool ok = v.len >= 0;
+    const int tail = ok ? v.len - h.page_units * kGroup : 0;
+    const int item = (int)((at - sh.first[seq]) / h.steps);
+    const int64_t item0 = sh.first[seq] + (int64_t)item * h.steps;  // the item's first step
+    const int st0 = (int)(at - item0), st1 = (int)min((int64_t)h.steps, end - item0);
+    const int second = at != begin;  // the run's second partial sum
+    at += st1 - st0;
+    if (st0 >= h.steps - kItemSteps) continue;
+    const int kvh = item / h.blocks, block = item % h.blocks;
+    const int wt = kWaves / h.wr, wr = wave & (h.wr - 1), ph = wave / h.wr;  // the wave's tiles, its share of the tokens
+    const int block_row = block * h.wr * kTile, q_rows = v.rows * group;
+    const int block_rows = min(h.wr * kTile, q_rows - block_row);
+    const int wave_row = block_row + wr * kTile;  // the wave's first query row
+    const bool idle = wave_row >= q_rows || !ok;
+    const int b_lo = block_row / group, b_hi = min((int)v.rows, (block_row + block_rows - 1) / group + 1);
+    const int my = wave_row + col;  // the lane's query row: row my / group, head my % group
+    const bool on = my < q_rows && ok;
 
-    // ancestors of the tile's rows
-    const int row_lo = first_row / group, row_hi = min(v.rows, (first_row + kTile - 1) / group + 1);
+    // pages: units st * wt + ph, ids and scales of 64 at a time
+    const int pst1 = idle ? st0 : min(st1, (h.page_units - ph + wt - 1) / wt);
+    const int np = max(0, pst1 - st0);
+    const uint8_t* page0 = a.c.pages + page_at(a.c, a.layer, 0, kvh, 0);
+    const size_t page_bytes = (size_t)a.c.kv_heads * 2 * a.c.page * DIM;
+    const int to_v = a.c.page * DIM;
+    const float c2 = a.scale * kLog2e;
+    int id, off, cnt;
+    float ks, lv, rv;
+    auto fetch = [&](int kb) __attribute__((always_inline)) {
+      cnt = min(64, np - kb);
+      // lanes past the last unit: a weight of zero (2^-inf)
+      id = off = 0;
+      ks = rv = 0.f;
+      lv = -__builtin_huge_valf();
+      if (lane < cnt) {
+        const int u = (st0 + kb + lane) * wt + ph, j = u / per_page;
+        id = a.c.table[(size_t)v.slot * a.c.max_pages + j];
+        off = (u - j * per_page) * (kGroup * DIM);
+        const bool good = id >= 0 && id < a.c.num_pages;
+        if (!good) id = 0;
+        const float2 sc = *reinterpret_cast<const float2*>(a.c.scales + scale_at(a.c, a.layer, id, kvh, 0));
+        ks = good ? sc.x * c2 : __builtin_nanf("");
+        lv = __builtin_amdgcn_logf(sc.y);
+        rv = __builtin_amdgcn_rcpf(sc.y);
+      }
+    };
+    // past the last unit the loads repeat it: they stay unconditional, so
+    // that every wait is for the oldest ones in flight alone
+    auto at_page = [&](int k) __attribute__((always_inline)) {
+      k = min(k, cnt - 1);
+      const uint32_t pid = __builtin_amdgcn_readlane(id, k), o = __builtin_amdgcn_readlane(off, k);
+      return page0 + (size_t)pid * page_bytes + o;
+    };
+    auto load_page = [&](const uint8_t* p, u32x4 (&x)[NB]) __attribute__((always_inline)) {
+#pragma unroll
+      for (int i = 0; i < NB; ++i) {
+        const u32x4* q = reinterpret_cast<const u32x4*>(p + i * 1024 + lane * 16);
+        x[i] = STREAM ? __builtin_nontemporal_load(q) : *q;
+      }
+    };
+    u32x4 kr[U][NB], vr[U][NB];
+    // the first keys are on their way before anything else of the item,
+    // where the registers hold them next to the recent rows' operands
+    auto load_keys = [&]() __attribute__((always_inline)) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) load_page(at_page(u), kr[u]);
+    };
+    auto load_values = [&]() __attribute__((always_inline)) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) load_page(at_page(u) + to_v, vr[u]);
+    };
+    if (np > 0) {
+      fetch(0);
+      if constexpr (DIM <= 128) load_keys();
+    }
+
+    // ancestors of the block's rows, a set of bits for each
     __syncthreads();
-    if (tid == 0) s_bad = 0;
+    if (tid == 0) sh.bad = sh.strange = 0;
     __syncthreads();
-    if (v.ok && u1 > page_units) {
+    if (ok && st1 * wt > h.page_units) {
       if (a.st.parent) {
         int bad = 0;
         for (int i = tid; i < v.rows; i += kThreads) {
           const int p = a.st.parent[v.row0 + i];
-          s_parent[i] = p;
+          sh.parent[i] = p;
           if (i == 0 ? p != -1 : (p < 0 || p >= i)) bad = 1;
         }
-        for (int i = tid; i < kTile * (kStepRows / 32); i += kThreads) (&s_anc[0][0])[i] = 0;
-        if (bad) s_bad = 1;
+        for (int i = tid; i < (b_hi - b_lo) * (kStepRows / 32); i += kThreads) (&sh.anc[0][0])[i] = 0;
+        if (bad) sh.bad = 1;
         __syncthreads();
-        if (!s_bad && row_lo + tid < row_hi) {
-          for (int i = row_lo + tid; i >= 0; i = s_parent[i]) s_anc[tid][i >> 5] |= 1u << (i & 31);
-        }
+        if (!sh.bad)
+          for (int r = b_lo + tid; r < b_hi; r += kThreads)
+            for (int i = r; i >= 0; i = sh.parent[i]) sh.anc[r - b_lo][i >> 5] |= 1u << (i & 31);
       } else {
-        for (int i = tid; i < (row_hi - row_lo) * (kStepRows / 32); i += kThreads) {
-          const int r = row_lo + i / (kStepRows / 32) - (i % (kStepRows / 32)) * 32;  // highest visible bit
-          s_anc[i / (kStepRows / 32)][i % (kStepRows / 32)] = r < 0 ? 0u : r >= 31 ? ~0u : (2u << r) - 1u;
+        for (int i = tid; i < (b_hi - b_lo) * (kStepRows / 32); i += kThreads) {
+          const int r = b_lo + i / (kStepRows / 32) - (i % (kStepRows / 32)) * 32;  // highest visible bit
+          (&sh.anc[0][0])[i] = r < 0 ? 0u : r >= 31 ? ~0u : (2u << r) - 1u;
         }
       }
+    }
+    // the tile's query rows as B operands: dims 32 i + 16 half + 0..15 of a lane's row
+    bf16x8 qr[kQueryRegs ? NB : 1][2];
+    if (kQueryRegs || ph == 0) {
+      const int r = on ? my / group : 0, hd = kvh * group + (on ? my % group : 0);
+      const u32x4* p = reinterpret_cast<const u32x4*>(a.q + ((size_t)(v.row0 + r) * a.q_heads + hd) * DIM + half * 16);
+#pragma unroll
+      for (int i = 0; i < NB; ++i)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          u32x4 x = {0, 0, 0, 0};
+          if (on) x = p[i * 4 + e];
+          if constexpr (kQueryRegs)
+            qr[i][e] = __builtin_bit_cast(bf16x8, x);
+          else
+            sh.q[wr][i][e][lane] = __builtin_bit_cast(uint4, x);
+        }
     }
     __syncthreads();
-    poison = poison || s_bad;
+    const bool poison = !ok || sh.bad;
 
-    // the lane's query row as B operands: dims 32 i + 16 half + 0..15
-    bf16x8 qf[NB][2];
-    {
-      const int r = on ? my / group : 0, h = kvh * group + (on ? my % group : 0);
-      const u32x4* p = reinterpret_cast<const u32x4*>(a.q + ((size_t)(v.row0 + r) * a.q_heads + h) * DIM + half * 16);
-#pragma unroll
-      for (int i = 0; i < NB; ++i) {
-        u32x4 x = {0, 0, 0, 0}, y = {0, 0, 0, 0};
-        if (on) {
-          x = p[i * 4];
-          y = p[i * 4 + 1];
-        }
-        qf[i][0] = __builtin_bit_cast(bf16x8, x);
-        qf[i][1] = __builtin_bit_cast(bf16x8, y);
-      }
-    }
-    Acc<DIM> acc;
+    f32x16 acc[NB];
+    float m = kFloor, l = 0.f;
 #pragma unroll
     for (int i = 0; i < NB; ++i)
 #pragma unroll
-      for (int r = 0; r < 16; ++r) acc.o[i][r] = 0.f;
-    acc.m = kFloor;
-    acc.l = 0.f;
-    const float c2 = a.scale * kLog2e;
+      for (int r = 0; r < 16; ++r) acc[i][r] = 0.f;
+    const uint4* qs = &sh.q[wr][0][0][lane];
+    auto query = [&](int i, int e) __attribute__((always_inline)) {
+      if constexpr (kQueryRegs)
+        return qr[i][e];
+      else
+        return __builtin_bit_cast(bf16x8, qs[(i * 2 + e) * 64]);
+    };
 
-    // pages: units u0 + wave + 4 k below `page_units`, ids and scales of 64 at a time
-    const int pu1 = min(u1, page_units);
-    const int np = u0 + wave < pu1 ? (pu1 - u0 - wave + kWaves - 1) / kWaves : 0;
-    const int per_page = a.c.page / kGroup;
-    for (int kb = 0; kb < np; kb += 64) {
-      int id = 0;
-      float ks = 0.f, vs = 0.f;
-      if (kb + lane < np) {
-        const int j = (u0 + wave + kWaves * (kb + lane)) / per_page;
-        id = a.c.table[(size_t)v.slot * a.c.max_pages + j];
-        const bool good = id >= 0 && id < a.c.num_pages;
-        if (!good) id = 0;
-        const float2 sc = *reinterpret_cast<const float2*>(a.c.scales + scale_at(a.c, a.layer, id, kvh, 0));
-        ks = good ? sc.x : __builtin_nanf("");
-        vs = sc.y;
-      }
-      const int cnt = min(64, np - kb);
-      u32x4 kr[NB], vr[NB];
-      auto load = [&](int k) {
-        const int u = u0 + wave + kWaves * (kb + k);
-        const int pid = __builtin_amdgcn_readlane(id, k);
-        const uint8_t* p = a.c.pages + page_at(a.c, a.layer, pid, kvh, 0) + (size_t)(u % per_page) * (kGroup * DIM) + lane * 16;
-        const size_t to_v = (size_t)a.c.page * DIM;
+    // recent rows: the committed tail, then the step's rows; the wave's tiles
+    // see nothing behind their own last row
+    if (!poison && !idle) {
+      const uint16_t* kb = a.c.recent + recent_at(a.c, a.layer, v.slot, kvh, 0) + lane * 16;
+      const uint16_t* vb = a.c.recent + recent_at(a.c, a.layer, v.slot, kvh, 1) + lane * 16;
+      const int rows = tail + v.rows, seen = tail + min((int)v.rows, (wave_row + kTile - 1) / group + 1);
+      const uint32_t* anc = sh.anc[on ? my / group - b_lo : 0];
+      constexpr int HB = NB < 4 ? NB : 4;  // blocks of 32 dims loaded at a time
+      auto load = [&](const uint16_t* p, u32x4 (&x)[HB][2]) __attribute__((always_inline)) {
 #pragma unroll
-        for (int i = 0; i < NB; ++i) kr[i] = *reinterpret_cast<const u32x4*>(p + i * 1024);
-#pragma unroll
-        for (int i = 0; i < NB; ++i) vr[i] = *reinterpret_cast<const u32x4*>(p + to_v + i * 1024);
+        for (int i = 0; i < HB; ++i) {
+          x[i][0] = *reinterpret_cast<const u32x4*>(p + i * 1024);
+          x[i][1] = *reinterpret_cast<const u32x4*>(p + i * 1024 + 8);
+        }
       };
-      load(0);
-      for (int k = 0; k < cnt; ++k) {
-        f32x16 sc;
-#pragma unroll
-        for (int r = 0; r < 16; ++r) sc[r] = 0.f;
-#pragma unroll
-        for (int i = 0; i < NB; ++i) {
-          bf16x8 x, y;
-          codes16<KIND>(kr[i], x, y);
-          sc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, qf[i][0], sc, 0, 0, 0);
-          sc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(y, qf[i][1], sc, 0, 0, 0);
-        }
-        const float ksk = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(ks), k));
-        const float vsk = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(vs), k));
-        u32x4 vn[NB];
-#pragma unroll
-        for (int i = 0; i < NB; ++i) vn[i] = vr[i];
-        if (k + 1 < cnt) load(k + 1);
-        float p[16];
-        bf16x8 pb[2];
-        softmax_step(acc, sc, c2 * ksk, vsk, ~0u, half, p, pb);
-#pragma unroll
-        for (int i = 0; i < NB; ++i) {
-          bf16x8 x, y;
-          codes16<KIND>(vn[i], x, y);
-          acc.o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, pb[0], acc.o[i], 0, 0, 0);
-          acc.o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(y, pb[1], acc.o[i], 0, 0, 0);
-        }
-      }
-    }
-
-    // recent rows: the committed tail, then the step's rows
-    if (!poison) {
-      const uint16_t* kb = a.c.recent + recent_at(a.c, a.layer, v.slot, kvh, 0);
-      const uint16_t* vb = a.c.recent + recent_at(a.c, a.layer, v.slot, kvh, 1);
-      const int rows = v.tail + v.rows;
-      int u = u0 + wave;
-      if (u < page_units) u += (page_units - u + kWaves - 1) / kWaves * kWaves;
-      for (; u < u1; u += kWaves) {
-        const int t0 = (u - page_units) * kGroup;
-        const int held = rows - t0 >= 32 ? 32 : rows - t0;  // rows of this group that there are
+      for (int st = max(st0, (h.page_units - ph + wt - 1) / wt); st < st1; ++st) {
+        const int t0 = (st * wt + ph - h.page_units) * kGroup;
+        if (t0 >= seen) break;
+        const int held = min(32, rows - t0);  // rows of this group that there are
         const uint32_t there = held == 32 ? ~0u : (1u << held) - 1u;
-        f32x16 sc;
+        const uint16_t* kp = kb + (size_t)t0 * DIM;
+        const uint16_t* vp = vb + (size_t)t0 * DIM;
+        u32x4 x[HB][2];
+        f32x16 sc[1];
 #pragma unroll
-        for (int r = 0; r < 16; ++r) sc[r] = 0.f;
+        for (int r = 0; r < 16; ++r) sc[0][r] = 0.f;
+        load(kp, x);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int i = 0; i < NB; ++i) {
-          const u32x4* p = reinterpret_cast<const u32x4*>(kb + (size_t)t0 * DIM + i * 1024 + lane * 16);
-          sc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, p[0]), qf[i][0], sc, 0, 0, 0);
-          sc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, p[1]), qf[i][1], sc, 0, 0, 0);
+        for (int i0 = 0; i0 < NB; i0 += HB) {
+          if (i0) load(kp + i0 * 1024, x);
+#pragma unroll
+          for (int i = 0; i < HB; ++i)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              sc[0] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, x[i][e]), query(i0 + i, e), sc[0], 0, 0, 0);
+          __builtin_amdgcn_sched_barrier(0);
         }
-        // bit t: the lane's row sees place t0 + t: every tail token, and its ancestors
+        load(vp, x);
+        // bit b: the lane's row sees place t0 + b: every tail token, and its ancestors
         uint32_t see = 0;
         if (on) {
-          const int rr = my / group - row_lo;
-          const int shift = t0 - v.tail;  // the step's row at place t0
-          uint32_t w = 0;
+          const int shift = t0 - tail;  // the step's row at place t0
           if (shift >= 0) {
             const int k = shift >> 5, b = shift & 31;
-            const uint64_t two = (uint64_t)s_anc[rr][k] | ((uint64_t)(k + 1 < kStepRows / 32 ? s_anc[rr][k + 1] : 0u) << 32);
-            w = (uint32_t)(two >> b);
+            const uint64_t two = (uint64_t)anc[k] | ((uint64_t)(k + 1 < kStepRows / 32 ? anc[k + 1] : 0u) << 32);
+            see = (uint32_t)(two >> b);
           } else if (shift > -32) {
-            w = (s_anc[rr][0] << -shift) | ((1u << -shift) - 1u);
+            see = (anc[0] << -shift) | ((1u << -shift) - 1u);
           } else {
-            w = ~0u;
+            see = ~0u;
           }
-          see = w & there;
+          see &= there;
         }
-        float p[16];
-        bf16x8 pb[2];
-        softmax_step(acc, sc, c2, 1.0f, see, half, p, pb);
+        bf16x8 pb[1][2];
+        softmax_step<NB, 1, true>(acc, m, l, sc, {c2}, {0.f}, {1.f}, {true}, see, half, pb);
         // values: a row that is not there, or an infinity or NaN that some
         // query row does not see, must not meet its probability of zero
-        u32x4 vr[NB][2];
         uint32_t odd = 0;
+        const uint32_t mine = there >> (half * 4);
 #pragma unroll
-        for (int i = 0; i < NB; ++i) {
-          const u32x4* q = reinterpret_cast<const u32x4*>(vb + (size_t)t0 * DIM + i * 1024 + lane * 16);
-          vr[i][0] = q[0];
-          vr[i][1] = q[1];
+        for (int i0 = 0; i0 < NB; i0 += HB) {
+          if (i0) load(vp + i0 * 1024, x);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            // slots 2 e, 2 e + 1: tokens 8 (e >> 1) + 4 half + 2 (e & 1) and the next
-            const int t = (e >> 1) * 8 + half * 4 + (e & 1) * 2;
-            uint32_t w = vr[i][e >> 2][e & 3];
-            w &= ((there >> t) & 1 ? 0xFFFFu : 0u) | ((there >> (t + 1)) & 1 ? 0xFFFF0000u : 0u);
-            odd |= (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
-            vr[i][e >> 2][e & 3] = w;
-          }
-        }
-        const bool strange = __any(odd);
-        if (strange) {
-#pragma unroll
-          for (int i = 0; i < NB; ++i)
+          for (int i = 0; i < HB; ++i) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-              uint32_t w = vr[i][e >> 2][e & 3];
-              if ((w & 0x7F80u) == 0x7F80u) w &= 0xFFFF0000u;
-              if ((w & 0x7F800000u) == 0x7F800000u) w &= 0xFFFFu;
-              vr[i][e >> 2][e & 3] = w;
+              // slots 2 e, 2 e + 1: tokens 8 (e >> 1) + 4 half + 2 (e & 1) and the next
+              const int b = (e >> 1) * 8 + (e & 1) * 2;
+              uint32_t w = x[i][e >> 2][e & 3];
+              w &= (bit_mask(mine, b) & 0xFFFFu) | (bit_mask(mine, b + 1) & 0xFFFF0000u);
+              // an exponent of all ones carries into the sign's place
+              const uint32_t bad = ((((w & 0x7F807F80u) + 0x00800080u) >> 15) & 0x00010001u) * 0xFFFFu;
+              odd |= bad;
+              w &= ~bad;
+              x[i][e >> 2][e & 3] = w;
             }
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              acc[i0 + i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, x[i][e]), pb[0][e], acc[i0 + i], 0, 0, 0);
+            __builtin_amdgcn_sched_barrier(0);
+          }
         }
+        if (odd) sh.strange = 1;
+      }
+    }
+
+    if (np > 0) {
+      if constexpr (DIM > 128) load_keys();
+      load_values();
+    }
+    for (int kb = 0; kb < np;) {
+      for (int k = 0; k < cnt; k += U) {
+        f32x16 sc[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) sc[u][r] = 0.f;
 #pragma unroll
         for (int i = 0; i < NB; ++i) {
-          acc.o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, vr[i][0]), pb[0], acc.o[i], 0, 0, 0);
-          acc.o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, vr[i][1]), pb[1], acc.o[i], 0, 0, 0);
+          bf16x8 x[U], y[U];
+#pragma unroll
+          for (int u = 0; u < U; ++u) codes16<KIND>(kr[u][i], x[u], y[u]);
+#pragma unroll
+          for (int u = 0; u < U; ++u) sc[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x[u], query(i, 0), sc[u], 0, 0, 0);
+#pragma unroll
+          for (int u = 0; u < U; ++u) sc[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(y[u], query(i, 1), sc[u], 0, 0, 0);
+          // in order: the next fragments' conversion runs under these
+          // products, and no earlier (hoisted, they take every register)
+          __builtin_amdgcn_sched_barrier(0);
         }
-        if (strange) {  // those values again, by themselves, for the rows that see them
-          float* sp = &s_o[0][0] + wave * (32 * kTile);  // free until the waves join
+        const uint8_t* next[U];
 #pragma unroll
-          for (int r = 0; r < 16; ++r) sp[((r >> 2) * 8 + half * 4 + (r & 3)) * kTile + col] = p[r];
-          wave_lds_sync();
-          for (int t = 0; t < held; ++t) {
-            if (!((see >> t) & 1)) continue;
-            const float pt = sp[t * kTile + col];
+        for (int u = 0; u < U; ++u) {
+          next[u] = at_page(k + U + u);
+          load_page(next[u], kr[u]);
+        }
+        float c[U], e[U], f[U];
+        bool valid[U];
 #pragma unroll
-            for (int i = 0; i < NB; ++i)
+        for (int u = 0; u < U; ++u) {
+          auto lane_of = [&](float x) __attribute__((always_inline)) {
+            return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(x), k + u));
+          };
+          c[u] = lane_of(ks);
+          e[u] = lane_of(lv);
+          f[u] = lane_of(rv);
+          valid[u] = k + u < cnt;
+        }
+        bf16x8 pb[U][2];
+        softmax_step<NB, U, false>(acc, m, l, sc, c, e, f, valid, 0u, half, pb);
 #pragma unroll
-              for (int r = 0; r < 16; ++r) {
-                const uint16_t w = vb[value_at(t0 + t, i * 32 + (r >> 2) * 8 + half * 4 + (r & 3), DIM)];
-                if ((w & 0x7F80u) == 0x7F80u) acc.o[i][r] += pt * __uint_as_float((uint32_t)w << 16);
-              }
+        for (int u = 0; u < U; ++u) {
+#pragma unroll
+          for (int i = 0; i < NB; i += 2) {
+            bf16x8 x[2], y[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) codes16<KIND>(vr[u][i + j], x[j], y[j]);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) acc[i + j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x[j], pb[u][0], acc[i + j], 0, 0, 0);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) acc[i + j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(y[j], pb[u][1], acc[i + j], 0, 0, 0);
+            __builtin_amdgcn_sched_barrier(0);
           }
-          wave_lds_sync();
         }
+#pragma unroll
+        for (int u = 0; u < U; ++u) load_page(next[u] + to_v, vr[u]);
+      }
+      kb += 64;
+      if (kb < np) {
+        fetch(kb);
+        load_keys();
+        load_values();
       }
     }
 
-    // join the four waves: both halves of a column's sum, then the columns
-    acc.l += __shfl_xor(acc.l, 32, 64);
-    if (poison) acc.l = __builtin_nanf("");
+    // join the waves that share a tile: both halves of a column's sum, then
+    // the waves' shares of the tokens, half of the waves to the other half
+    l += __shfl_xor(l, 32, 64);
+    if (poison) l = __builtin_nanf("");
     if (half == 0) {
-      s_ml[wave][col][0] = acc.m;
-      s_ml[wave][col][1] = acc.l;
+      sh.ml[wave][col][0] = m;
+      sh.ml[wave][col][1] = l;
     }
     __syncthreads();
-    float m = kFloor, l = 0.f;
+    {
+      const float own = m;
+      for (int w = wr; w < kWaves; w += h.wr) m = fmaxf(m, sh.ml[w][col][0]);
+      l = 0.f;
+      for (int w = wr; w < kWaves; w += h.wr) l += sh.ml[w][col][1] * __builtin_amdgcn_exp2f(sh.ml[w][col][0] - m);
+      const float f = __builtin_amdgcn_exp2f(own - m);
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) m = fmaxf(m, s_ml[w][col][0]);
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) l += s_ml[w][col][1] * __builtin_amdgcn_exp2f(s_ml[w][col][0] - m);
-    const float f = __builtin_amdgcn_exp2f(acc.m - m);
-#pragma unroll
-    for (int i = 0; i < NB; ++i) acc.o[i] *= f;
-    // dims in the order (block, register, half): a lane's place is conflict-free
-    auto place = [&](int i, int r) { return ((i * 16 + r) * 2 + half) * 32 + col; };
-    if (wave >= 2) {
-#pragma unroll
-      for (int i = 0; i < NB; ++i)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) s_o[wave - 2][place(i, r)] = acc.o[i][r];
+      for (int i = 0; i < NB; ++i) acc[i] *= f;
     }
-    __syncthreads();
-    if (wave < 2) {
+    if (h.wr < kWaves) {
+      constexpr int HB = NB < 4 ? NB : 4;
+      auto place = [&](int i, int r) __attribute__((always_inline)) { return ((i * 16 + r) * 2 + half) * 32 + col; };
 #pragma unroll
-      for (int i = 0; i < NB; ++i)
+      for (int i0 = 0; i0 < NB; i0 += HB) {
+        auto give = [&](float* to) __attribute__((always_inline)) {
 #pragma unroll
-        for (int r = 0; r < 16; ++r) acc.o[i][r] += s_o[wave][place(i, r)];
-    }
-    __syncthreads();
-    if (wave == 1) {
+          for (int i = 0; i < HB; ++i)
 #pragma unroll
-      for (int i = 0; i < NB; ++i)
+            for (int r = 0; r < 16; ++r) to[place(i, r)] = acc[i0 + i][r];
+        };
+        auto take = [&](const float* from) __attribute__((always_inline)) {
 #pragma unroll
-        for (int r = 0; r < 16; ++r) s_o[0][place(i, r)] = acc.o[i][r];
-    }
-    __syncthreads();
-    if (wave == 0) {
+          for (int i = 0; i < HB; ++i) {
 #pragma unroll
-      for (int i = 0; i < NB; ++i)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) s_o[0][place(i, r)] += acc.o[i][r];
-    }
-    __syncthreads();
-
-    // the item's rows from s_o[0] (sum m, l in every lane): thread = (row, dims)
-    const int nrow = min(kTile, q_rows - first_row);
-    const bool split = u0 > 0 || u1 < units;
-    auto sum_at = [&](int row, int d) {  // dim d of row `row` in s_o[0]
-      const int i = d >> 5, e = d & 31;
-      const int r = (e >> 3) * 4 + (e & 3), h = (e >> 2) & 1;
-      return s_o[0][((i * 16 + r) * 2 + h) * 32 + row];
-    };
-    auto out_at = [&](int row) {
-      const int q = first_row + row;
-      return ((size_t)(v.row0 + q / group) * a.q_heads + kvh * group + q % group) * DIM;
-    };
-    if (!split) {
-      if (wave == 0 && half == 0) s_ml[0][col][1] = l;
-      __syncthreads();
-      for (int e = tid; e < nrow * (DIM / 2); e += kThreads) {
-        const int row = e / (DIM / 2), d = e % (DIM / 2) * 2;
-        const float inv = 1.0f / s_ml[0][row][1];
-        *reinterpret_cast<uint32_t*>(a.out + out_at(row) + d) = pack_bf16(sum_at(row, d) * inv, sum_at(row, d + 1) * inv);
-      }
-    } else {
-      // hand-off without a device-scope fence (which writes back the whole
-      // L2): partials are stored through to the coherent level, every thread
-      // waits for its own stores, then one thread counts the arrival
-      const int slot = 2 * wg + (at != begin);
-      const rsrc_t rp = make_rsrc(a.part + (size_t)slot * (kTile * DIM), kTile * DIM * 4);
-      for (int e = tid; e < nrow * (DIM / 4); e += kThreads) {
-        const int row = e / (DIM / 4), d = e % (DIM / 4) * 4;
-        const u32x4 x = {__float_as_uint(sum_at(row, d)), __float_as_uint(sum_at(row, d + 1)),
-                         __float_as_uint(sum_at(row, d + 2)), __float_as_uint(sum_at(row, d + 3))};
-        __builtin_amdgcn_raw_buffer_store_b128(x, rp, (row * DIM + d) * 4, 0, kDeviceScope);
-      }
-      const rsrc_t rm = make_rsrc(a.part_ml, (uint32_t)(2 * a.G) * kTile * 8);
-      if (wave == 0 && half == 0) {
-        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(m), rm, (slot * kTile + col) * 8, 0, kDeviceScope);
-        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(l), rm, (slot * kTile + col) * 8 + 4, 0, kDeviceScope);
-      }
-      __atomic_signal_fence(__ATOMIC_SEQ_CST);
-      __builtin_amdgcn_s_waitcnt(0);
-      __atomic_signal_fence(__ATOMIC_SEQ_CST);
-      __syncthreads();
-      const int wf = owner_of(item0, total, wgs), wl = owner_of(item0 + units - 1, total, wgs);
-      // one counter for each split item: its first unit's workgroup can begin
-      // at most one such item before its own end
-      if (tid == 0) s_last = atomicAdd(&a.cnt[wf], 1u) == (uint32_t)(wl - wf) ? 1 : 0;
-      __syncthreads();
-      if (s_last) {
-        if (tid == 0) a.cnt[wf] = 0;
-        auto slot_of = [&](int w) { return 2 * w + (total * w / wgs < item0 ? 1 : 0); };
-        for (int e = tid; e < nrow * (DIM / 4); e += kThreads) {
-          const int row = e / (DIM / 4), d = e % (DIM / 4) * 4;
-          float M = kFloor;
-          for (int w = wf; w <= wl; ++w)
-            M = fmaxf(M, __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rm, (slot_of(w) * kTile + row) * 8, 0, kDeviceScope)));
-          float L = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-          for (int w = wf; w <= wl; ++w) {
-            const int sl = slot_of(w);
-            const float mw = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rm, (sl * kTile + row) * 8, 0, kDeviceScope));
-            const float lw = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rm, (sl * kTile + row) * 8 + 4, 0, kDeviceScope));
-            const rsrc_t rw = make_rsrc(a.part + (size_t)sl * (kTile * DIM), kTile * DIM * 4);
-            const u32x4 x = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rw, (row * DIM + d) * 4, 0, kDeviceScope));
-            const float g = __builtin_amdgcn_exp2f(mw - M);
-            L += lw * g;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) o[i] += __uint_as_float(x[i]) * g;
+            for (int r = 0; r < 16; ++r) acc[i0 + i][r] += from[place(i, r)];
+            __builtin_amdgcn_sched_barrier(0);
           }
-          const float inv = 1.0f / L;
-          *reinterpret_cast<uint2*>(a.out + out_at(row) + d) =
-              make_uint2(pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv));
+        };
+        for (int n = kWaves / 2; n >= h.wr; n >>= 1) {  // the upper half of the waves to the lower
+          if (wave >= n && wave < 2 * n) give(sh.o[wave - n]);
+          __syncthreads();
+          if (wave < n) take(sh.o[wave]);
+          __syncthreads();
         }
       }
     }
-    __syncthreads();
-    at += u1 - u0;
+    // waves 0 .. wr - 1 hold the tiles' sums: out, or to the partial sums
+    const bool split = st0 > 0 || st1 < h.steps - kItemSteps;
+    float* part = a.part + (size_t)(2 * wg + second) * kPartFloats;
+    float2* part_ml = reinterpret_cast<float2*>(a.part_ml) + (size_t)(2 * wg + second) * (kPartFloats / DIM);
+    if (wave < h.wr && my < q_rows) {
+      const int row = my - block_row;
+      if (!split) {
+        const float inv = 1.0f / l;
+        uint16_t* o = a.out + ((size_t)(v.row0 + my / group) * a.q_heads + kvh * group + my % group) * DIM + half * 4;
+#pragma unroll
+        for (int i = 0; i < NB; ++i)
+#pragma unroll
+          for (int r = 0; r < 16; r += 4)
+            *reinterpret_cast<uint2*>(o + i * 32 + r * 2) =
+                make_uint2(pack_bf16(acc[i][r] * inv, acc[i][r + 1] * inv), pack_bf16(acc[i][r + 2] * inv, acc[i][r + 3] * inv));
+      } else {
+        float* o = part + row * DIM + half * 4;
+#pragma unroll
+        for (int i = 0; i < NB; ++i)
+#pragma unroll
+          for (int r = 0; r < 16; r += 4)
+            *reinterpret_cast<float4*>(o + i * 32 + r * 2) = make_float4(acc[i][r], acc[i][r + 1], acc[i][r + 2], acc[i][r + 3]);
+        if (half == 0) part_ml[row] = make_float2(m, l);
+      }
+    }
+    // infinities and NaN among the run's recent values, by themselves, for the
+    // rows that see them: no finite sum brings the output back from them
+    if (sh.strange) {
+      __syncthreads();
+      const uint16_t* vb = a.c.recent + recent_at(a.c, a.layer, v.slot, kvh, 1);
+      const int t0 = max(0, (st0 * wt - h.page_units) * kGroup);
+      const int t1 = min(tail + v.rows, (st1 * wt - h.page_units) * kGroup);
+      for (int e = tid; e < block_rows * DIM; e += kThreads) {
+        const int q = block_row + e / DIM, d = e % DIM, r = q / group;
+        float sum = 0.f;
+        for (int t = t0; t < t1; ++t) {
+          const int j = t - tail;
+          const uint16_t w = vb[value_at(t, d, DIM)];
+          if ((w & 0x7F80u) == 0x7F80u && (j < 0 || ((sh.anc[r - b_lo][j >> 5] >> (j & 31)) & 1)))
+            sum += __uint_as_float((uint32_t)w << 16);
+        }
+        if (sum == 0.f) continue;
+        if (split) {
+          part[e] += sum;
+        } else {
+          uint16_t* o = a.out + ((size_t)(v.row0 + r) * a.q_heads + kvh * group + q % group) * DIM + d;
+          *o = f32_to_bf16_rne(__uint_as_float((uint32_t)*o << 16) + sum);
+        }
+      }
+    }
+    if (split && st0 == 0 && tid == 0) {  // at most one item per workgroup begins here and ends elsewhere
+      SplitItem t;
+      t.last = (int)(((item0 + h.steps - kItemSteps) * wgs - 1) / total);
+      t.rows = block_rows;
+      t.row0 = v.row0;
+      t.first_row = block_row;
+      t.kvh = kvh;
+      t.first_slot = second;
+      *split_item = t;
+    }
   }
 }
 
+// Joins the partial sums of the items that several workgroups share: with
+// the largest running maximum M, out = sum_w 2^(m_w - M) o_w / sum_w 2^(m_w - M) l_w.
+// One workgroup per split item and piece of its rows. The weights 2^(m_w - M)
+// of its rows come first, a thread each; then a thread owns 4 dims of a row,
+// its loads from the contributors independent of each other.
+constexpr int kJoinThreads = 256, kJoinPieces = 8;
+
 template <int DIM>
+__global__ __launch_bounds__(kJoinThreads) void kv_attention_join_kernel(AttentionArgs a) {
+  constexpr int kPer = DIM / 4;               // threads of a row
+  constexpr int kRows = kJoinThreads / kPer;  // rows a workgroup handles at a time
+  constexpr int kFew = 64;                    // contributors whose weights are kept at a time
+  __shared__ float s_w[kRows][kFew], s_m[kRows][kPer], s_l[kRows][kPer];
+  const SplitItem t = static_cast<const SplitItem*>(a.items)[blockIdx.x];
+  if (t.last < 0) return;
+  const int group = a.q_heads / a.c.kv_heads, wf = blockIdx.x, n = t.last - wf + 1;
+  const int r = threadIdx.x / kPer, d4 = threadIdx.x % kPer;
+  const float2* ml = reinterpret_cast<const float2*>(a.part_ml);
+  for (int row0 = blockIdx.y * kRows; row0 < t.rows; row0 += kJoinPieces * kRows) {
+    const int row = min(row0 + r, t.rows - 1);
+    // contributor w's partial sum: the first may be its workgroup's second, later ones begin with the item
+    auto slot = [&](int w) __attribute__((always_inline)) { return 2 * (wf + w) + (w ? 0 : t.first_slot); };
+    auto ml_at = [&](int w) __attribute__((always_inline)) { return ml[(size_t)slot(w) * (kPartFloats / DIM) + row]; };
+    float M = kFloor;
+    for (int w = d4; w < n; w += kPer) M = fmaxf(M, ml_at(w).x);
+    s_m[r][d4] = M;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) M = fmaxf(M, s_m[r][i]);
+    float L = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int w0 = 0; w0 < n; w0 += kFew) {
+      const int cnt = min(kFew, n - w0);
+      __syncthreads();
+      for (int w = d4; w < cnt; w += kPer) {
+        const float2 x = ml_at(w0 + w);
+        const float g = __builtin_amdgcn_exp2f(x.x - M);
+        s_w[r][w] = g;
+        L += x.y * g;
+      }
+      __syncthreads();
+#pragma unroll 8
+      for (int w = 0; w < cnt; ++w) {
+        const float4 z = *reinterpret_cast<const float4*>(a.part + (size_t)slot(w0 + w) * kPartFloats + row * DIM + d4 * 4);
+        const float g = s_w[r][w];
+        o.x = __builtin_fmaf(z.x, g, o.x);
+        o.y = __builtin_fmaf(z.y, g, o.y);
+        o.z = __builtin_fmaf(z.z, g, o.z);
+        o.w = __builtin_fmaf(z.w, g, o.w);
+      }
+    }
+    s_l[r][d4] = L;
+    __syncthreads();
+    L = 0.f;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) L += s_l[r][i];
+    if (row0 + r < t.rows) {
+      const float inv = 1.0f / L;
+      const int q = t.first_row + row;
+      *reinterpret_cast<uint2*>(a.out + ((size_t)(t.row0 + q / group) * a.q_heads + t.kvh * group + q % group) * DIM + d4 * 4) =
+          make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+    }
+  }
+}
+
+template <int DIM, bool STREAM>
 hipError_t launch_dim(const AttentionArgs& a, hipStream_t s) {
   if (a.c.kind == 0)
-    hipLaunchKernelGGL((kv_attention_kernel<DIM, 0>), dim3(a.G), dim3(kThreads), 0, s, a);
+    hipLaunchKernelGGL((kv_attention_kernel<DIM, 0, STREAM>), dim3(a.G), dim3(kThreads), 0, s, a);
   else
-    hipLaunchKernelGGL((kv_attention_kernel<DIM, 1>), dim3(a.G), dim3(kThreads), 0, s, a);
+    hipLaunchKernelGGL((kv_attention_kernel<DIM, 1, STREAM>), dim3(a.G), dim3(kThreads), 0, s, a);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((kv_attention_join_kernel<DIM>), dim3(a.G, kJoinPieces), dim3(kJoinThreads), 0, s, a);
   return hipGetLastError();
 }
 
@@ -547,19 +740,20 @@ hipError_t launch_dim(const AttentionArgs& a, hipStream_t s) {
 AttentionPlan plan_kv_attention(const KvArgs& c, int num_seq, int total, int q_heads, int num_cu) {
   (void)num_seq; (void)total; (void)q_heads;
   AttentionPlan p{};
-  p.G = num_cu * 2;
-  p.max_items = p.G;
-  p.off_part = ((size_t)p.G * 4 + 255) & ~size_t(255);
-  p.off_ml = p.off_part + (size_t)2 * p.G * kTile * c.dim * 4;
-  p.ws_bytes = p.off_ml + (size_t)2 * p.G * kTile * 8;
+  p.G = num_cu;
+  p.off_part = ((size_t)p.G * sizeof(SplitItem) + 255) & ~size_t(255);
+  p.off_ml = p.off_part + (size_t)2 * p.G * kPartFloats * 4;
+  p.ws_bytes = p.off_ml + (size_t)2 * p.G * (kPartFloats / c.dim) * 8;
   return p;
 }
 
 hipError_t launch_kv_attention(const AttentionArgs& a, hipStream_t s) {
+  // sequences of about one tile read every page once: past the caches
+  const bool stream = (int64_t)a.st.total * (a.q_heads / a.c.kv_heads) <= (int64_t)a.st.num_seq * kTile;
   switch (a.c.dim) {
-    case 64: return launch_dim<64>(a, s);
-    case 128: return launch_dim<128>(a, s);
-    default: return launch_dim<256>(a, s);
+    case 64: return stream ? launch_dim<64, true>(a, s) : launch_dim<64, false>(a, s);
+    case 128: return stream ? launch_dim<128, true>(a, s) : launch_dim<128, false>(a, s);
+    default: return stream ? launch_dim<256, true>(a, s) : launch_dim<256, false>(a, s);
   }
 }
 

@@ -52,11 +52,10 @@ struct AttentionArgs {
   int q_heads;
   float scale;
   uint16_t* out;
-  uint32_t* cnt;   // [items] arrival counters, zero between calls
-  float* part;     // [2 G][32 rows][dim] partial sums, not normalised
-  float* part_ml;  // [2 G][32 rows][2] their running maxima and sums
+  void* items;     // [G] the item each workgroup begins and others go on with
+  float* part;     // [2 G][128 rows][dim] partial sums, not normalised
+  float* part_ml;  // [2 G][128 rows][2] their running maxima and sums
   int G;           // workgroups
-  int max_items;   // counters the workspace holds
 };
 
 struct CommitArgs {
@@ -90,7 +89,7 @@ hipError_t launch_kv_append(const AppendArgs& a, hipStream_t s);
 hipError_t launch_kv_commit(const CommitArgs& a, hipStream_t s);
 
 struct AttentionPlan {
-  int G, max_items;
+  int G;
   size_t off_part, off_ml, ws_bytes;
 };
 AttentionPlan plan_kv_attention(const KvArgs& c, int num_seq, int total, int q_heads, int num_cu);
