@@ -21,6 +21,8 @@
 // batches balance. Items that several workgroups share leave partial sums,
 // which a second launch joins in workgroup order: results are bitwise
 // reproducible.
+#include <limits.h>
+
 #include "kv_internal.h"
 #include "w12_device.h"
 
@@ -173,7 +175,7 @@ struct Shared {
   static constexpr int kRows = kBlockTiles<DIM> * kTile;
   union {
     uint4 q[kBlockTiles<DIM>][DIM / 32][2][64];  // query tiles as B operands
-    float o[kWaves / 2][4096];                   // sums of four waves while they join
+    float4 x[kWaves][512];                       // sums that waves hand to each other
   };
   uint32_t anc[kRows][kStepRows / 32];
   int64_t first[kStepRows + 1];  // steps before each sequence
@@ -256,7 +258,16 @@ __global__ __launch_bounds__(kThreads, 2) void kv_attention_kernel(AttentionArgs
     seq = lo;
   }
 
+  // the thread's index, opaque: each phase of an item derives its places anew,
+  // so that none is computed ahead and kept in a register (or spilled) through
+  // the others
+  auto own_index = [thread = tid]() __attribute__((always_inline)) {
+    int t = thread;
+    asm volatile("" : "+v"(t));
+    return t;
+  };
   for (int64_t at = begin; at < end;) {
+    const int tid = own_index(), lane = tid & 63, col = lane & 31, half = lane >> 5;
     while (sh.first[seq + 1] <= at) ++seq;
     const SeqInfo v = sh.seq[seq];
     const Shape h = shape_of(v);
@@ -278,6 +289,24 @@ __global__ __launch_bounds__(kThreads, 2) void kv_attention_kernel(AttentionArgs
     const int my = wave_row + col;  // the lane's query row: row my / group, head my % group
     const bool on = my < q_rows && ok;
 
+    // the tile's query rows as B operands: dims 32 i + 16 half + 0..15 of a lane's row
+    bf16x8 qr[kQueryRegs ? NB : 1][2];
+    __syncthreads();  // the last item's joins are done with the shared arrays
+    if (kQueryRegs || ph == 0) {
+      const int r = on ? my / group : 0, hd = kvh * group + (on ? my % group : 0);
+      const u32x4* p = reinterpret_cast<const u32x4*>(a.q + ((size_t)(v.row0 + r) * a.q_heads + hd) * DIM + half * 16);
+#pragma unroll
+      for (int i = 0; i < NB; ++i)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          u32x4 x = {0, 0, 0, 0};
+          if (on) x = p[i * 4 + e];
+          if constexpr (kQueryRegs)
+            qr[i][e] = __builtin_bit_cast(bf16x8, x);
+          else
+            sh.q[wr][i][e][lane] = __builtin_bit_cast(uint4, x);
+        }
+    }
     // pages: units st * wt + ph, ids and scales of 64 at a time
     const int pst1 = idle ? st0 : min(st1, (h.page_units - ph + wt - 1) / wt);
     const int np = max(0, pst1 - st0);
@@ -287,56 +316,61 @@ __global__ __launch_bounds__(kThreads, 2) void kv_attention_kernel(AttentionArgs
     const float c2 = a.scale * kLog2e;
     int id, off, cnt;
     float ks, lv, rv;
-    auto fetch = [&](int kb) __attribute__((always_inline)) {
+    // ids of up to 64 units, a lane each, and (as loaded) their scales
+    auto fetch = [&](int kb, int lane) __attribute__((always_inline)) {
       cnt = min(64, np - kb);
-      // lanes past the last unit: a weight of zero (2^-inf)
       id = off = 0;
-      ks = rv = 0.f;
-      lv = -__builtin_huge_valf();
       if (lane < cnt) {
         const int u = (st0 + kb + lane) * wt + ph, j = u / per_page;
         id = a.c.table[(size_t)v.slot * a.c.max_pages + j];
         off = (u - j * per_page) * (kGroup * DIM);
-        const bool good = id >= 0 && id < a.c.num_pages;
-        if (!good) id = 0;
-        const float2 sc = *reinterpret_cast<const float2*>(a.c.scales + scale_at(a.c, a.layer, id, kvh, 0));
-        ks = good ? sc.x * c2 : __builtin_nanf("");
-        lv = __builtin_amdgcn_logf(sc.y);
-        rv = __builtin_amdgcn_rcpf(sc.y);
       }
+      const bool good = id >= 0 && id < a.c.num_pages;
+      if (!good) id = 0;
+      const float2 sc = *reinterpret_cast<const float2*>(a.c.scales + scale_at(a.c, a.layer, id, kvh, 0));
+      ks = sc.x;
+      rv = sc.y;
+      off = good ? off : off | INT_MIN;
+    };
+    // the scales' factors; lanes past the last unit: a weight of zero (2^-inf)
+    auto factors = [&](int lane) __attribute__((always_inline)) {
+      const bool live = lane < cnt;
+      ks = live ? ks * c2 : 0.f;
+      if (off < 0) ks = __builtin_nanf("");
+      lv = live ? __builtin_amdgcn_logf(rv) : -__builtin_huge_valf();
+      rv = live ? __builtin_amdgcn_rcpf(rv) : 0.f;
     };
     // past the last unit the loads repeat it: they stay unconditional, so
     // that every wait is for the oldest ones in flight alone
     auto at_page = [&](int k) __attribute__((always_inline)) {
       k = min(k, cnt - 1);
-      const uint32_t pid = __builtin_amdgcn_readlane(id, k), o = __builtin_amdgcn_readlane(off, k);
+      const uint32_t pid = __builtin_amdgcn_readlane(id, k), o = __builtin_amdgcn_readlane(off, k) & INT_MAX;
       return page0 + (size_t)pid * page_bytes + o;
     };
-    auto load_page = [&](const uint8_t* p, u32x4 (&x)[NB]) __attribute__((always_inline)) {
+    auto load_page = [&](const uint8_t* p, int to, u32x4 (&x)[NB]) __attribute__((always_inline)) {
 #pragma unroll
       for (int i = 0; i < NB; ++i) {
-        const u32x4* q = reinterpret_cast<const u32x4*>(p + i * 1024 + lane * 16);
+        const u32x4* q = reinterpret_cast<const u32x4*>(p + i * 1024 + to);
         x[i] = STREAM ? __builtin_nontemporal_load(q) : *q;
       }
     };
     u32x4 kr[U][NB], vr[U][NB];
     // the first keys are on their way before anything else of the item,
     // where the registers hold them next to the recent rows' operands
-    auto load_keys = [&]() __attribute__((always_inline)) {
+    auto load_keys = [&](int to) __attribute__((always_inline)) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) load_page(at_page(u), kr[u]);
+      for (int u = 0; u < U; ++u) load_page(at_page(u), to, kr[u]);
     };
-    auto load_values = [&]() __attribute__((always_inline)) {
+    auto load_values = [&](int to) __attribute__((always_inline)) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) load_page(at_page(u) + to_v, vr[u]);
+      for (int u = 0; u < U; ++u) load_page(at_page(u) + to_v, to, vr[u]);
     };
     if (np > 0) {
-      fetch(0);
-      if constexpr (DIM <= 128) load_keys();
+      fetch(0, lane);
+      if constexpr (DIM <= 128) load_keys(lane * 16);
     }
 
     // ancestors of the block's rows, a set of bits for each
-    __syncthreads();
     if (tid == 0) sh.bad = sh.strange = 0;
     __syncthreads();
     if (ok && st1 * wt > h.page_units) {
@@ -360,23 +394,6 @@ __global__ __launch_bounds__(kThreads, 2) void kv_attention_kernel(AttentionArgs
         }
       }
     }
-    // the tile's query rows as B operands: dims 32 i + 16 half + 0..15 of a lane's row
-    bf16x8 qr[kQueryRegs ? NB : 1][2];
-    if (kQueryRegs || ph == 0) {
-      const int r = on ? my / group : 0, hd = kvh * group + (on ? my % group : 0);
-      const u32x4* p = reinterpret_cast<const u32x4*>(a.q + ((size_t)(v.row0 + r) * a.q_heads + hd) * DIM + half * 16);
-#pragma unroll
-      for (int i = 0; i < NB; ++i)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          u32x4 x = {0, 0, 0, 0};
-          if (on) x = p[i * 4 + e];
-          if constexpr (kQueryRegs)
-            qr[i][e] = __builtin_bit_cast(bf16x8, x);
-          else
-            sh.q[wr][i][e][lane] = __builtin_bit_cast(uint4, x);
-        }
-    }
     __syncthreads();
     const bool poison = !ok || sh.bad;
 
@@ -386,17 +403,18 @@ __global__ __launch_bounds__(kThreads, 2) void kv_attention_kernel(AttentionArgs
     for (int i = 0; i < NB; ++i)
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][r] = 0.f;
-    const uint4* qs = &sh.q[wr][0][0][lane];
-    auto query = [&](int i, int e) __attribute__((always_inline)) {
-      if constexpr (kQueryRegs)
-        return qr[i][e];
-      else
-        return __builtin_bit_cast(bf16x8, qs[(i * 2 + e) * 64]);
-    };
-
     // recent rows: the committed tail, then the step's rows; the wave's tiles
     // see nothing behind their own last row
     if (!poison && !idle) {
+      const int lane = own_index() & 63, col = lane & 31, half = lane >> 5, my = wave_row + col;
+      const bool on = my < q_rows;
+      const uint4* qs = &sh.q[wr][0][0][lane];
+      auto query = [&](int i, int e) __attribute__((always_inline)) {
+        if constexpr (kQueryRegs)
+          return qr[i][e];
+        else
+          return __builtin_bit_cast(bf16x8, qs[(i * 2 + e) * 64]);
+      };
       const uint16_t* kb = a.c.recent + recent_at(a.c, a.layer, v.slot, kvh, 0) + lane * 16;
       const uint16_t* vb = a.c.recent + recent_at(a.c, a.layer, v.slot, kvh, 1) + lane * 16;
       const int rows = tail + v.rows, seen = tail + min((int)v.rows, (wave_row + kTile - 1) / group + 1);
@@ -450,57 +468,79 @@ __global__ __launch_bounds__(kThreads, 2) void kv_attention_kernel(AttentionArgs
         }
         bf16x8 pb[1][2];
         softmax_step<NB, 1, true>(acc, m, l, sc, {c2}, {0.f}, {1.f}, {true}, see, half, pb);
-        // values: a row that is not there, or an infinity or NaN that some
-        // query row does not see, must not meet its probability of zero
-        uint32_t odd = 0;
+        // values: what a query row does not see, be it an infinity or NaN of
+        // another branch or whatever lies behind the rows, must not meet its
+        // probability of zero; finite values may
         const uint32_t mine = there >> (half * 4);
+        uint32_t odd = 0;
 #pragma unroll
         for (int i0 = 0; i0 < NB; i0 += HB) {
           if (i0) load(vp + i0 * 1024, x);
+          uint32_t any = 0;  // an exponent of all ones carries into the sign's place
 #pragma unroll
-          for (int i = 0; i < HB; ++i) {
+          for (int i = 0; i < HB; ++i)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              // slots 2 e, 2 e + 1: tokens 8 (e >> 1) + 4 half + 2 (e & 1) and the next
-              const int b = (e >> 1) * 8 + (e & 1) * 2;
-              uint32_t w = x[i][e >> 2][e & 3];
-              w &= (bit_mask(mine, b) & 0xFFFFu) | (bit_mask(mine, b + 1) & 0xFFFF0000u);
-              // an exponent of all ones carries into the sign's place
-              const uint32_t bad = ((((w & 0x7F807F80u) + 0x00800080u) >> 15) & 0x00010001u) * 0xFFFFu;
-              odd |= bad;
-              w &= ~bad;
-              x[i][e >> 2][e & 3] = w;
-            }
+            for (int e = 0; e < 8; ++e) any |= (x[i][e >> 2][e & 3] & 0x7F807F80u) + 0x00800080u;
+          if (__any(any & 0x80008000u)) {
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
-              acc[i0 + i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, x[i][e]), pb[0][e], acc[i0 + i], 0, 0, 0);
-            __builtin_amdgcn_sched_barrier(0);
+            for (int i = 0; i < HB; ++i)
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                // slots 2 e, 2 e + 1: tokens 8 (e >> 1) + 4 half + 2 (e & 1) and the next
+                const int b = (e >> 1) * 8 + (e & 1) * 2;
+                uint32_t w = x[i][e >> 2][e & 3];
+                w &= (bit_mask(mine, b) & 0xFFFFu) | (bit_mask(mine, b + 1) & 0xFFFF0000u);
+                const uint32_t bad = ((((w & 0x7F807F80u) + 0x00800080u) >> 15) & 0x00010001u) * 0xFFFFu;
+                odd |= bad;
+                w &= ~bad;
+                x[i][e >> 2][e & 3] = w;
+              }
           }
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int i = 0; i < HB; ++i)
+              acc[i0 + i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, x[i][e]), pb[0][e], acc[i0 + i], 0, 0, 0);
+          __builtin_amdgcn_sched_barrier(0);
         }
         if (odd) sh.strange = 1;
       }
     }
 
-    if (np > 0) {
-      if constexpr (DIM > 128) load_keys();
-      load_values();
-    }
     for (int kb = 0; kb < np;) {
+      const int lane = own_index() & 63, half = lane >> 5, to = lane * 16;
+      if (kb) fetch(kb, lane);
+      if (kb || DIM > 128) load_keys(to);
+      load_values(to);
+      factors(lane);
+      const uint4* qs = &sh.q[wr][0][0][lane];
+      auto query = [&](int i, int e) __attribute__((always_inline)) {
+        if constexpr (kQueryRegs)
+          return qr[i][e];
+        else
+          return __builtin_bit_cast(bf16x8, qs[(i * 2 + e) * 64]);
+      };
       for (int k = 0; k < cnt; k += U) {
         f32x16 sc[U];
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
           for (int r = 0; r < 16; ++r) sc[u][r] = 0.f;
+        bf16x8 q0 = query(0, 0), q1 = query(0, 1);
 #pragma unroll
         for (int i = 0; i < NB; ++i) {
+          // the next operands' reads are under way while these are used
+          const bf16x8 n0 = query(i + 1 < NB ? i + 1 : i, 0), n1 = query(i + 1 < NB ? i + 1 : i, 1);
           bf16x8 x[U], y[U];
 #pragma unroll
           for (int u = 0; u < U; ++u) codes16<KIND>(kr[u][i], x[u], y[u]);
+          if constexpr (!kQueryRegs) __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-          for (int u = 0; u < U; ++u) sc[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x[u], query(i, 0), sc[u], 0, 0, 0);
+          for (int u = 0; u < U; ++u) sc[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x[u], q0, sc[u], 0, 0, 0);
 #pragma unroll
-          for (int u = 0; u < U; ++u) sc[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(y[u], query(i, 1), sc[u], 0, 0, 0);
+          for (int u = 0; u < U; ++u) sc[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(y[u], q1, sc[u], 0, 0, 0);
+          q0 = n0;
+          q1 = n1;
           // in order: the next fragments' conversion runs under these
           // products, and no earlier (hoisted, they take every register)
           __builtin_amdgcn_sched_barrier(0);
@@ -509,7 +549,7 @@ __global__ __launch_bounds__(kThreads, 2) void kv_attention_kernel(AttentionArgs
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           next[u] = at_page(k + U + u);
-          load_page(next[u], kr[u]);
+          load_page(next[u], to, kr[u]);
         }
         float c[U], e[U], f[U];
         bool valid[U];
@@ -540,18 +580,15 @@ __global__ __launch_bounds__(kThreads, 2) void kv_attention_kernel(AttentionArgs
           }
         }
 #pragma unroll
-        for (int u = 0; u < U; ++u) load_page(next[u] + to_v, vr[u]);
+        for (int u = 0; u < U; ++u) load_page(next[u] + to_v, to, vr[u]);
       }
       kb += 64;
-      if (kb < np) {
-        fetch(kb);
-        load_keys();
-        load_values();
-      }
     }
 
     // join the waves that share a tile: both halves of a column's sum, then
-    // the waves' shares of the tokens, half of the waves to the other half
+    // the waves' shares of the tokens
+    {
+    const int tid = own_index(), lane = tid & 63, col = lane & 31, half = lane >> 5, my = wave_row + col;
     l += __shfl_xor(l, 32, 64);
     if (poison) l = __builtin_nanf("");
     if (half == 0) {
@@ -559,65 +596,74 @@ __global__ __launch_bounds__(kThreads, 2) void kv_attention_kernel(AttentionArgs
       sh.ml[wave][col][1] = l;
     }
     __syncthreads();
+    constexpr int kR = 16 * NB;
+    float r[kR];  // the lane's sums, now one by one (a change of one in a vector of 16 may copy it)
     {
       const float own = m;
       for (int w = wr; w < kWaves; w += h.wr) m = fmaxf(m, sh.ml[w][col][0]);
       l = 0.f;
       for (int w = wr; w < kWaves; w += h.wr) l += sh.ml[w][col][1] * __builtin_amdgcn_exp2f(sh.ml[w][col][0] - m);
-      const float f = __builtin_amdgcn_exp2f(own - m);
+      const float scale = __builtin_amdgcn_exp2f(own - m);
 #pragma unroll
-      for (int i = 0; i < NB; ++i) acc[i] *= f;
+      for (int f = 0; f < kR; ++f) r[f] = acc[f >> 4][f & 15] * scale;
     }
-    if (h.wr < kWaves) {
-      constexpr int HB = NB < 4 ? NB : 4;
-      auto place = [&](int i, int r) __attribute__((always_inline)) { return ((i * 16 + r) * 2 + half) * 32 + col; };
+    // Of a tile's kR = 16 NB sums a lane, each of its wt waves ends with
+    // kR / wt: in every round two waves swap halves of what they hold, each
+    // adding the half that it keeps. Sum F is dim 2 F + 4 half (F % 4 == 0).
+    int mine0 = 0;  // the wave's first sum
 #pragma unroll
-      for (int i0 = 0; i0 < NB; i0 += HB) {
-        auto give = [&](float* to) __attribute__((always_inline)) {
+    for (int j = 0; j < 3; ++j) {
+      constexpr int kMost = 32;  // sums of a lane in the exchange buffer
+      const int n = kR >> (j + 1), part_n = n < kMost ? n : kMost, stride = kWaves >> (j + 1);  // partner: ph ^ stride
+      if (stride < h.wr) break;
+      const bool upper = tid & (stride * 64);  // keeps the upper half
+      if (wave & stride) mine0 += n;
 #pragma unroll
-          for (int i = 0; i < HB; ++i)
+      for (int f0 = 0; f0 < n; f0 += part_n) {
 #pragma unroll
-            for (int r = 0; r < 16; ++r) to[place(i, r)] = acc[i0 + i][r];
-        };
-        auto take = [&](const float* from) __attribute__((always_inline)) {
-#pragma unroll
-          for (int i = 0; i < HB; ++i) {
-#pragma unroll
-            for (int r = 0; r < 16; ++r) acc[i0 + i][r] += from[place(i, r)];
-            __builtin_amdgcn_sched_barrier(0);
-          }
-        };
-        for (int n = kWaves / 2; n >= h.wr; n >>= 1) {  // the upper half of the waves to the lower
-          if (wave >= n && wave < 2 * n) give(sh.o[wave - n]);
-          __syncthreads();
-          if (wave < n) take(sh.o[wave]);
-          __syncthreads();
+        for (int f = f0; f < f0 + part_n; ++f) {  // selects, not a branch: that would hold every sum twice
+          const float x = r[f], y = r[f + n];
+          r[f] = upper ? y : x;
+          r[f + n] = upper ? x : y;
         }
+        __builtin_amdgcn_sched_barrier(0);
+        float4* give = sh.x[wave] + lane;
+        const float4* take = sh.x[wave ^ stride] + lane;
+#pragma unroll
+        for (int f = 0; f < part_n; f += 4)
+          give[f * 16] = make_float4(r[n + f0 + f], r[n + f0 + f + 1], r[n + f0 + f + 2], r[n + f0 + f + 3]);
+        __syncthreads();
+#pragma unroll
+        for (int f = 0; f < part_n; f += 4) {
+          const float4 t = take[f * 16];
+          r[f0 + f] += t.x;
+          r[f0 + f + 1] += t.y;
+          r[f0 + f + 2] += t.z;
+          r[f0 + f + 3] += t.w;
+        }
+        __syncthreads();
       }
     }
-    // waves 0 .. wr - 1 hold the tiles' sums: out, or to the partial sums
+    // out, or to the partial sums
     const bool split = st0 > 0 || st1 < h.steps - kItemSteps;
     float* part = a.part + (size_t)(2 * wg + second) * kPartFloats;
     float2* part_ml = reinterpret_cast<float2*>(a.part_ml) + (size_t)(2 * wg + second) * (kPartFloats / DIM);
-    if (wave < h.wr && my < q_rows) {
-      const int row = my - block_row;
+    if (my < q_rows) {
+      const int row = my - block_row, n = kR / wt;
       if (!split) {
         const float inv = 1.0f / l;
-        uint16_t* o = a.out + ((size_t)(v.row0 + my / group) * a.q_heads + kvh * group + my % group) * DIM + half * 4;
+        uint16_t* o = a.out + ((size_t)(v.row0 + my / group) * a.q_heads + kvh * group + my % group) * DIM + 2 * mine0 + half * 4;
 #pragma unroll
-        for (int i = 0; i < NB; ++i)
-#pragma unroll
-          for (int r = 0; r < 16; r += 4)
-            *reinterpret_cast<uint2*>(o + i * 32 + r * 2) =
-                make_uint2(pack_bf16(acc[i][r] * inv, acc[i][r + 1] * inv), pack_bf16(acc[i][r + 2] * inv, acc[i][r + 3] * inv));
+        for (int f = 0; f < kR; f += 4)
+          if (f < n)
+            *reinterpret_cast<uint2*>(o + 2 * f) =
+                make_uint2(pack_bf16(r[f] * inv, r[f + 1] * inv), pack_bf16(r[f + 2] * inv, r[f + 3] * inv));
       } else {
-        float* o = part + row * DIM + half * 4;
+        float* o = part + row * DIM + 2 * mine0 + half * 4;
 #pragma unroll
-        for (int i = 0; i < NB; ++i)
-#pragma unroll
-          for (int r = 0; r < 16; r += 4)
-            *reinterpret_cast<float4*>(o + i * 32 + r * 2) = make_float4(acc[i][r], acc[i][r + 1], acc[i][r + 2], acc[i][r + 3]);
-        if (half == 0) part_ml[row] = make_float2(m, l);
+        for (int f = 0; f < kR; f += 4)
+          if (f < n) *reinterpret_cast<float4*>(o + 2 * f) = make_float4(r[f], r[f + 1], r[f + 2], r[f + 3]);
+        if (half == 0 && ph == 0) part_ml[row] = make_float2(m, l);
       }
     }
     // infinities and NaN among the run's recent values, by themselves, for the
@@ -655,6 +701,7 @@ __global__ __launch_bounds__(kThreads, 2) void kv_attention_kernel(AttentionArgs
       t.first_slot = second;
       *split_item = t;
     }
+    }
   }
 }
 
@@ -663,7 +710,7 @@ __global__ __launch_bounds__(kThreads, 2) void kv_attention_kernel(AttentionArgs
 // One workgroup per split item and piece of its rows. The weights 2^(m_w - M)
 // of its rows come first, a thread each; then a thread owns 4 dims of a row,
 // its loads from the contributors independent of each other.
-constexpr int kJoinThreads = 256, kJoinPieces = 8;
+constexpr int kJoinThreads = 256, kJoinPieces = 16;
 
 template <int DIM>
 __global__ __launch_bounds__(kJoinThreads) void kv_attention_join_kernel(AttentionArgs a) {
