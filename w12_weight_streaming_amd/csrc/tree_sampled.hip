@@ -19,9 +19,10 @@
 // differ; at 64 none in 10^9).
 //
 // Three launches: chunk maxima and sums of every row (bound by reading the
-// logits); one workgroup per tree walks from the root; the next token is
-// drawn from the last row, chunk sums over many workgroups, the last of a
-// tree's to arrive finding the chunk and the token in it.
+// logits and by 64-bit arithmetic in equal parts); one workgroup per tree
+// walks from the root, every node's probability looked up beforehand; the
+// next token is drawn from the last row, chunk sums over many workgroups, the
+// last of a tree's to arrive finding the chunk and the token in it.
 #include "kv_internal.h"
 #include "w12_device.h"
 
@@ -32,10 +33,12 @@ constexpr int kChunk = 4096;      // tokens of one workgroup of a row
 constexpr int kStatThreads = 256;
 constexpr int kWalkThreads = 1024;
 constexpr int kTreeNodes = 1024;  // most nodes of a tree
+constexpr int kPer = kChunk / kStatThreads;  // neighbouring tokens of a thread
+static_assert(kPer == 16);
 
 struct Layout {
   int splits;
-  size_t off_stat, off_sum, off_state, off_cnt, total;
+  size_t off_stat, off_sum, off_state, off_cnt, total;  // in the workspace
 };
 __host__ __device__ __forceinline__ Layout layout_of(int num_trees, int total, int vocab) {
   Layout l;
@@ -50,18 +53,91 @@ __host__ __device__ __forceinline__ Layout layout_of(int num_trees, int total, i
 
 // Where a tree's walk ended.
 struct State {
-  double max, sum, c;  // of the last row; c: the residual is max(p - c q, 0)
-  int row, node;       // last row, -1: no token to draw; its node in the tree
-  double pad;
+  double sum, c;  // of the last row; c: the residual is max(p - c q, 0)
+  float max;
+  int row, node;  // last row, -1: no token to draw; its node in the tree
+  int pad[3];
 };
 
-__device__ __forceinline__ double logit(const SampledArgs& a, int row, int t) {
+__device__ __forceinline__ float logit(const SampledArgs& a, int row, int t) {
   const size_t at = (size_t)row * a.vocab + t;
-  if (a.logits_f32) return (double)static_cast<const float*>(a.logits)[at];
-  return (double)__uint_as_float((uint32_t)static_cast<const uint16_t*>(a.logits)[at] << 16);
+  if (a.logits_f32) return static_cast<const float*>(a.logits)[at];
+  return __uint_as_float((uint32_t)static_cast<const uint16_t*>(a.logits)[at] << 16);
 }
 __device__ __forceinline__ double inv_temperature(const SampledArgs& a, int tree) {
   return a.temperature ? 1.0 / (double)a.temperature[tree] : 1.0;
+}
+
+// 16 neighbouring values of a row from t on, in 16-byte loads where every row
+// begins on 16 bytes; `fill` past the end.
+__device__ __forceinline__ bool vectors(const void* p, int elem, int vocab) {
+  return ((reinterpret_cast<uintptr_t>(p) | ((uintptr_t)vocab * elem)) & 15) == 0;
+}
+__device__ __forceinline__ void load16(const float* p, bool vec, int vocab, int t, float fill, float (&x)[kPer]) {
+  if (vec && t + kPer <= vocab) {
+#pragma unroll
+    for (int i = 0; i < kPer; i += 4) {
+      const float4 v = *reinterpret_cast<const float4*>(p + t + i);
+      x[i] = v.x; x[i + 1] = v.y; x[i + 2] = v.z; x[i + 3] = v.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) x[i] = t + i < vocab ? p[t + i] : fill;
+  }
+}
+__device__ __forceinline__ void load16(const uint16_t* p, bool vec, int vocab, int t, float fill, float (&x)[kPer]) {
+  if (vec && t + kPer <= vocab) {
+#pragma unroll
+    for (int i = 0; i < kPer; i += 8) {
+      const uint4 v = *reinterpret_cast<const uint4*>(p + t + i);
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        x[i + 2 * j] = __uint_as_float(w[j] << 16);
+        x[i + 2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) x[i] = t + i < vocab ? __uint_as_float((uint32_t)p[t + i] << 16) : fill;
+  }
+}
+__device__ __forceinline__ void logits16(const SampledArgs& a, int row, int t, float (&x)[kPer]) {
+  const float none = -__builtin_huge_valf();
+  if (a.logits_f32)
+    load16(static_cast<const float*>(a.logits) + (size_t)row * a.vocab, vectors(a.logits, 4, a.vocab), a.vocab, t, none, x);
+  else
+    load16(static_cast<const uint16_t*>(a.logits) + (size_t)row * a.vocab, vectors(a.logits, 2, a.vocab), a.vocab, t, none, x);
+}
+__device__ __forceinline__ void draft16(const SampledArgs& a, int row, int t, float (&x)[kPer]) {
+  load16(a.draft + (size_t)row * a.vocab, vectors(a.draft, 4, a.vocab), a.vocab, t, 0.f, x);
+}
+
+// exp(x) for x <= 0 in 64 bits, given y = x log2(e): 2^n times the Taylor
+// series of 2^f, |f| <= 1/2, to the 12th power (0.3466^13 / 13! = 2e-16). A
+// third of the library function's instructions, which bound the first launch.
+__device__ __forceinline__ double exp2_64(double y) {
+  y = fmax(y, -1100.0);  // 0; keeps -inf out
+  const double n = __builtin_rint(y), f = (y - n) * 0.693147180559945309417232;
+  double p = 1.0 / 479001600.0;
+  p = __builtin_fma(p, f, 1.0 / 39916800.0);
+  p = __builtin_fma(p, f, 1.0 / 3628800.0);
+  p = __builtin_fma(p, f, 1.0 / 362880.0);
+  p = __builtin_fma(p, f, 1.0 / 40320.0);
+  p = __builtin_fma(p, f, 1.0 / 5040.0);
+  p = __builtin_fma(p, f, 1.0 / 720.0);
+  p = __builtin_fma(p, f, 1.0 / 120.0);
+  p = __builtin_fma(p, f, 1.0 / 24.0);
+  p = __builtin_fma(p, f, 1.0 / 6.0);
+  p = __builtin_fma(p, f, 0.5);
+  p = __builtin_fma(p, f, 1.0);
+  p = __builtin_fma(p, f, 1.0);
+  return __builtin_amdgcn_ldexp(p, (int)n);
+}
+constexpr double kLog2e = 1.442695040888963407359925;
+// exp((x - max) / temperature), it2 = log2(e) / temperature
+__device__ __forceinline__ double weight_of(float x, float mx, double it2) {
+  return exp2_64(((double)x - (double)mx) * it2);
 }
 
 __device__ __forceinline__ double shfl_xor_d(double v, int o) {
@@ -69,7 +145,7 @@ __device__ __forceinline__ double shfl_xor_d(double v, int o) {
   const uint32_t lo = __shfl_xor((uint32_t)b, o, 64), hi = __shfl_xor((uint32_t)(b >> 32), o, 64);
   return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
 }
-// Sum (maximum) over the workgroup in a fixed order, in every thread.
+// Sum over the workgroup in a fixed order, in every thread.
 template <int NT>
 __device__ __forceinline__ double block_sum(double v, double* s_red) {
 #pragma unroll
@@ -82,19 +158,6 @@ __device__ __forceinline__ double block_sum(double v, double* s_red) {
   for (int i = 0; i < NT / 64; ++i) r += s_red[i];
   return r;
 }
-template <int NT>
-__device__ __forceinline__ double block_max(double v, double* s_red) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v = fmax(v, shfl_xor_d(v, o));
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) s_red[threadIdx.x >> 6] = v;
-  __syncthreads();
-  double r = s_red[0];
-#pragma unroll
-  for (int i = 1; i < NT / 64; ++i) r = fmax(r, s_red[i]);
-  return r;
-}
-
 // Tree of a row; num_trees where none holds it.
 template <int NT>
 __device__ __forceinline__ int tree_of(const SampledArgs& a, int row, int* s_tree) {
@@ -109,6 +172,7 @@ __device__ __forceinline__ int tree_of(const SampledArgs& a, int row, int* s_tre
 // (max, sum of exp(x - max)) of one chunk of one row.
 __global__ __launch_bounds__(kStatThreads) void sampled_stat_kernel(SampledArgs a) {
   __shared__ double s_red[kStatThreads / 64];
+  __shared__ float s_top[kStatThreads / 64];
   __shared__ int s_tree;
   const int row = blockIdx.y, split = blockIdx.x, tid = threadIdx.x;
   const Layout L = layout_of(a.num_trees, a.total, a.vocab);
@@ -117,46 +181,56 @@ __global__ __launch_bounds__(kStatThreads) void sampled_stat_kernel(SampledArgs 
     for (int t = tid; t < a.num_trees; t += kStatThreads) reinterpret_cast<uint32_t*>(ws + L.off_cnt)[t] = 0;
   const int tree = tree_of<kStatThreads>(a, row, &s_tree);
   if (tree >= a.num_trees) return;
-  const double it = inv_temperature(a, tree);
-  const int t0 = split * kChunk;
-  double x[kChunk / kStatThreads], mx = -__builtin_huge_val();
+  const double it2 = inv_temperature(a, tree) * kLog2e;
+  float x[kPer], top = -__builtin_huge_valf();
+  bool nan = false;
+  logits16(a, row, split * kChunk + tid * kPer, x);
 #pragma unroll
-  for (int i = 0; i < kChunk / kStatThreads; ++i) {
-    const int t = t0 + i * kStatThreads + tid;
-    x[i] = t < a.vocab ? logit(a, row, t) * it : -__builtin_huge_val();
-    mx = fmax(mx, x[i]);
+  for (int i = 0; i < kPer; ++i) {
+    top = fmaxf(top, x[i]);
+    nan = nan || x[i] != x[i];
   }
-  mx = block_max<kStatThreads>(mx, s_red);
-  double sum = 0.0;
-  if (mx > -__builtin_huge_val()) {
 #pragma unroll
-    for (int i = 0; i < kChunk / kStatThreads; ++i) sum += exp(x[i] - mx);
-  } else {
-    // nothing but -inf and NaN: a NaN must still reach the row's sum
+  for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
+  if ((tid & 63) == 0) s_top[tid >> 6] = top;
+  __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kChunk / kStatThreads; ++i) sum += x[i] != x[i] ? x[i] : 0.0;
+  for (int i = 0; i < kStatThreads / 64; ++i) top = fmaxf(top, s_top[i]);
+  // a NaN or +inf must reach the row's sum; nothing but -inf has no weight
+  double sum = nan || top == __builtin_huge_valf() ? __builtin_nan("") : 0.0;
+  if (top > -__builtin_huge_valf() && top < __builtin_huge_valf()) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) sum += weight_of(x[i], top, it2);
   }
   sum = block_sum<kStatThreads>(sum, s_red);
-  if (tid == 0) reinterpret_cast<double2*>(ws + L.off_stat)[(size_t)row * L.splits + split] = make_double2(mx, sum);
+  if (tid == 0) reinterpret_cast<double2*>(ws + L.off_stat)[(size_t)row * L.splits + split] = make_double2(top, sum);
 }
 
-// Maximum and sum of a whole row from its chunks, in every thread.
-template <int NT>
-__device__ __forceinline__ void row_stat(const double2* st, int splits, double* s_red, double& mx, double& sum) {
-  mx = -__builtin_huge_val();
-  for (int i = threadIdx.x; i < splits; i += NT) mx = fmax(mx, st[i].x);
-  mx = block_max<NT>(mx, s_red);
+// Maximum and sum of a whole row from its chunks, by one wave.
+__device__ __forceinline__ void row_stat(const double2* st, int splits, double it2, float& mx, double& sum) {
+  const int lane = threadIdx.x & 63;
+  float m = -__builtin_huge_valf();
+  for (int i = lane; i < splits; i += 64) m = fmaxf(m, (float)st[i].x);
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o, 64));
   double s = 0.0;
-  for (int i = threadIdx.x; i < splits; i += NT) {
+  for (int i = lane; i < splits; i += 64) {
     const double2 v = st[i];
-    s += v.x > -__builtin_huge_val() ? v.y * exp(v.x - mx) : v.y;
+    s += v.x > -__builtin_huge_val() && v.x < __builtin_huge_val() ? v.y * weight_of((float)v.x, m, it2) : v.y;
   }
-  sum = block_sum<NT>(s, s_red);
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) s += shfl_xor_d(s, o);
+  mx = m;
+  sum = s;
 }
 
-// One workgroup walks one tree.
+// One workgroup walks one tree. The rows' maxima and sums (a wave each) and
+// the nodes' probabilities (a thread each) come first, so that the walk itself
+// reads nothing but LDS, save where a drawn draft is rejected and has siblings.
 __global__ __launch_bounds__(kWalkThreads) void sampled_walk_kernel(SampledArgs a) {
   __shared__ int s_parent[kTreeNodes], s_token[kTreeNodes], s_next[kTreeNodes], s_first[kTreeNodes];
+  __shared__ float s_max[kTreeNodes], s_u[kTreeNodes], s_q[kTreeNodes];
+  __shared__ double s_sum[kTreeNodes], s_p[kTreeNodes];
   __shared__ double s_red[kWalkThreads / 64];
   __shared__ int s_bad;
   const int t = blockIdx.x, tid = threadIdx.x;
@@ -166,7 +240,7 @@ __global__ __launch_bounds__(kWalkThreads) void sampled_walk_kernel(SampledArgs 
   const int b0 = a.node_off[t], b1 = a.node_off[t + 1];
   const bool range_ok = b0 >= 0 && b0 <= b1 && b1 <= a.total;
   const int n = range_ok ? b1 - b0 : 0;
-  const double it = inv_temperature(a, t);
+  const double it = inv_temperature(a, t), it2 = it * kLog2e;
   if (tid == 0) s_bad = (n < 1 || n > kTreeNodes || !(it > 0.0 && it < __builtin_huge_val())) ? 1 : 0;
   __syncthreads();
   if (n <= kTreeNodes) {
@@ -174,14 +248,24 @@ __global__ __launch_bounds__(kWalkThreads) void sampled_walk_kernel(SampledArgs 
       const int p = a.parent[b0 + i], tok = a.token[b0 + i];
       s_parent[i] = p;
       s_token[i] = tok;
+      s_u[i] = a.u_accept[b0 + i];
       if (i == 0 ? p != -1 : (p < 0 || p >= i || tok < 0 || tok >= a.vocab)) s_bad = 1;
     }
   }
   __syncthreads();
   bool bad = s_bad;
   int last = 0, len = -1;
-  double mx = 0.0, sum = 0.0, c = 0.0;
+  double c = 0.0;
   if (!bad) {
+    for (int i = tid >> 6; i < n; i += kWalkThreads / 64) {
+      float mx;
+      double sum;
+      row_stat(reinterpret_cast<const double2*>(ws + L.off_stat) + (size_t)(b0 + i) * L.splits, L.splits, it2, mx, sum);
+      if ((tid & 63) == 0) {
+        s_max[i] = mx;
+        s_sum[i] = sum;
+      }
+    }
     for (int i = tid; i < n; i += kWalkThreads) {
       int first = -1, next = -1;
       for (int j = n - 1; j > i; --j) {
@@ -192,13 +276,19 @@ __global__ __launch_bounds__(kWalkThreads) void sampled_walk_kernel(SampledArgs 
       s_next[i] = i == 0 ? -1 : next;
     }
     __syncthreads();
+    for (int i = tid + 1; i < n; i += kWalkThreads) {
+      const int up = s_parent[i], row = b0 + up;
+      s_p[i] = weight_of(logit(a, row, s_token[i]), s_max[up], it2) / s_sum[up];
+      if (a.draft) s_q[i] = a.draft[(size_t)row * a.vocab + s_token[i]];
+    }
+    __syncthreads();
     int node = 0;
     while (node >= 0) {
       ++len;
       last = node;
       const int row = b0 + node;
       if (tid == 0) a.path[b0 + len] = node;
-      row_stat<kWalkThreads>(reinterpret_cast<const double2*>(ws + L.off_stat) + (size_t)row * L.splits, L.splits, s_red, mx, sum);
+      const double sum = s_sum[node];
       if (!(sum > 0.0 && sum < __builtin_huge_val())) {
         bad = true;
         break;
@@ -207,25 +297,29 @@ __global__ __launch_bounds__(kWalkThreads) void sampled_walk_kernel(SampledArgs 
       double left = 1.0;  // n_r
       int chosen = -1;
       for (int k = s_first[node]; k >= 0; k = s_next[k]) {
-        const int tok = s_token[k];
-        const double p = exp(logit(a, row, tok) * it - mx) / sum;
-        const double u = (double)a.u_accept[b0 + k];
+        const double p = s_p[k], u = (double)s_u[k];
         if (a.draft) {
-          const float* q = a.draft + (size_t)row * a.vocab;
-          const double qx = (double)q[tok];
+          const double qx = (double)s_q[k];
           if (u * qx * left < p - c * qx) {
             chosen = k;
             break;
           }
           c += left;
           if (s_next[k] < 0) break;  // the draw sums its residual itself
+          const float mx = s_max[node];
+          const double inv = 1.0 / sum;
           double r = 0.0;
-          for (int i = tid; i < a.vocab; i += kWalkThreads)
-            r += fmax(exp(logit(a, row, i) * it - mx) / sum - c * (double)q[i], 0.0);
+          for (int i = tid * kPer; i < a.vocab; i += kWalkThreads * kPer) {
+            float x[kPer], q[kPer];
+            logits16(a, row, i, x);
+            draft16(a, row, i, q);
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) r += fmax(weight_of(x[j], mx, it2) * inv - c * (double)q[j], 0.0);
+          }
           left = block_sum<kWalkThreads>(r, s_red);
         } else {
           bool again = false;
-          for (int j = s_first[node]; j != k; j = s_next[j]) again = again || s_token[j] == tok;
+          for (int j = s_first[node]; j != k; j = s_next[j]) again = again || s_token[j] == s_token[k];
           if (!again) {
             if (u * left < p) {
               chosen = k;
@@ -249,8 +343,8 @@ __global__ __launch_bounds__(kWalkThreads) void sampled_walk_kernel(SampledArgs 
     a.accept_len[t] = bad ? -1 : len;
     if (bad) a.bonus[t] = -1;
     State s{};
-    s.max = mx;
-    s.sum = sum;
+    s.max = bad ? 0.f : s_max[last];
+    s.sum = bad ? 0.0 : s_sum[last];
     s.c = c;
     s.row = bad ? -1 : b0 + last;
     s.node = last;
@@ -260,9 +354,8 @@ __global__ __launch_bounds__(kWalkThreads) void sampled_walk_kernel(SampledArgs 
 
 // The next token of each tree.
 __global__ __launch_bounds__(kStatThreads) void sampled_draw_kernel(SampledArgs a) {
-  constexpr int kPer = kChunk / kStatThreads;
   __shared__ double s_red[kStatThreads / 64];
-  __shared__ double s_scan[kStatThreads];
+  __shared__ double s_scan[kStatThreads / 64];
   __shared__ uint32_t s_gone[kChunk / 32];
   __shared__ int s_last, s_chunk, s_pick, s_some;
   __shared__ double s_before;
@@ -271,7 +364,7 @@ __global__ __launch_bounds__(kStatThreads) void sampled_draw_kernel(SampledArgs 
   char* ws = static_cast<char*>(a.ws);
   const State st = reinterpret_cast<const State*>(ws + L.off_state)[t];
   if (st.row < 0) return;
-  const double it = inv_temperature(a, t);
+  const double it2 = inv_temperature(a, t) * kLog2e;
   double2* sums = reinterpret_cast<double2*>(ws + L.off_sum) + (size_t)t * L.splits;
   const int b0 = a.node_off[t], n = a.node_off[t + 1] - b0;
 
@@ -287,21 +380,32 @@ __global__ __launch_bounds__(kStatThreads) void sampled_draw_kernel(SampledArgs 
         }
     __syncthreads();
   };
-  // (residual, p) of one token of the chunk
-  auto weight = [&](int chunk, int k) {
-    const int tok = chunk * kChunk + k;
-    if (tok >= a.vocab) return make_double2(0.0, 0.0);
-    const double p = exp(logit(a, st.row, tok) * it - st.max) / st.sum;
-    if (a.draft) return make_double2(fmax(p - st.c * (double)a.draft[(size_t)st.row * a.vocab + tok], 0.0), p);
-    return make_double2((s_gone[k >> 5] >> (k & 31)) & 1 ? 0.0 : p, p);
+  // (residual, p) of the thread's tokens of a chunk; without drafts in units
+  // of the likeliest token's
+  const double inv = a.draft ? 1.0 / st.sum : 1.0;
+  auto weights = [&](int chunk, double (&res)[kPer], double (&all)[kPer]) {
+    const int t0 = chunk * kChunk + tid * kPer;
+    float x[kPer], q[kPer];
+    logits16(a, st.row, t0, x);
+    if (a.draft) draft16(a, st.row, t0, q);
+    const uint32_t gone = s_gone[tid >> 1] >> (tid & 1 ? 16 : 0);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      all[i] = weight_of(x[i], st.max, it2) * inv;
+      res[i] = a.draft ? fmax(all[i] - st.c * (double)q[i], 0.0) : (gone >> i) & 1 ? 0.0 : all[i];
+    }
   };
 
   mark(split);
   double r = 0.0, p = 0.0;
-  for (int i = 0; i < kPer; ++i) {
-    const double2 w = weight(split, i * kStatThreads + tid);
-    r += w.x;
-    p += w.y;
+  {
+    double res[kPer], all[kPer];
+    weights(split, res, all);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      r += res[i];
+      p += all[i];
+    }
   }
   r = block_sum<kStatThreads>(r, s_red);
   p = block_sum<kStatThreads>(p, s_red);
@@ -317,69 +421,89 @@ __global__ __launch_bounds__(kStatThreads) void sampled_draw_kernel(SampledArgs 
   if (!s_last) return;
 
   auto sum_of = [&](int i, bool residual) {
+    if (i >= L.splits) return 0.0;
     return __hip_atomic_load(residual ? &sums[i].x : &sums[i].y, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   };
+  // inclusive running sum over the threads; `whole`: over all of them
+  auto running = [&](double v, double& whole) {
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const uint64_t w = __builtin_bit_cast(uint64_t, v);
+      const uint32_t lo = __shfl_up((uint32_t)w, o, 64), hi = __shfl_up((uint32_t)(w >> 32), o, 64);
+      if ((tid & 63) >= o) v += __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+    }
+    __syncthreads();
+    if ((tid & 63) == 63) s_scan[tid >> 6] = v;
+    __syncthreads();
+    whole = 0.0;
+#pragma unroll
+    for (int w = 0; w < kStatThreads / 64; ++w) {
+      if (w < (tid >> 6)) v += s_scan[w];
+      whole += s_scan[w];
+    }
+    return v;
+  };
+  double total = 0.0;
+  for (int i = tid; i < L.splits; i += kStatThreads) total += sum_of(i, true);
+  total = block_sum<kStatThreads>(total, s_red);
+  const bool residual = total > 0.0;
+  if (!residual) {  // nothing is left but by rounding: p itself
+    total = 0.0;
+    for (int i = tid; i < L.splits; i += kStatThreads) total += sum_of(i, false);
+    total = block_sum<kStatThreads>(total, s_red);
+  }
+  // the first chunk in which the running sum passes the target; else the last
+  // that holds anything, and in it the last token
+  const double target = (double)a.u_bonus[t] * total;
   if (tid == 0) {
-    double total = 0.0;
-    bool residual = true;
-    for (int i = 0; i < L.splits; ++i) total += sum_of(i, true);
-    if (!(total > 0.0)) {  // nothing is left but by rounding: p itself
-      residual = false;
-      total = 0.0;
-      for (int i = 0; i < L.splits; ++i) total += sum_of(i, false);
+    s_chunk = L.splits;
+    s_last = -1;
+  }
+  __syncthreads();
+  double before = 0.0;
+  for (int i0 = 0; i0 < L.splits; i0 += kStatThreads) {
+    const double v = sum_of(i0 + tid, residual);
+    double whole;
+    const double upto = before + running(v, whole);
+    if (v > 0.0) {
+      atomicMax(&s_last, i0 + tid);
+      if (upto > target) atomicMin(&s_chunk, i0 + tid);
     }
-    const double target = (double)a.u_bonus[t] * total;
-    double before = 0.0, keep = 0.0;
-    int chunk = -1, some = 0;
-    for (int i = 0; i < L.splits; ++i) {
-      const double v = sum_of(i, residual);
-      if (v > 0.0) {
-        chunk = i;  // at the end: the last chunk that holds anything
-        keep = before;
-        if (before + v > target) {
-          some = 1;
-          break;
-        }
-      }
-      before += v;
+    __syncthreads();
+    if (s_chunk == i0 + tid) s_before = target - (upto - v);
+    __syncthreads();
+    if (s_chunk < L.splits) break;
+    before += whole;
+  }
+  if (tid == 0) {
+    if (s_chunk == L.splits) {
+      s_chunk = s_last;
+      s_before = __builtin_huge_val();
     }
-    s_chunk = chunk;
-    s_before = some ? target - keep : __builtin_huge_val();
-    s_some = residual ? 1 : 0;
     s_pick = kChunk;
+    s_some = -1;
   }
   __syncthreads();
   const int chunk = s_chunk;
-  const double target = s_before;
-  const bool residual = s_some;
+  const double in_chunk = s_before;
   mark(chunk);
-  double w[kPer], own = 0.0;
+  double res[kPer], all[kPer], own = 0.0, whole;
+  weights(chunk, res, all);
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
-    const double2 v = weight(chunk, tid * kPer + i);
-    w[i] = residual ? v.x : v.y;
-    own += w[i];
+    if (!residual) res[i] = all[i];
+    own += res[i];
   }
-  s_scan[tid] = own;
-  __syncthreads();
-  for (int o = 1; o < kStatThreads; o <<= 1) {
-    const double x = tid >= o ? s_scan[tid - o] : 0.0;
-    __syncthreads();
-    s_scan[tid] += x;
-    __syncthreads();
-  }
-  double cum = tid ? s_scan[tid - 1] : 0.0;
+  double cum = running(own, whole) - own;
   int pick = kChunk, end = -1;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
-    cum += w[i];
-    if (w[i] > 0.0) {
+    cum += res[i];
+    if (res[i] > 0.0) {
       end = tid * kPer + i;
-      if (pick == kChunk && cum > target) pick = end;
+      if (pick == kChunk && cum > in_chunk) pick = end;
     }
   }
-  if (tid == 0) s_some = -1;
-  __syncthreads();
   if (pick < kChunk) atomicMin(&s_pick, pick);
   if (end >= 0) atomicMax(&s_some, end);
   __syncthreads();
