@@ -434,8 +434,8 @@ w12_status w12_kv_attention_workspace(const w12_kv_cache *cache, int32_t num_seq
  * reproducible.
  *   q    [total_rows][q_heads][head_dim] bf16 (w12_kv_append's output).
  *   out  [total_rows][q_heads * head_dim] bf16: the x of the Wo product.
- *   ws   zero-filled workspace of >= w12_kv_attention_workspace bytes, 256-byte
- *        aligned; left zero-filled where it must be.
+ *   ws   workspace of >= w12_kv_attention_workspace bytes, 256-byte aligned,
+ *        content ignored.
  * Device-detected, reported as NaN outputs of the sequence: what w12_kv_append
  * lists (a slot named twice is allowed here), and a page id outside
  * [0, num_pages). A block with a NaN scale reads as NaN.

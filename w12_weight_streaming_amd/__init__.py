@@ -419,6 +419,47 @@ def w12_tree_build(lp: torch.Tensor, tok: torch.Tensor, depth: torch.Tensor, roo
 
 # ------------------------------------------------------------------ KV cache of the verify pass
 
+def _is(t, dtype, ndim: int | None = None) -> bool:
+    """Whether t is what _need asks for (which names what is wrong when not)."""
+    return (isinstance(t, torch.Tensor) and t.dtype == dtype and t.is_cuda and t.is_contiguous()
+            and (ndim is None or t.dim() == ndim))
+
+
+def _check(dev: torch.device, *wanted) -> None:
+    """Checks (name, tensor, dtype, ndim, entries or None) tuples of a call on dev."""
+    for name, t, dtype, ndim, n in wanted:
+        if not _is(t, dtype, ndim):
+            _need(t, dtype, name, ndim)
+        if t.device != dev:
+            raise ValueError(f"{name} must be on {dev} (got {t.device})")
+        if n is not None and t.numel() != n:
+            raise ValueError(f"{name} must have {n} entries (got {t.numel()})")
+
+
+def _at(t: torch.Tensor | None) -> int:
+    return t.data_ptr() if t is not None else 0
+
+
+class _On:
+    """The device of a call made current while its kernels are launched;
+    gives the current stream there."""
+    __slots__ = ("index", "before")
+
+    def __init__(self, dev: torch.device):
+        self.index, self.before = dev.index, None
+
+    def __enter__(self) -> int:
+        current = torch.cuda.current_device()
+        if current != self.index:
+            self.before = current
+            torch.cuda.set_device(self.index)
+        return torch.cuda.current_stream(self.index).cuda_stream
+
+    def __exit__(self, *exc):
+        if self.before is not None:
+            torch.cuda.set_device(self.before)
+
+
 @dataclass
 class KvCache:
     """Device-resident KV cache: the arrays of include/w12.h. pages is
@@ -436,34 +477,25 @@ class KvCache:
     def __post_init__(self):
         if not isinstance(self.pages, torch.Tensor) or self.pages.dtype not in (torch.float8_e4m3fn, torch.int8):
             raise TypeError("pages must be a float8_e4m3fn or int8 tensor")
-        for t, dt, nm, nd in ((self.pages, self.pages.dtype, "pages", 5), (self.scales, torch.float32, "scales", 4),
-                              (self.recent, torch.bfloat16, "recent", 5), (self.page_table, torch.int32, "page_table", 2),
-                              (self.length, torch.int32, "length", 1)):
-            _need(t, dt, nm, nd)
-            if t.device != self.pages.device:
-                raise ValueError("the cache's arrays must be on one GPU")
-        layers, num_pages, kv, two, page = self.pages.shape
-        slots = self.length.numel()
-        if (two != 2 or page % self.head_dim or tuple(self.scales.shape) != (layers, num_pages, kv, 2)
-                or self.recent.shape[:4] != (layers, slots, kv, 2) or self.recent.shape[4] % self.head_dim
-                or self.page_table.shape[0] != slots):
+        pages, scales, recent, table, length = self.pages, self.scales, self.recent, self.page_table, self.length
+        dev, dim = pages.device, self.head_dim
+        _check(dev, ("pages", pages, pages.dtype, 5, None), ("scales", scales, torch.float32, 4, None),
+               ("recent", recent, torch.bfloat16, 5, None), ("page_table", table, torch.int32, 2, None),
+               ("length", length, torch.int32, 1, None))
+        layers, num_pages, kv, two, page = pages.shape
+        slots, blocks = table.shape
+        rows = recent.shape
+        if (two != 2 or dim < 1 or page % dim or scales.shape != pages.shape[:4] or length.shape[0] != slots
+                or rows[:4] != (layers, slots, kv, 2) or rows[4] % dim):
             raise ValueError("the cache's arrays differ in shape")
-        self._desc = W12KvCache(W12_KV_E4M3 if self.pages.dtype == torch.float8_e4m3fn else W12_KV_INT8, layers,
-                                num_pages, kv, page // self.head_dim, self.head_dim, slots,
-                                self.recent.shape[4] // self.head_dim, self.page_table.shape[1],
-                                self.pages.data_ptr(), self.scales.data_ptr(), self.recent.data_ptr(),
-                                self.page_table.data_ptr(), self.length.data_ptr())
+        self.device, self.kv_heads = dev, kv
+        self._desc = W12KvCache(W12_KV_INT8 if pages.dtype == torch.int8 else W12_KV_E4M3, layers, num_pages, kv,
+                                page // dim, dim, slots, rows[4] // dim, blocks, pages.data_ptr(), scales.data_ptr(),
+                                recent.data_ptr(), table.data_ptr(), length.data_ptr())
+        self._ref = ctypes.byref(self._desc)
 
     def desc(self) -> W12KvCache:
         return self._desc
-
-    @property
-    def device(self):
-        return self.pages.device
-
-    @property
-    def kv_heads(self) -> int:
-        return self.pages.shape[2]
 
     def nbytes(self) -> int:
         return sum(t.numel() * t.element_size()
@@ -483,23 +515,15 @@ def kv_cache(layers: int, kv_heads: int, head_dim: int, num_pages: int, slots: i
         torch.zeros(slots, dtype=torch.int32, device=device), head_dim)
 
 
-def _on(dev: torch.device):
-    """The device of a call made current while its kernels are launched."""
-    return torch.cuda.device(dev)
-
-
-def _step(cache: KvCache, row_off, slot, rows: int, **more):
+def _step(cache: KvCache, row_off, slot, rows: int, name: str, more) -> int:
     """Checks the step's arrays; returns the number of sequences."""
-    _need(row_off, torch.int32, "row_off", 1)
-    seqs = row_off.numel() - 1
-    for nm, t, n in (("slot", slot, seqs), *((nm, t, rows) for nm, t in more.items())):
-        if t is not None:
-            _need(t, torch.int32, nm, 1)
-            if t.numel() != n:
-                raise ValueError(f"{nm} must have {n} entries (got {t.numel()})")
-    for t in (row_off, slot, *more.values()):
-        if t is not None and t.device != cache.device:
-            raise ValueError("the step's arrays must be on the cache's GPU")
+    dev = cache.device
+    _check(dev, ("row_off", row_off, torch.int32, 1, None))
+    seqs = row_off.shape[0] - 1
+    if slot is not None:
+        _check(dev, ("slot", slot, torch.int32, 1, seqs))
+    if more is not None:
+        _check(dev, (name, more, torch.int32, 1, rows))
     return seqs
 
 
@@ -511,36 +535,39 @@ def w12_kv_append(cache: KvCache, layer: int, qkv: torch.Tensor, row_off: torch.
     fp32 holds cosines, then sines. Returns q [rows, q_heads, head_dim] bf16."""
     if not isinstance(qkv, torch.Tensor) or qkv.dtype not in (torch.float32, torch.bfloat16):
         raise TypeError("qkv must be a float32 or bfloat16 tensor")
-    _need(qkv, qkv.dtype, "qkv", 2)
-    _need(rope, torch.float32, "rope", 2)
-    rows = qkv.shape[0]
-    if qkv.shape[1] != (q_heads + 2 * cache.kv_heads) * cache.head_dim:
-        raise ValueError(f"qkv has {qkv.shape[1]} columns, {q_heads} + 2 * {cache.kv_heads} heads of "
-                         f"{cache.head_dim} need {(q_heads + 2 * cache.kv_heads) * cache.head_dim}")
-    seqs = _step(cache, row_off, slot, rows, parent=parent)
+    dev, dim, f32 = cache.device, cache.head_dim, qkv.dtype == torch.float32
+    _check(dev, ("qkv", qkv, qkv.dtype, 2, None), ("rope", rope, torch.float32, 2, None))
+    rows, width = qkv.shape
+    if width != (q_heads + 2 * cache.kv_heads) * dim:
+        raise ValueError(f"qkv has {width} columns, {q_heads} + 2 * {cache.kv_heads} heads of "
+                         f"{dim} need {(q_heads + 2 * cache.kv_heads) * dim}")
+    seqs = _step(cache, row_off, slot, rows, "parent", parent)
     if out is None:
-        out = torch.empty(rows, q_heads, cache.head_dim, dtype=torch.bfloat16, device=qkv.device)
-    _need(out, torch.bfloat16, "out")
-    if out.numel() < rows * q_heads * cache.head_dim:
-        raise ValueError("out must hold [rows, q_heads, head_dim]")
-    if any(t.device != cache.device for t in (qkv, rope, out)):
-        raise ValueError("qkv, rope and out must be on the cache's GPU")
-    d = cache.desc()
-    with _on(cache.device):
-        _ok(lib().w12_kv_append(ctypes.byref(d), layer, seqs, _ptr(slot), _ptr(row_off), rows, _ptr(parent), _ptr(qkv),
-                                W12_Y_F32 if qkv.dtype == torch.float32 else W12_Y_BF16, q_heads, _ptr(rope),
-                                rope.shape[0], rope.shape[1], int(interleaved), _ptr(out), _stream(cache.device)),
+        out = torch.empty(rows, q_heads, dim, dtype=torch.bfloat16, device=dev)
+    else:
+        _check(dev, ("out", out, torch.bfloat16, None, None))
+        if out.numel() < rows * q_heads * dim:
+            raise ValueError("out must hold [rows, q_heads, head_dim]")
+    with _On(dev) as stream:
+        _ok(lib().w12_kv_append(cache._ref, layer, seqs, _at(slot), row_off.data_ptr(), rows, _at(parent),
+                                qkv.data_ptr(), W12_Y_F32 if f32 else W12_Y_BF16, q_heads, rope.data_ptr(),
+                                rope.shape[0], rope.shape[1], 1 if interleaved else 0, out.data_ptr(), stream),
             "w12_kv_append")
     return out
 
 
-def _call_workspace(nbytes: int, device: torch.device, tag: str) -> torch.Tensor:
-    """workspace(), but a zero-filled one of its own for a call that is being
-    captured: the graph's replays and eager calls, or two graphs, may overlap
-    in time, and must not share arrival counters."""
-    if torch.cuda.is_current_stream_capturing():
-        return torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=device)
-    return workspace(nbytes, device, tag)
+_kv_ws: dict = {}  # workspace bytes of w12_kv_attention by device and sizes
+
+
+def _attention_workspace_bytes(cache: KvCache, seqs: int, rows: int, q_heads: int) -> int:
+    key = (cache.device.index, cache.head_dim, cache.kv_heads, seqs, rows, q_heads)
+    need = _kv_ws.get(key)
+    if need is None:
+        out = ctypes.c_size_t(0)
+        _ok(lib().w12_kv_attention_workspace(cache._ref, seqs, rows, q_heads, ctypes.byref(out)),
+            "w12_kv_attention_workspace")
+        need = _kv_ws[key] = out.value
+    return need
 
 
 def w12_kv_attention(cache: KvCache, layer: int, q: torch.Tensor, row_off: torch.Tensor,
@@ -548,29 +575,33 @@ def w12_kv_attention(cache: KvCache, layer: int, q: torch.Tensor, row_off: torch
                      out: torch.Tensor | None = None, ws: torch.Tensor | None = None) -> torch.Tensor:
     """Attention of the step's rows q [rows, q_heads, head_dim] bf16 over the
     cache; returns [rows, q_heads * head_dim] bf16. scale defaults to
-    head_dim ** -0.5."""
-    _need(q, torch.bfloat16, "q", 3)
+    head_dim ** -0.5. ws: a workspace of the caller's (its content is
+    ignored); without one the call takes one kept per stream, or, while it is
+    captured, one of its own (replays may overlap in time with other calls)."""
+    dev = cache.device
+    _check(dev, ("q", q, torch.bfloat16, 3, None))
     rows, q_heads, dim = q.shape
     if dim != cache.head_dim:
         raise ValueError(f"q has head_dim {dim}, the cache {cache.head_dim}")
-    seqs = _step(cache, row_off, slot, rows, parent=parent)
+    seqs = _step(cache, row_off, slot, rows, "parent", parent)
     if out is None:
-        out = torch.empty(rows, q_heads * dim, dtype=torch.bfloat16, device=q.device)
-    _need(out, torch.bfloat16, "out")
-    if out.numel() < rows * q_heads * dim:
-        raise ValueError("out must hold [rows, q_heads * head_dim]")
-    if q.device != cache.device or out.device != cache.device:
-        raise ValueError("q and out must be on the cache's GPU")
-    d = cache.desc()
-    need = ctypes.c_size_t(0)
-    with _on(cache.device):
-        _ok(lib().w12_kv_attention_workspace(ctypes.byref(d), seqs, rows, q_heads, ctypes.byref(need)),
-            "w12_kv_attention_workspace")
+        out = torch.empty(rows, q_heads * dim, dtype=torch.bfloat16, device=dev)
+    else:
+        _check(dev, ("out", out, torch.bfloat16, None, None))
+        if out.numel() < rows * q_heads * dim:
+            raise ValueError("out must hold [rows, q_heads * head_dim]")
+    with _On(dev) as stream:
+        need = _attention_workspace_bytes(cache, seqs, rows, q_heads)
         if ws is None:
-            ws = _call_workspace(need.value, cache.device, "kv")
-        _ok(lib().w12_kv_attention(ctypes.byref(d), layer, seqs, _ptr(slot), _ptr(row_off), rows, _ptr(parent), _ptr(q),
-                                   q_heads, dim ** -0.5 if scale is None else scale, _ptr(out), _ptr(ws), ws.numel(),
-                                   _stream(cache.device)), "w12_kv_attention")
+            if torch.cuda.is_current_stream_capturing():
+                ws = torch.empty(need, dtype=torch.uint8, device=dev)
+            else:
+                ws = _ws_cache.get((dev.index, stream, "kv"))
+                if ws is None or ws.numel() < need:
+                    ws = workspace(need, dev, "kv")
+        _ok(lib().w12_kv_attention(cache._ref, layer, seqs, _at(slot), row_off.data_ptr(), rows, _at(parent),
+                                   q.data_ptr(), q_heads, dim ** -0.5 if scale is None else scale, out.data_ptr(),
+                                   ws.data_ptr(), ws.numel() * ws.element_size(), stream), "w12_kv_attention")
     return out
 
 
@@ -580,26 +611,20 @@ def w12_kv_commit(cache: KvCache, row_off: torch.Tensor, accept_len: torch.Tenso
     path; path None: each sequence's first accept_len + 1 rows) in every
     layer. Writes the new lengths into length_out [slots] (the cache's own by
     default) and returns it."""
+    dev = cache.device
     if path is not None:
-        _need(path, torch.int32, "path", 1)
-        rows = path.numel()
+        _check(dev, ("path", path, torch.int32, 1, None))
+        rows = path.shape[0]
     else:
         rows = MAX_ROWS
-    seqs = _step(cache, row_off, slot, rows, path=path)
-    _need(accept_len, torch.int32, "accept_len", 1)
-    if accept_len.numel() != seqs:
-        raise ValueError(f"accept_len must have {seqs} entries (got {accept_len.numel()})")
+    seqs = _step(cache, row_off, slot, rows, "path", None)
     if length_out is None:
         length_out = cache.length
-    _need(length_out, torch.int32, "length_out", 1)
-    if length_out.numel() != cache.length.numel():
-        raise ValueError("length_out must have one entry per slot")
-    if accept_len.device != cache.device or length_out.device != cache.device:
-        raise ValueError("accept_len and length_out must be on the cache's GPU")
-    d = cache.desc()
-    with _on(cache.device):
-        _ok(lib().w12_kv_commit(ctypes.byref(d), seqs, _ptr(slot), _ptr(row_off), rows, _ptr(accept_len), _ptr(path),
-                                _ptr(length_out), _stream(cache.device)), "w12_kv_commit")
+    _check(dev, ("accept_len", accept_len, torch.int32, 1, seqs),
+           ("length_out", length_out, torch.int32, 1, cache.length.shape[0]))
+    with _On(dev) as stream:
+        _ok(lib().w12_kv_commit(cache._ref, seqs, _at(slot), row_off.data_ptr(), rows, accept_len.data_ptr(), _at(path),
+                                length_out.data_ptr(), stream), "w12_kv_commit")
     return length_out
 
 
@@ -612,36 +637,32 @@ def tree_accept_sampled(node_off: torch.Tensor, parent: torch.Tensor, token: tor
     None (chosen drafts). Returns (accept_len, path, bonus) as tree_accept."""
     if not isinstance(logits, torch.Tensor) or logits.dtype not in (torch.float32, torch.bfloat16):
         raise TypeError("logits must be a float32 or bfloat16 tensor")
-    _need(logits, logits.dtype, "logits", 2)
+    dev, i32, f32 = logits.device, torch.int32, torch.float32
+    _check(dev, ("logits", logits, logits.dtype, 2, None), ("node_off", node_off, i32, 1, None))
     total, vocab = logits.shape
-    for t, nm in ((node_off, "node_off"), (parent, "parent"), (token, "token")):
-        _need(t, torch.int32, nm, 1)
-    T = node_off.numel() - 1
-    for t, nm, n in ((u_accept, "u_accept", total), (u_bonus, "u_bonus", T), (temperature, "temperature", T)):
-        if t is not None:
-            _need(t, torch.float32, nm, 1)
-            if t.numel() != n:
-                raise ValueError(f"{nm} must have {n} entries (got {t.numel()})")
+    T = node_off.shape[0] - 1
+    _check(dev, ("parent", parent, i32, 1, total), ("token", token, i32, 1, total), ("u_accept", u_accept, f32, 1, total),
+           ("u_bonus", u_bonus, f32, 1, T))
+    if temperature is not None:
+        _check(dev, ("temperature", temperature, f32, 1, T))
     if draft is not None:
-        _need(draft, torch.float32, "draft", 2)
+        _check(dev, ("draft", draft, f32, 2, None))
         if draft.shape != logits.shape:
             raise ValueError("draft and logits differ in shape")
-    if T < 0 or parent.numel() != total or token.numel() != total:
-        raise ValueError("tree_accept_sampled: inconsistent array sizes")
-    dev = logits.device
-    if any(t is not None and t.device != dev for t in (node_off, parent, token, u_accept, u_bonus, temperature, draft)):
-        raise ValueError("tree_accept_sampled: tensors on different devices")
-    acc = torch.empty(max(T, 0), dtype=torch.int32, device=dev)
-    path = torch.empty(total, dtype=torch.int32, device=dev)
-    bonus = torch.empty(max(T, 0), dtype=torch.int32, device=dev)
-    need = ctypes.c_size_t(0)
-    with _on(dev):
-        _ok(lib().tree_accept_sampled_workspace(T, total, vocab, ctypes.byref(need)), "tree_accept_sampled_workspace")
+    if T < 1:
+        raise ValueError("tree_accept_sampled: no trees")
+    acc = torch.empty(T, dtype=i32, device=dev)
+    path = torch.empty(total, dtype=i32, device=dev)
+    bonus = torch.empty(T, dtype=i32, device=dev)
+    with _On(dev) as stream:
+        L = lib()
         if ws is None:
+            need = ctypes.c_size_t(0)
+            _ok(L.tree_accept_sampled_workspace(T, total, vocab, ctypes.byref(need)), "tree_accept_sampled_workspace")
             ws = torch.empty(need.value, dtype=torch.uint8, device=dev)
-        _ok(lib().tree_accept_sampled(T, _ptr(node_off), total, _ptr(parent), _ptr(token), _ptr(logits),
-                                      W12_Y_F32 if logits.dtype == torch.float32 else W12_Y_BF16, vocab,
-                                      _ptr(temperature), _ptr(draft), _ptr(u_accept), _ptr(u_bonus), _ptr(acc),
-                                      _ptr(path), _ptr(bonus), _ptr(ws), ws.numel(), _stream(dev)),
+        _ok(L.tree_accept_sampled(T, node_off.data_ptr(), total, parent.data_ptr(), token.data_ptr(), logits.data_ptr(),
+                                  W12_Y_F32 if logits.dtype == f32 else W12_Y_BF16, vocab, _at(temperature), _at(draft),
+                                  u_accept.data_ptr(), u_bonus.data_ptr(), acc.data_ptr(), path.data_ptr(),
+                                  bonus.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(), stream),
             "tree_accept_sampled")
     return acc, path, bonus

@@ -225,7 +225,9 @@ __device__ __forceinline__ void gather16(const uint16_t* __restrict__ base, int 
 // sequence's full blocks one after another, then moves what is left to the
 // front; every dest row lies at or before its source and sources ascend, so
 // moving in order, reads before writes within a round, never overwrites a
-// row that is still to be read.
+// row that is still to be read. A block stays in registers between its
+// maximum and its codes: kPer pieces of 16 values a thread.
+template <int kPer>
 __global__ __launch_bounds__(kCommitThreads) void kv_commit_kernel(CommitArgs a) {
   __shared__ int s_src[kStepRows];
   __shared__ int s_bad;
@@ -238,7 +240,6 @@ __global__ __launch_bounds__(kCommitThreads) void kv_commit_kernel(CommitArgs a)
   const int closed = n / page, left = n - closed * page;
   uint16_t* base = a.c.recent + recent_at(a.c, layer, w.v.slot, head, v);
   const int chunks = page * dim / 16;
-  constexpr int kPer = kMaxPage * 256 / 16 / kCommitThreads;  // chunks per thread of the largest block
   for (int b = 0; b < closed; ++b) {
     auto src = [&](int i) {
       const int r = b * page + i;
@@ -283,7 +284,8 @@ __global__ __launch_bounds__(kCommitThreads) void kv_commit_kernel(CommitArgs a)
     }
     const int id = a.c.table[(size_t)w.v.slot * a.c.max_pages + w.v.full + b];
     if (tid == 0) a.c.scales[scale_at(a.c, layer, id, head, v)] = scale;
-    const float div = most >= 0x7F800000u ? 1.0f : scale;
+    // dividing by a power of two is multiplying by its inverse
+    const float div = most >= 0x7F800000u ? 1.0f : scale, inv = a.c.kind == 0 ? 1.0f / div : 0.0f;
     uint8_t* dst = a.c.pages + page_at(a.c, layer, id, head, v);
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
@@ -293,13 +295,15 @@ __global__ __launch_bounds__(kCommitThreads) void kv_commit_kernel(CommitArgs a)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const uint32_t p = x[k][2 * j], q = x[k][2 * j + 1];
-          const float f0 = __uint_as_float(p << 16) / div, f1 = __uint_as_float(p & 0xFFFF0000u) / div;
-          const float f2 = __uint_as_float(q << 16) / div, f3 = __uint_as_float(q & 0xFFFF0000u) / div;
+          const float f0 = __uint_as_float(p << 16), f1 = __uint_as_float(p & 0xFFFF0000u);
+          const float f2 = __uint_as_float(q << 16), f3 = __uint_as_float(q & 0xFFFF0000u);
           if (a.c.kind == 0) {
-            int c = __builtin_amdgcn_cvt_pk_fp8_f32(f0, f1, 0, false);
-            o[j] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(f2, f3, c, true);
+            int c = __builtin_amdgcn_cvt_pk_fp8_f32(f0 * inv, f1 * inv, 0, false);
+            o[j] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(f2 * inv, f3 * inv, c, true);
           } else {
-            auto code = [](float f) { return (uint32_t)(int)fminf(fmaxf(rintf(f), -127.0f), 127.0f) & 0xFFu; };
+            auto code = [div](float f) {
+              return (uint32_t)(int)fminf(fmaxf(rintf(__fdiv_rn(f, div)), -127.0f), 127.0f) & 0xFFu;
+            };
             o[j] = code(f0) | code(f1) << 8 | code(f2) << 16 | code(f3) << 24;
           }
         }
@@ -357,7 +361,16 @@ hipError_t launch_kv_append(const AppendArgs& a, hipStream_t s) {
 }
 
 hipError_t launch_kv_commit(const CommitArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL(kv_commit_kernel, dim3(a.c.layers * a.c.kv_heads * 2, a.st.num_seq), dim3(kCommitThreads), 0, s, a);
+  const dim3 grid(a.c.layers * a.c.kv_heads * 2, a.st.num_seq), block(kCommitThreads);
+  const int pieces = (a.c.page * a.c.dim + kCommitThreads * 16 - 1) / (kCommitThreads * 16);  // 1 .. 8
+  if (pieces <= 1)
+    hipLaunchKernelGGL(kv_commit_kernel<1>, grid, block, 0, s, a);
+  else if (pieces <= 2)
+    hipLaunchKernelGGL(kv_commit_kernel<2>, grid, block, 0, s, a);
+  else if (pieces <= 4)
+    hipLaunchKernelGGL(kv_commit_kernel<4>, grid, block, 0, s, a);
+  else
+    hipLaunchKernelGGL(kv_commit_kernel<8>, grid, block, 0, s, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(kv_commit_len_kernel, dim3(a.st.num_seq), dim3(64), 0, s, a);

@@ -113,31 +113,36 @@ __device__ __forceinline__ void draft16(const SampledArgs& a, int row, int t, fl
   load16(a.draft + (size_t)row * a.vocab, vectors(a.draft, 4, a.vocab), a.vocab, t, 0.f, x);
 }
 
-// exp(x) for x <= 0 in 64 bits, given y = x log2(e): 2^n times the Taylor
-// series of 2^f, |f| <= 1/2, to the 12th power (0.3466^13 / 13! = 2e-16). A
-// third of the library function's instructions, which bound the first launch.
-__device__ __forceinline__ double exp2_64(double y) {
-  y = fmax(y, -1100.0);  // 0; keeps -inf out
-  const double n = __builtin_rint(y), f = (y - n) * 0.693147180559945309417232;
-  double p = 1.0 / 479001600.0;
-  p = __builtin_fma(p, f, 1.0 / 39916800.0);
-  p = __builtin_fma(p, f, 1.0 / 3628800.0);
-  p = __builtin_fma(p, f, 1.0 / 362880.0);
-  p = __builtin_fma(p, f, 1.0 / 40320.0);
-  p = __builtin_fma(p, f, 1.0 / 5040.0);
-  p = __builtin_fma(p, f, 1.0 / 720.0);
-  p = __builtin_fma(p, f, 1.0 / 120.0);
-  p = __builtin_fma(p, f, 1.0 / 24.0);
-  p = __builtin_fma(p, f, 1.0 / 6.0);
-  p = __builtin_fma(p, f, 0.5);
-  p = __builtin_fma(p, f, 1.0);
-  p = __builtin_fma(p, f, 1.0);
-  return __builtin_amdgcn_ldexp(p, (int)n);
-}
 constexpr double kLog2e = 1.442695040888963407359925;
-// exp((x - max) / temperature), it2 = log2(e) / temperature
-__device__ __forceinline__ double weight_of(float x, float mx, double it2) {
-  return exp2_64(((double)x - (double)mx) * it2);
+// exp((x - max) / temperature) in 64 bits, it2 = log2(e) / temperature: 2^y =
+// 2^n 2^f with |f| <= 1/2 for y = (x - max) it2 (0 exactly at the maximum, at
+// any temperature). n comes from adding 1.5 2^52, whose low bits then hold it;
+// 2^f is its Taylor series
+// to the 11th power (0.3466^12 / 12! = 6e-15 relative); 2^n goes straight into
+// the exponent. Below 2^-1000, and for -inf, 0. Plain 64-bit multiply-adds
+// throughout: conversions, ldexp and the library's exp made this twice and
+// three times as slow, and it bounds the first launch.
+__device__ __forceinline__ double weight_of(float x, double mx, double it2) {
+  const double y = ((double)x - mx) * it2;
+  const double t = y + 0x1.8p52;
+  const double f = y - (t - 0x1.8p52);
+  double p = 0x1.e8cac7351bb25p-32;  // ln(2)^k / k!
+  p = __builtin_fma(p, f, 0x1.e4cf5158b8ecap-28);
+  p = __builtin_fma(p, f, 0x1.b5253d395e7c4p-24);
+  p = __builtin_fma(p, f, 0x1.62c0223a5c824p-20);
+  p = __builtin_fma(p, f, 0x1.ffcbfc588b0c7p-17);
+  p = __builtin_fma(p, f, 0x1.430912f86c787p-13);
+  p = __builtin_fma(p, f, 0x1.5d87fe78a6731p-10);
+  p = __builtin_fma(p, f, 0x1.3b2ab6fba4e77p-7);
+  p = __builtin_fma(p, f, 0x1.c6b08d704a0c0p-5);
+  p = __builtin_fma(p, f, 0x1.ebfbdff82c58fp-3);
+  p = __builtin_fma(p, f, 0x1.62e42fefa39efp-1);
+  p = __builtin_fma(p, f, 1.0);
+  const uint64_t b = __builtin_bit_cast(uint64_t, p);
+  const uint32_t n = (uint32_t)__builtin_bit_cast(uint64_t, t);
+  const bool gone = !(y > -1000.0);
+  const uint32_t hi = gone ? 0u : (uint32_t)(b >> 32) + (n << 20), lo = gone ? 0u : (uint32_t)b;
+  return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
 }
 
 __device__ __forceinline__ double shfl_xor_d(double v, int o) {
@@ -197,10 +202,11 @@ __global__ __launch_bounds__(kStatThreads) void sampled_stat_kernel(SampledArgs 
 #pragma unroll
   for (int i = 0; i < kStatThreads / 64; ++i) top = fmaxf(top, s_top[i]);
   // a NaN or +inf must reach the row's sum; nothing but -inf has no weight
+  const double mx = top;
   double sum = nan || top == __builtin_huge_valf() ? __builtin_nan("") : 0.0;
   if (top > -__builtin_huge_valf() && top < __builtin_huge_valf()) {
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) sum += weight_of(x[i], top, it2);
+    for (int i = 0; i < kPer; ++i) sum += weight_of(x[i], mx, it2);
   }
   sum = block_sum<kStatThreads>(sum, s_red);
   if (tid == 0) reinterpret_cast<double2*>(ws + L.off_stat)[(size_t)row * L.splits + split] = make_double2(top, sum);
@@ -306,7 +312,7 @@ __global__ __launch_bounds__(kWalkThreads) void sampled_walk_kernel(SampledArgs 
           }
           c += left;
           if (s_next[k] < 0) break;  // the draw sums its residual itself
-          const float mx = s_max[node];
+          const double mx = s_max[node];
           const double inv = 1.0 / sum;
           double r = 0.0;
           for (int i = tid * kPer; i < a.vocab; i += kWalkThreads * kPer) {
@@ -382,7 +388,7 @@ __global__ __launch_bounds__(kStatThreads) void sampled_draw_kernel(SampledArgs 
   };
   // (residual, p) of the thread's tokens of a chunk; without drafts in units
   // of the likeliest token's
-  const double inv = a.draft ? 1.0 / st.sum : 1.0;
+  const double inv = a.draft ? 1.0 / st.sum : 1.0, mx = st.max;
   auto weights = [&](int chunk, double (&res)[kPer], double (&all)[kPer]) {
     const int t0 = chunk * kChunk + tid * kPer;
     float x[kPer], q[kPer];
@@ -391,7 +397,7 @@ __global__ __launch_bounds__(kStatThreads) void sampled_draw_kernel(SampledArgs 
     const uint32_t gone = s_gone[tid >> 1] >> (tid & 1 ? 16 : 0);
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      all[i] = weight_of(x[i], st.max, it2) * inv;
+      all[i] = weight_of(x[i], mx, it2) * inv;
       res[i] = a.draft ? fmax(all[i] - st.c * (double)q[i], 0.0) : (gone >> i) & 1 ? 0.0 : all[i];
     }
   };
