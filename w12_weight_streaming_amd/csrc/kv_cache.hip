@@ -240,18 +240,26 @@ __global__ __launch_bounds__(kCommitThreads) void kv_commit_kernel(CommitArgs a)
   const int closed = n / page, left = n - closed * page;
   uint16_t* base = a.c.recent + recent_at(a.c, layer, w.v.slot, head, v);
   const int chunks = page * dim / 16;
-  for (int b = 0; b < closed; ++b) {
+  uint32_t x[kPer][8], next[kPer][8];
+  auto fetch = [&](int b, uint32_t (&to)[kPer][8]) __attribute__((always_inline)) {
     auto src = [&](int i) {
       const int r = b * page + i;
       return r < tail ? r : s_src[r - tail];
     };
-    uint32_t x[kPer][8];
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      const int ch = k * kCommitThreads + tid;
+      if (ch < chunks) gather16(base, v, dim, ch, src, to[k]);
+    }
+  };
+  if (closed > 0) fetch(0, x);
+  for (int b = 0; b < closed; ++b) {
+    if (b + 1 < closed) fetch(b + 1, next);  // in flight while this block is quantised
     uint32_t most = 0;  // largest magnitude's bits: ordered as integers, NaN above infinity
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
       const int ch = k * kCommitThreads + tid;
       if (ch < chunks) {
-        gather16(base, v, dim, ch, src, x[k]);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           most = max(most, (x[k][i] << 16) & 0x7FFF0000u);
@@ -310,6 +318,10 @@ __global__ __launch_bounds__(kCommitThreads) void kv_commit_kernel(CommitArgs a)
         *reinterpret_cast<uint4*>(dst + (size_t)ch * 16) = make_uint4(o[0], o[1], o[2], o[3]);
       }
     }
+#pragma unroll
+    for (int k = 0; k < kPer; ++k)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[k][i] = next[k][i];
   }
   // rows that stay recent: logical row closed * page + i to place i, where
   // it does not lie there already

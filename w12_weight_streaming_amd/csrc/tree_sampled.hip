@@ -18,23 +18,24 @@
 // held in 64 bits (at 152064 tokens and 32 bits every hundredth draw would
 // differ; at 64 none in 10^9).
 //
-// Three launches: chunk maxima and sums of every row (bound by reading the
-// logits and by 64-bit arithmetic in equal parts); one workgroup per tree
-// walks from the root, every node's probability looked up beforehand; the
-// next token is drawn from the last row, chunk sums over many workgroups, the
-// last of a tree's to arrive finding the chunk and the token in it.
+// Two or three launches. Every wave takes the maximum and sum of a chunk of
+// 1024 tokens (bound by reading the logits). One workgroup per tree walks from
+// the root, every node's probability looked up beforehand, and, without draft
+// probabilities, draws the next token: the chunks' sums are at hand, those that
+// hold a rejected token are summed again without it. With draft probabilities
+// the residual's chunk sums take another pass over the last row, by many
+// workgroups; a tree's last to arrive finds the token.
 #include "kv_internal.h"
 #include "w12_device.h"
 
 namespace w12 {
 namespace {
 
-constexpr int kChunk = 4096;      // tokens of one workgroup of a row
-constexpr int kStatThreads = 256;
-constexpr int kWalkThreads = 1024;
+constexpr int kChunk = 1024;   // tokens of a wave
+constexpr int kPer = 16;       // neighbouring tokens of a lane
+constexpr int kThreads = 256;  // of the launches over chunks: four chunks a workgroup
+constexpr int kWaves = kThreads / 64;
 constexpr int kTreeNodes = 1024;  // most nodes of a tree
-constexpr int kPer = kChunk / kStatThreads;  // neighbouring tokens of a thread
-static_assert(kPer == 16);
 
 struct Layout {
   int splits;
@@ -114,47 +115,94 @@ __device__ __forceinline__ void draft16(const SampledArgs& a, int row, int t, fl
 }
 
 constexpr double kLog2e = 1.442695040888963407359925;
-// exp((x - max) / temperature) in 64 bits, it2 = log2(e) / temperature: 2^y =
-// 2^n 2^f with |f| <= 1/2 for y = (x - max) it2 (0 exactly at the maximum, at
-// any temperature). n comes from adding 1.5 2^52, whose low bits then hold it;
-// 2^f is its Taylor series
-// to the 11th power (0.3466^12 / 12! = 6e-15 relative); 2^n goes straight into
-// the exponent. Below 2^-1000, and for -inf, 0. Plain 64-bit multiply-adds
-// throughout: conversions, ldexp and the library's exp made this twice and
-// three times as slow, and it bounds the first launch.
-__device__ __forceinline__ double weight_of(float x, double mx, double it2) {
-  const double y = ((double)x - mx) * it2;
-  const double t = y + 0x1.8p52;
-  const double f = y - (t - 0x1.8p52);
-  double p = 0x1.e8cac7351bb25p-32;  // ln(2)^k / k!
-  p = __builtin_fma(p, f, 0x1.e4cf5158b8ecap-28);
-  p = __builtin_fma(p, f, 0x1.b5253d395e7c4p-24);
-  p = __builtin_fma(p, f, 0x1.62c0223a5c824p-20);
-  p = __builtin_fma(p, f, 0x1.ffcbfc588b0c7p-17);
-  p = __builtin_fma(p, f, 0x1.430912f86c787p-13);
-  p = __builtin_fma(p, f, 0x1.5d87fe78a6731p-10);
-  p = __builtin_fma(p, f, 0x1.3b2ab6fba4e77p-7);
-  p = __builtin_fma(p, f, 0x1.c6b08d704a0c0p-5);
-  p = __builtin_fma(p, f, 0x1.ebfbdff82c58fp-3);
-  p = __builtin_fma(p, f, 0x1.62e42fefa39efp-1);
-  p = __builtin_fma(p, f, 1.0);
-  const uint64_t b = __builtin_bit_cast(uint64_t, p);
-  const uint32_t n = (uint32_t)__builtin_bit_cast(uint64_t, t);
-  const bool gone = !(y > -1000.0);
-  const uint32_t hi = gone ? 0u : (uint32_t)(b >> 32) + (n << 20), lo = gone ? 0u : (uint32_t)b;
-  return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+// exp((x - max) / temperature) in 64 bits: 2^(y / 32) = 2^(n / 32) 2^(f / 32)
+// with |f| <= 1/2 for y = 32 (x - max) it2, it2 = log2(e) / temperature (0
+// exactly at the maximum, at any temperature). n comes from adding 1.5 2^52,
+// whose low bits then hold it: 2^(n mod 32 / 32) from a table in LDS, the rest
+// of n straight into the exponent. 2^(f / 32) is its Taylor series to the 5th
+// power (0.0108^6 / 720 = 2e-15 relative). Below 2^-1000, and for -inf, 0.
+// 64-bit operations run at half rate and bound the first launch: 192 rows of
+// 152064 tokens take 52 us with the library's exp, 33 with a series to the
+// 11th power and no table.
+struct Weigher {
+  const double* table;  // LDS, 32 entries
+  double mx, it32;
+  float least;  // logits at or below it weigh nothing
+  __device__ __forceinline__ Weigher(const double* t, float top, double it2) : table(t), mx(top), it32(32.0 * it2) {
+    least = (float)(mx - 1000.0 / it2);
+  }
+  __device__ __forceinline__ double operator()(float x) const {
+    const double y = ((double)x - mx) * it32;
+    const double t = y + 0x1.8p52;
+    const double f = y - (t - 0x1.8p52);
+    double p = 0x1.5d87fe78a6731p-35;  // (ln(2) / 32)^k / k!
+    p = __builtin_fma(p, f, 0x1.3b2ab6fba4e77p-27);
+    p = __builtin_fma(p, f, 0x1.c6b08d704a0c0p-20);
+    p = __builtin_fma(p, f, 0x1.ebfbdff82c58fp-13);
+    p = __builtin_fma(p, f, 0x1.62e42fefa39efp-6);
+    p = __builtin_fma(p, f, 1.0);
+    const int32_t n = (int32_t)__builtin_bit_cast(uint64_t, t);
+    p *= table[n & 31];
+    const uint64_t b = __builtin_bit_cast(uint64_t, p);
+    const bool some = x > least;
+    const uint32_t hi = some ? (uint32_t)(b >> 32) + ((uint32_t)(n >> 5) << 20) : 0u, lo = some ? (uint32_t)b : 0u;
+    return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+  }
+};
+__device__ const double kPowers[32] = {
+    0x1.0000000000000p+0, 0x1.059b0d3158574p+0, 0x1.0b5586cf9890fp+0, 0x1.11301d0125b51p+0,
+    0x1.172b83c7d517bp+0, 0x1.1d4873168b9aap+0, 0x1.2387a6e756238p+0, 0x1.29e9df51fdee1p+0,
+    0x1.306fe0a31b715p+0, 0x1.371a7373aa9cbp+0, 0x1.3dea64c123422p+0, 0x1.44e086061892dp+0,
+    0x1.4bfdad5362a27p+0, 0x1.5342b569d4f82p+0, 0x1.5ab07dd485429p+0, 0x1.6247eb03a5585p+0,
+    0x1.6a09e667f3bcdp+0, 0x1.71f75e8ec5f74p+0, 0x1.7a11473eb0187p+0, 0x1.82589994cce13p+0,
+    0x1.8ace5422aa0dbp+0, 0x1.93737b0cdc5e5p+0, 0x1.9c49182a3f090p+0, 0x1.a5503b23e255dp+0,
+    0x1.ae89f995ad3adp+0, 0x1.b7f76f2fb5e47p+0, 0x1.c199bdd85529cp+0, 0x1.cb720dcef9069p+0,
+    0x1.d5818dcfba487p+0, 0x1.dfc97337b9b5fp+0, 0x1.ea4afa2a490dap+0, 0x1.f50765b6e4540p+0,
+};
+// The table in LDS; the caller synchronises before its first use.
+__device__ __forceinline__ void load_powers(double* s_pow) {
+  if (threadIdx.x < 32) s_pow[threadIdx.x] = kPowers[threadIdx.x];
 }
 
-__device__ __forceinline__ double shfl_xor_d(double v, int o) {
+// A lane's value from 1, 2, 4 or 8 lanes before it in its row of 16 (around).
+template <int N>
+__device__ __forceinline__ uint32_t from_row(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x120 + N, 0xF, 0xF, false);
+}
+template <int N>
+__device__ __forceinline__ double from_row(double v) {
   const uint64_t b = __builtin_bit_cast(uint64_t, v);
-  const uint32_t lo = __shfl_xor((uint32_t)b, o, 64), hi = __shfl_xor((uint32_t)(b >> 32), o, 64);
+  const uint32_t lo = from_row<N>((uint32_t)b), hi = from_row<N>((uint32_t)(b >> 32));
   return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
 }
+__device__ __forceinline__ double lane_of(double v, int lane) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)b, lane), hi = __builtin_amdgcn_readlane((uint32_t)(b >> 32), lane);
+  return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+// Sum (maximum) over the wave in a fixed order, the same in every lane: rows
+// of 16 by lane moves, then the four rows' first lanes.
+__device__ __forceinline__ double wave_sum(double v) {
+  v += from_row<8>(v);
+  v += from_row<4>(v);
+  v += from_row<2>(v);
+  v += from_row<1>(v);
+  return (lane_of(v, 0) + lane_of(v, 16)) + (lane_of(v, 32) + lane_of(v, 48));
+}
+__device__ __forceinline__ float wave_max(float v) {
+  auto step = [](float x, uint32_t y) { return fmaxf(x, __uint_as_float(y)); };
+  v = step(v, from_row<8>(__float_as_uint(v)));
+  v = step(v, from_row<4>(__float_as_uint(v)));
+  v = step(v, from_row<2>(__float_as_uint(v)));
+  v = step(v, from_row<1>(__float_as_uint(v)));
+  auto at = [v](int lane) { return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), lane)); };
+  return fmaxf(fmaxf(at(0), at(16)), fmaxf(at(32), at(48)));
+}
+
 // Sum over the workgroup in a fixed order, in every thread.
 template <int NT>
 __device__ __forceinline__ double block_sum(double v, double* s_red) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v += shfl_xor_d(v, o);
+  v = wave_sum(v);
   __syncthreads();
   if ((threadIdx.x & 63) == 0) s_red[threadIdx.x >> 6] = v;
   __syncthreads();
@@ -163,82 +211,172 @@ __device__ __forceinline__ double block_sum(double v, double* s_red) {
   for (int i = 0; i < NT / 64; ++i) r += s_red[i];
   return r;
 }
-// Tree of a row; num_trees where none holds it.
+// Inclusive running sum over the workgroup's threads; `whole`: over all.
 template <int NT>
-__device__ __forceinline__ int tree_of(const SampledArgs& a, int row, int* s_tree) {
-  if (threadIdx.x == 0) *s_tree = a.num_trees;
+__device__ __forceinline__ double running_sum(double v, double* s_scan, double& whole) {
+  const int tid = threadIdx.x;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const uint64_t w = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = __shfl_up((uint32_t)w, o, 64), hi = __shfl_up((uint32_t)(w >> 32), o, 64);
+    if ((tid & 63) >= o) v += __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+  }
   __syncthreads();
-  for (int t = threadIdx.x; t < a.num_trees; t += NT)
-    if (row >= a.node_off[t] && row < a.node_off[t + 1]) atomicMin(s_tree, t);
+  if ((tid & 63) == 63) s_scan[tid >> 6] = v;
   __syncthreads();
-  return *s_tree;
+  whole = 0.0;
+#pragma unroll
+  for (int w = 0; w < NT / 64; ++w) {
+    if (w < (tid >> 6)) v += s_scan[w];
+    whole += s_scan[w];
+  }
+  return v;
 }
 
-// (max, sum of exp(x - max)) of one chunk of one row.
-__global__ __launch_bounds__(kStatThreads) void sampled_stat_kernel(SampledArgs a) {
-  __shared__ double s_red[kStatThreads / 64];
-  __shared__ float s_top[kStatThreads / 64];
-  __shared__ int s_tree;
-  const int row = blockIdx.y, split = blockIdx.x, tid = threadIdx.x;
-  const Layout L = layout_of(a.num_trees, a.total, a.vocab);
-  char* ws = static_cast<char*>(a.ws);
-  if (row == 0 && split == 0)
-    for (int t = tid; t < a.num_trees; t += kStatThreads) reinterpret_cast<uint32_t*>(ws + L.off_cnt)[t] = 0;
-  const int tree = tree_of<kStatThreads>(a, row, &s_tree);
-  if (tree >= a.num_trees) return;
-  const double it2 = inv_temperature(a, tree) * kLog2e;
-  float x[kPer], top = -__builtin_huge_valf();
-  bool nan = false;
-  logits16(a, row, split * kChunk + tid * kPer, x);
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    top = fmaxf(top, x[i]);
-    nan = nan || x[i] != x[i];
+// The first of `splits` chunks, value(i) each, at which the running sum passes
+// `target`, and what of the target is left in it; else the last chunk that
+// holds anything, with an infinite rest.
+struct Found {
+  int chunk;
+  double rest;
+};
+template <int NT, typename F>
+__device__ __forceinline__ Found find_chunk(F value, int splits, double target, double* s_scan, int* s_int, double* s_rest) {
+  const int tid = threadIdx.x;
+  if (tid == 0) {
+    s_int[0] = splits;
+    s_int[1] = -1;
+    *s_rest = __builtin_huge_val();
   }
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
-  if ((tid & 63) == 0) s_top[tid >> 6] = top;
   __syncthreads();
-#pragma unroll
-  for (int i = 0; i < kStatThreads / 64; ++i) top = fmaxf(top, s_top[i]);
-  // a NaN or +inf must reach the row's sum; nothing but -inf has no weight
-  const double mx = top;
-  double sum = nan || top == __builtin_huge_valf() ? __builtin_nan("") : 0.0;
-  if (top > -__builtin_huge_valf() && top < __builtin_huge_valf()) {
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) sum += weight_of(x[i], mx, it2);
+  double before = 0.0;
+  for (int i0 = 0; i0 < splits; i0 += NT) {
+    const double v = i0 + tid < splits ? value(i0 + tid) : 0.0;
+    double whole;
+    const double upto = before + running_sum<NT>(v, s_scan, whole);
+    if (v > 0.0) {
+      atomicMax(&s_int[1], i0 + tid);
+      if (upto > target) atomicMin(&s_int[0], i0 + tid);
+    }
+    __syncthreads();
+    if (s_int[0] == i0 + tid && s_int[0] < splits) *s_rest = target - (upto - v);
+    __syncthreads();
+    if (s_int[0] < splits) break;
+    before += whole;
   }
-  sum = block_sum<kStatThreads>(sum, s_red);
-  if (tid == 0) reinterpret_cast<double2*>(ws + L.off_stat)[(size_t)row * L.splits + split] = make_double2(top, sum);
+  Found f;
+  f.chunk = max(0, s_int[0] < splits ? s_int[0] : s_int[1]);
+  f.rest = *s_rest;
+  return f;
+}
+// The first of N tokens a thread (weights w, in order over the threads) at
+// which the running sum passes `rest`; else the last with any weight.
+template <int NT, int N>
+__device__ __forceinline__ int find_token(const double (&w)[N], double rest, double* s_scan, int* s_int) {
+  const int tid = threadIdx.x;
+  double own = 0.0, whole;
+#pragma unroll
+  for (int i = 0; i < N; ++i) own += w[i];
+  __syncthreads();
+  if (tid == 0) {
+    s_int[0] = NT * N;
+    s_int[1] = -1;
+  }
+  double cum = running_sum<NT>(own, s_scan, whole) - own;
+  int pick = NT * N, end = -1;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    cum += w[i];
+    if (w[i] > 0.0) {
+      end = tid * N + i;
+      if (pick == NT * N && cum > rest) pick = end;
+    }
+  }
+  if (pick < NT * N) atomicMin(&s_int[0], pick);
+  if (end >= 0) atomicMax(&s_int[1], end);
+  __syncthreads();
+  return s_int[0] < NT * N ? s_int[0] : s_int[1];
+}
+
+// (max, sum of exp(x - max)) of chunks of a row: `each` neighbouring ones a
+// wave, the next one's logits on their way while one is summed.
+__global__ __launch_bounds__(kThreads) void sampled_stat_kernel(SampledArgs a, int each) {
+  const int row = blockIdx.y, lane = threadIdx.x & 63;
+  const Layout L = layout_of(a.num_trees, a.total, a.vocab);
+  const int first = (blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6)) * each;
+  const int end = min(first + each, L.splits);
+  char* ws = static_cast<char*>(a.ws);
+  if (row == 0 && blockIdx.x == 0)
+    for (int t = threadIdx.x; t < a.num_trees; t += kThreads) reinterpret_cast<uint32_t*>(ws + L.off_cnt)[t] = 0;
+  __shared__ double s_pow[32];
+  load_powers(s_pow);
+  float x[kPer], next[kPer];
+  if (first < end) logits16(a, row, first * kChunk + lane * kPer, x);
+  __syncthreads();
+  if (first >= end) return;
+  int tree = -1;  // the first that holds the row
+  for (int t = 0; t < a.num_trees && tree < 0; t += 64) {
+    const bool in = t + lane < a.num_trees && row >= a.node_off[t + lane] && row < a.node_off[t + lane + 1];
+    const uint64_t hit = __ballot(in);
+    if (hit) tree = t + __builtin_ctzll(hit);
+  }
+  if (tree < 0) return;
+  const double it2 = inv_temperature(a, tree) * kLog2e;
+  for (int split = first; split < end; ++split) {
+    if (split + 1 < end) logits16(a, row, (split + 1) * kChunk + lane * kPer, next);
+    float top = -__builtin_huge_valf();
+    bool nan = false;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      top = fmaxf(top, x[i]);
+      nan = nan || x[i] != x[i];
+    }
+    top = wave_max(top);
+    // a NaN or +inf must reach the row's sum; nothing but -inf has no weight
+    double sum = nan || top == __builtin_huge_valf() ? __builtin_nan("") : 0.0;
+    if (top > -__builtin_huge_valf() && top < __builtin_huge_valf()) {
+      const Weigher weigh(s_pow, top, it2);
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) sum += weigh(x[i]);
+    }
+    sum = wave_sum(sum);
+    if (lane == 0) reinterpret_cast<double2*>(ws + L.off_stat)[(size_t)row * L.splits + split] = make_double2(top, sum);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) x[i] = next[i];
+  }
 }
 
 // Maximum and sum of a whole row from its chunks, by one wave.
-__device__ __forceinline__ void row_stat(const double2* st, int splits, double it2, float& mx, double& sum) {
+__device__ __forceinline__ void row_stat(const double2* st, int splits, const double* s_pow, double it2, float& mx, double& sum) {
   const int lane = threadIdx.x & 63;
   float m = -__builtin_huge_valf();
   for (int i = lane; i < splits; i += 64) m = fmaxf(m, (float)st[i].x);
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o, 64));
+  m = wave_max(m);
   double s = 0.0;
+  const Weigher weigh(s_pow, m, it2);
   for (int i = lane; i < splits; i += 64) {
     const double2 v = st[i];
-    s += v.x > -__builtin_huge_val() && v.x < __builtin_huge_val() ? v.y * weight_of((float)v.x, m, it2) : v.y;
+    s += v.x > -__builtin_huge_val() && v.x < __builtin_huge_val() ? v.y * weigh((float)v.x) : v.y;
   }
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) s += shfl_xor_d(s, o);
   mx = m;
-  sum = s;
+  sum = wave_sum(s);
 }
 
 // One workgroup walks one tree. The rows' maxima and sums (a wave each) and
 // the nodes' probabilities (a thread each) come first, so that the walk itself
-// reads nothing but LDS, save where a drawn draft is rejected and has siblings.
-__global__ __launch_bounds__(kWalkThreads) void sampled_walk_kernel(SampledArgs a) {
+// reads nothing but LDS, save where a drawn draft is rejected and has siblings
+// (a pass over the row: these trees get 1024 threads, the others 256).
+template <int NT>
+__global__ __launch_bounds__(NT) void sampled_walk_kernel(SampledArgs a) {
+  constexpr int kWalkThreads = NT;
+  __shared__ double s_pow[32];
+  load_powers(s_pow);
   __shared__ int s_parent[kTreeNodes], s_token[kTreeNodes], s_next[kTreeNodes], s_first[kTreeNodes];
   __shared__ float s_max[kTreeNodes], s_u[kTreeNodes], s_q[kTreeNodes];
   __shared__ double s_sum[kTreeNodes], s_p[kTreeNodes];
-  __shared__ double s_red[kWalkThreads / 64];
-  __shared__ int s_bad;
+  __shared__ double s_red[kWalkThreads / 64], s_fix[kTreeNodes], s_rest;
+  __shared__ uint32_t s_gone[kWalkThreads / 64][kChunk / 32];
+  __shared__ int s_bad, s_kids, s_int[2];
   const int t = blockIdx.x, tid = threadIdx.x;
   const Layout L = layout_of(a.num_trees, a.total, a.vocab);
   char* ws = static_cast<char*>(a.ws);
@@ -266,7 +404,7 @@ __global__ __launch_bounds__(kWalkThreads) void sampled_walk_kernel(SampledArgs 
     for (int i = tid >> 6; i < n; i += kWalkThreads / 64) {
       float mx;
       double sum;
-      row_stat(reinterpret_cast<const double2*>(ws + L.off_stat) + (size_t)(b0 + i) * L.splits, L.splits, it2, mx, sum);
+      row_stat(reinterpret_cast<const double2*>(ws + L.off_stat) + (size_t)(b0 + i) * L.splits, L.splits, s_pow, it2, mx, sum);
       if ((tid & 63) == 0) {
         s_max[i] = mx;
         s_sum[i] = sum;
@@ -284,7 +422,7 @@ __global__ __launch_bounds__(kWalkThreads) void sampled_walk_kernel(SampledArgs 
     __syncthreads();
     for (int i = tid + 1; i < n; i += kWalkThreads) {
       const int up = s_parent[i], row = b0 + up;
-      s_p[i] = weight_of(logit(a, row, s_token[i]), s_max[up], it2) / s_sum[up];
+      s_p[i] = Weigher(s_pow, s_max[up], it2)(logit(a, row, s_token[i])) / s_sum[up];
       if (a.draft) s_q[i] = a.draft[(size_t)row * a.vocab + s_token[i]];
     }
     __syncthreads();
@@ -312,7 +450,7 @@ __global__ __launch_bounds__(kWalkThreads) void sampled_walk_kernel(SampledArgs 
           }
           c += left;
           if (s_next[k] < 0) break;  // the draw sums its residual itself
-          const double mx = s_max[node];
+          const Weigher weigh(s_pow, s_max[node], it2);
           const double inv = 1.0 / sum;
           double r = 0.0;
           for (int i = tid * kPer; i < a.vocab; i += kWalkThreads * kPer) {
@@ -320,7 +458,7 @@ __global__ __launch_bounds__(kWalkThreads) void sampled_walk_kernel(SampledArgs 
             logits16(a, row, i, x);
             draft16(a, row, i, q);
 #pragma unroll
-            for (int j = 0; j < kPer; ++j) r += fmax(weight_of(x[j], mx, it2) * inv - c * (double)q[j], 0.0);
+            for (int j = 0; j < kPer; ++j) r += fmax(weigh(x[j]) * inv - c * (double)q[j], 0.0);
           }
           left = block_sum<kWalkThreads>(r, s_red);
         } else {
@@ -348,172 +486,159 @@ __global__ __launch_bounds__(kWalkThreads) void sampled_walk_kernel(SampledArgs 
   if (tid == 0) {
     a.accept_len[t] = bad ? -1 : len;
     if (bad) a.bonus[t] = -1;
-    State s{};
-    s.max = bad ? 0.f : s_max[last];
-    s.sum = bad ? 0.0 : s_sum[last];
-    s.c = c;
-    s.row = bad ? -1 : b0 + last;
-    s.node = last;
-    *state = s;
+    if (a.draft) {
+      State s{};
+      s.max = bad ? 0.f : s_max[last];
+      s.sum = bad ? 0.0 : s_sum[last];
+      s.c = c;
+      s.row = bad ? -1 : b0 + last;
+      s.node = last;
+      *state = s;
+    }
+    s_kids = 0;
   }
+  if (bad || a.draft) return;
+
+  // The next token, of the last row without its children's tokens.
+  const int row = b0 + last;
+  const Weigher weigh(s_pow, s_max[last], it2);
+  const double2* st = reinterpret_cast<const double2*>(ws + L.off_stat) + (size_t)row * L.splits;
+  int* s_list = s_next;  // the children, in no order (the walk is done)
+  __syncthreads();
+  for (int i = tid + 1; i < n; i += kWalkThreads)
+    if (s_parent[i] == last) s_list[atomicAdd(&s_kids, 1)] = s_token[i];
+  __syncthreads();
+  const int kids = s_kids, wave = tid >> 6, lane = tid & 63;
+  auto mark = [&](uint32_t* gone, int chunk, int first, int step) {
+    for (int k = first; k < kids; k += step) {
+      const int j = s_list[k] - chunk * kChunk;
+      if (j >= 0 && j < kChunk) atomicOr(&gone[j >> 5], 1u << (j & 31));
+    }
+  };
+  // chunks with a child's token, summed anew by a wave each
+  for (int k = wave; k < kids; k += kWalkThreads / 64) {
+    const int chunk = s_list[k] / kChunk;
+    uint32_t* gone = s_gone[wave];
+    if (lane < kChunk / 32) gone[lane] = 0;
+    wave_lds_sync();
+    mark(gone, chunk, lane, 64);
+    wave_lds_sync();
+    float x[kPer];
+    logits16(a, row, chunk * kChunk + lane * kPer, x);
+    const uint32_t out = gone[lane >> 1] >> (lane & 1 ? 16 : 0);
+    double r = 0.0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) r += (out >> i) & 1 ? 0.0 : weigh(x[i]);
+    r = wave_sum(r);
+    if (lane == 0) s_fix[k] = r;
+    wave_lds_sync();
+  }
+  __syncthreads();
+  bool taken = true;  // the children's tokens are out (unless nothing else is left)
+  auto chunk_sum = [&](int i) {
+    const double2 v = st[i];
+    double r = v.x > -__builtin_huge_val() ? v.y * weigh((float)v.x) : 0.0;
+    if (taken)
+      for (int k = 0; k < kids; ++k)
+        if (s_list[k] / kChunk == i) r = s_fix[k];
+    return r;
+  };
+  double total = 0.0;
+  for (int i = tid; i < L.splits; i += kWalkThreads) total += chunk_sum(i);
+  total = block_sum<kWalkThreads>(total, s_red);
+  if (!(total > 0.0)) {  // by rounding only: p itself
+    taken = false;
+    total = 0.0;
+    for (int i = tid; i < L.splits; i += kWalkThreads) total += chunk_sum(i);
+    total = block_sum<kWalkThreads>(total, s_red);
+  }
+  const Found f = find_chunk<kWalkThreads>(chunk_sum, L.splits, (double)a.u_bonus[t] * total, s_red, s_int, &s_rest);
+  if (tid < kChunk / 32) s_gone[0][tid] = 0;
+  __syncthreads();
+  if (taken) mark(s_gone[0], f.chunk, tid, kWalkThreads);
+  __syncthreads();
+  constexpr int N = kChunk / NT;
+  double w[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int j = tid * N + i, tok = f.chunk * kChunk + j;
+    w[i] = tok < a.vocab && !((s_gone[0][j >> 5] >> (j & 31)) & 1) ? weigh(logit(a, row, tok)) : 0.0;
+  }
+  const int pick = find_token<NT>(w, f.rest, s_red, s_int);
+  if (tid == 0) a.bonus[t] = f.chunk * kChunk + pick;
 }
 
-// The next token of each tree.
-__global__ __launch_bounds__(kStatThreads) void sampled_draw_kernel(SampledArgs a) {
-  __shared__ double s_red[kStatThreads / 64];
-  __shared__ double s_scan[kStatThreads / 64];
-  __shared__ uint32_t s_gone[kChunk / 32];
-  __shared__ int s_last, s_chunk, s_pick, s_some;
-  __shared__ double s_before;
-  const int t = blockIdx.y, split = blockIdx.x, tid = threadIdx.x;
+// The next token of each tree whose drafts were drawn: from the last row's
+// max(p - c q, 0), or from p where nothing of that is left (by rounding).
+__global__ __launch_bounds__(kThreads) void sampled_draw_kernel(SampledArgs a) {
+  __shared__ double s_red[kWaves], s_rest, s_pow[32];
+  __shared__ int s_last, s_int[2];
+  const int t = blockIdx.y, tid = threadIdx.x, lane = tid & 63;
+  const int split = blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane(tid >> 6);
   const Layout L = layout_of(a.num_trees, a.total, a.vocab);
   char* ws = static_cast<char*>(a.ws);
   const State st = reinterpret_cast<const State*>(ws + L.off_state)[t];
   if (st.row < 0) return;
-  const double it2 = inv_temperature(a, t) * kLog2e;
+  const double it2 = inv_temperature(a, t) * kLog2e, inv = 1.0 / st.sum;
+  load_powers(s_pow);
+  __syncthreads();
+  const Weigher weigh(s_pow, st.max, it2);
   double2* sums = reinterpret_cast<double2*>(ws + L.off_sum) + (size_t)t * L.splits;
-  const int b0 = a.node_off[t], n = a.node_off[t + 1] - b0;
-
-  // bits of the chunk's tokens that rejections took out
-  auto mark = [&](int chunk) {
-    for (int i = tid; i < kChunk / 32; i += kStatThreads) s_gone[i] = 0;
-    __syncthreads();
-    if (!a.draft)
-      for (int i = tid; i < n; i += kStatThreads)
-        if (i > 0 && a.parent[b0 + i] == st.node) {
-          const int k = a.token[b0 + i] - chunk * kChunk;
-          if (k >= 0 && k < kChunk) atomicOr(&s_gone[k >> 5], 1u << (k & 31));
-        }
-    __syncthreads();
-  };
-  // (residual, p) of the thread's tokens of a chunk; without drafts in units
-  // of the likeliest token's
-  const double inv = a.draft ? 1.0 / st.sum : 1.0, mx = st.max;
-  auto weights = [&](int chunk, double (&res)[kPer], double (&all)[kPer]) {
-    const int t0 = chunk * kChunk + tid * kPer;
+  if (split < L.splits) {
     float x[kPer], q[kPer];
-    logits16(a, st.row, t0, x);
-    if (a.draft) draft16(a, st.row, t0, q);
-    const uint32_t gone = s_gone[tid >> 1] >> (tid & 1 ? 16 : 0);
+    logits16(a, st.row, split * kChunk + lane * kPer, x);
+    draft16(a, st.row, split * kChunk + lane * kPer, q);
+    double r = 0.0, p = 0.0;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      all[i] = weight_of(x[i], mx, it2) * inv;
-      res[i] = a.draft ? fmax(all[i] - st.c * (double)q[i], 0.0) : (gone >> i) & 1 ? 0.0 : all[i];
+      const double w = weigh(x[i]) * inv;
+      p += w;
+      r += fmax(w - st.c * (double)q[i], 0.0);
     }
-  };
-
-  mark(split);
-  double r = 0.0, p = 0.0;
-  {
-    double res[kPer], all[kPer];
-    weights(split, res, all);
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      r += res[i];
-      p += all[i];
+    r = wave_sum(r);
+    p = wave_sum(p);
+    if (lane == 0) {
+      __hip_atomic_store(&sums[split].x, r, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      __hip_atomic_store(&sums[split].y, p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
   }
-  r = block_sum<kStatThreads>(r, s_red);
-  p = block_sum<kStatThreads>(p, s_red);
-  if (tid == 0) {
-    __hip_atomic_store(&sums[split].x, r, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    __hip_atomic_store(&sums[split].y, p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    __atomic_signal_fence(__ATOMIC_SEQ_CST);
-    __builtin_amdgcn_s_waitcnt(0);
-    __atomic_signal_fence(__ATOMIC_SEQ_CST);
-    s_last = atomicAdd(reinterpret_cast<uint32_t*>(ws + L.off_cnt) + t, 1u) == (uint32_t)(L.splits - 1) ? 1 : 0;
-  }
+  // hand-off without a device-scope fence (it would write back the whole L2):
+  // the sums went through to the coherent level; wait for them, then count
+  __atomic_signal_fence(__ATOMIC_SEQ_CST);
+  __builtin_amdgcn_s_waitcnt(0);
+  __atomic_signal_fence(__ATOMIC_SEQ_CST);
+  __syncthreads();
+  if (tid == 0) s_last = atomicAdd(reinterpret_cast<uint32_t*>(ws + L.off_cnt) + t, 1u) == gridDim.x - 1 ? 1 : 0;
   __syncthreads();
   if (!s_last) return;
 
-  auto sum_of = [&](int i, bool residual) {
-    if (i >= L.splits) return 0.0;
+  bool residual = true;
+  auto sum_of = [&](int i) {
     return __hip_atomic_load(residual ? &sums[i].x : &sums[i].y, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   };
-  // inclusive running sum over the threads; `whole`: over all of them
-  auto running = [&](double v, double& whole) {
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const uint64_t w = __builtin_bit_cast(uint64_t, v);
-      const uint32_t lo = __shfl_up((uint32_t)w, o, 64), hi = __shfl_up((uint32_t)(w >> 32), o, 64);
-      if ((tid & 63) >= o) v += __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
-    }
-    __syncthreads();
-    if ((tid & 63) == 63) s_scan[tid >> 6] = v;
-    __syncthreads();
-    whole = 0.0;
-#pragma unroll
-    for (int w = 0; w < kStatThreads / 64; ++w) {
-      if (w < (tid >> 6)) v += s_scan[w];
-      whole += s_scan[w];
-    }
-    return v;
-  };
   double total = 0.0;
-  for (int i = tid; i < L.splits; i += kStatThreads) total += sum_of(i, true);
-  total = block_sum<kStatThreads>(total, s_red);
-  const bool residual = total > 0.0;
-  if (!residual) {  // nothing is left but by rounding: p itself
+  for (int i = tid; i < L.splits; i += kThreads) total += sum_of(i);
+  total = block_sum<kThreads>(total, s_red);
+  if (!(total > 0.0)) {
+    residual = false;
     total = 0.0;
-    for (int i = tid; i < L.splits; i += kStatThreads) total += sum_of(i, false);
-    total = block_sum<kStatThreads>(total, s_red);
+    for (int i = tid; i < L.splits; i += kThreads) total += sum_of(i);
+    total = block_sum<kThreads>(total, s_red);
   }
-  // the first chunk in which the running sum passes the target; else the last
-  // that holds anything, and in it the last token
-  const double target = (double)a.u_bonus[t] * total;
-  if (tid == 0) {
-    s_chunk = L.splits;
-    s_last = -1;
-  }
-  __syncthreads();
-  double before = 0.0;
-  for (int i0 = 0; i0 < L.splits; i0 += kStatThreads) {
-    const double v = sum_of(i0 + tid, residual);
-    double whole;
-    const double upto = before + running(v, whole);
-    if (v > 0.0) {
-      atomicMax(&s_last, i0 + tid);
-      if (upto > target) atomicMin(&s_chunk, i0 + tid);
-    }
-    __syncthreads();
-    if (s_chunk == i0 + tid) s_before = target - (upto - v);
-    __syncthreads();
-    if (s_chunk < L.splits) break;
-    before += whole;
-  }
-  if (tid == 0) {
-    if (s_chunk == L.splits) {
-      s_chunk = s_last;
-      s_before = __builtin_huge_val();
-    }
-    s_pick = kChunk;
-    s_some = -1;
-  }
-  __syncthreads();
-  const int chunk = s_chunk;
-  const double in_chunk = s_before;
-  mark(chunk);
-  double res[kPer], all[kPer], own = 0.0, whole;
-  weights(chunk, res, all);
+  const Found f = find_chunk<kThreads>(sum_of, L.splits, (double)a.u_bonus[t] * total, s_red, s_int, &s_rest);
+  constexpr int N = kChunk / kThreads;
+  double w[N];
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    if (!residual) res[i] = all[i];
-    own += res[i];
-  }
-  double cum = running(own, whole) - own;
-  int pick = kChunk, end = -1;
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    cum += res[i];
-    if (res[i] > 0.0) {
-      end = tid * kPer + i;
-      if (pick == kChunk && cum > in_chunk) pick = end;
+  for (int i = 0; i < N; ++i) {
+    const int tok = f.chunk * kChunk + tid * N + i;
+    w[i] = 0.0;
+    if (tok < a.vocab) {
+      w[i] = weigh(logit(a, st.row, tok)) * inv;
+      if (residual) w[i] = fmax(w[i] - st.c * (double)a.draft[(size_t)st.row * a.vocab + tok], 0.0);
     }
   }
-  if (pick < kChunk) atomicMin(&s_pick, pick);
-  if (end >= 0) atomicMax(&s_some, end);
-  __syncthreads();
-  if (tid == 0) a.bonus[t] = chunk * kChunk + (s_pick < kChunk ? s_pick : s_some);
+  const int pick = find_token<kThreads>(w, f.rest, s_red, s_int);
+  if (tid == 0) a.bonus[t] = f.chunk * kChunk + pick;
 }
 
 }  // namespace
@@ -521,14 +646,20 @@ __global__ __launch_bounds__(kStatThreads) void sampled_draw_kernel(SampledArgs 
 size_t tree_sampled_ws_bytes(int num_trees, int total, int vocab) { return layout_of(num_trees, total, vocab).total; }
 
 hipError_t launch_tree_sampled(const SampledArgs& a, hipStream_t s) {
-  const int splits = (a.vocab + kChunk - 1) / kChunk;
-  hipLaunchKernelGGL(sampled_stat_kernel, dim3(splits, a.total), dim3(kStatThreads), 0, s, a);
+  const int groups = ((a.vocab + kChunk - 1) / kChunk + kWaves - 1) / kWaves;
+  // one chunk a wave until the waves fill the card (8192 of them), then up to 8
+  const int64_t waves = (int64_t)groups * kWaves * a.total;
+  const int each = (int)(waves <= 8192 ? 1 : waves >= 8 * 8192 ? 8 : (waves + 8191) / 8192);
+  hipLaunchKernelGGL(sampled_stat_kernel, dim3((groups + each - 1) / each, a.total), dim3(kThreads), 0, s, a, each);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(sampled_walk_kernel, dim3(a.num_trees), dim3(kWalkThreads), 0, s, a);
+  if (a.draft)
+    hipLaunchKernelGGL(sampled_walk_kernel<1024>, dim3(a.num_trees), dim3(1024), 0, s, a);
+  else
+    hipLaunchKernelGGL(sampled_walk_kernel<256>, dim3(a.num_trees), dim3(256), 0, s, a);
   e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(sampled_draw_kernel, dim3(splits, a.num_trees), dim3(kStatThreads), 0, s, a);
+  if (e != hipSuccess || !a.draft) return e;
+  hipLaunchKernelGGL(sampled_draw_kernel, dim3(groups, a.num_trees), dim3(kThreads), 0, s, a);
   return hipGetLastError();
 }
 
