@@ -419,45 +419,40 @@ def w12_tree_build(lp: torch.Tensor, tok: torch.Tensor, depth: torch.Tensor, roo
 
 # ------------------------------------------------------------------ KV cache of the verify pass
 
-def _is(t, dtype, ndim: int | None = None) -> bool:
-    """Whether t is what _need asks for (which names what is wrong when not)."""
-    return (isinstance(t, torch.Tensor) and t.dtype == dtype and t.is_cuda and t.is_contiguous()
-            and (ndim is None or t.dim() == ndim))
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
 
 
-def _check(dev: torch.device, *wanted) -> None:
-    """Checks (name, tensor, dtype, ndim, entries or None) tuples of a call on dev."""
-    for name, t, dtype, ndim, n in wanted:
-        if not _is(t, dtype, ndim):
-            _need(t, dtype, name, ndim)
-        if t.device != dev:
-            raise ValueError(f"{name} must be on {dev} (got {t.device})")
-        if n is not None and t.numel() != n:
-            raise ValueError(f"{name} must have {n} entries (got {t.numel()})")
+def _get(t, dtype, name: str, ndim: int | None, index: int | None, entries: int | None = None) -> int:
+    """Checks a tensor argument (on GPU `index`, if given, with that many
+    entries, if given) and returns its address."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_contiguous() and (ndim is None or t.dim() == ndim)
+            and t.get_device() >= 0):
+        _need(t, dtype, name, ndim)
+    if index is not None and t.get_device() != index:
+        raise ValueError(f"{name} must be on cuda:{index} (got {t.device})")
+    if entries is not None and t.numel() != entries:
+        raise ValueError(f"{name} must have {entries} entries (got {t.numel()})")
+    return t.data_ptr()
 
 
-def _at(t: torch.Tensor | None) -> int:
-    return t.data_ptr() if t is not None else 0
+def _raw_stream(index: int) -> int:
+    return torch.cuda.current_stream(index).cuda_stream
 
 
-class _On:
-    """The device of a call made current while its kernels are launched;
-    gives the current stream there."""
-    __slots__ = ("index", "before")
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
 
-    def __init__(self, dev: torch.device):
-        self.index, self.before = dev.index, None
 
-    def __enter__(self) -> int:
-        current = torch.cuda.current_device()
-        if current != self.index:
-            self.before = current
-            torch.cuda.set_device(self.index)
-        return torch.cuda.current_stream(self.index).cuda_stream
-
-    def __exit__(self, *exc):
-        if self.before is not None:
-            torch.cuda.set_device(self.before)
+def _run(index: int, what: str, *args) -> None:
+    """Calls an entry point with the current stream of GPU `index`, that GPU
+    being the current one meanwhile."""
+    fn = getattr(_lib or lib(), what)
+    if torch.cuda.current_device() == index:
+        status = fn(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, _raw_stream(index))
+    if status != W12_OK:
+        raise W12Error(status, what)
 
 
 @dataclass
@@ -477,22 +472,26 @@ class KvCache:
     def __post_init__(self):
         if not isinstance(self.pages, torch.Tensor) or self.pages.dtype not in (torch.float8_e4m3fn, torch.int8):
             raise TypeError("pages must be a float8_e4m3fn or int8 tensor")
-        pages, scales, recent, table, length = self.pages, self.scales, self.recent, self.page_table, self.length
-        dev, dim = pages.device, self.head_dim
-        _check(dev, ("pages", pages, pages.dtype, 5, None), ("scales", scales, torch.float32, 4, None),
-               ("recent", recent, torch.bfloat16, 5, None), ("page_table", table, torch.int32, 2, None),
-               ("length", length, torch.int32, 1, None))
+        pages, scales, recent, table, length, dim = (self.pages, self.scales, self.recent, self.page_table, self.length,
+                                                     self.head_dim)
+        at = _get(pages, pages.dtype, "pages", 5, None)
+        self.index = index = pages.get_device()
+        ats = (at, _get(scales, _F32, "scales", 4, index), _get(recent, _BF16, "recent", 5, index),
+               _get(table, _I32, "page_table", 2, index), _get(length, _I32, "length", 1, index))
         layers, num_pages, kv, two, page = pages.shape
         slots, blocks = table.shape
         rows = recent.shape
-        if (two != 2 or dim < 1 or page % dim or scales.shape != pages.shape[:4] or length.shape[0] != slots
-                or rows[:4] != (layers, slots, kv, 2) or rows[4] % dim):
+        if (two != 2 or dim < 1 or page % dim or scales.shape != (layers, num_pages, kv, 2) or length.shape[0] != slots
+                or rows[0] != layers or rows[1] != slots or rows[2] != kv or rows[3] != 2 or rows[4] % dim):
             raise ValueError("the cache's arrays differ in shape")
-        self.device, self.kv_heads = dev, kv
-        self._desc = W12KvCache(W12_KV_INT8 if pages.dtype == torch.int8 else W12_KV_E4M3, layers, num_pages, kv,
-                                page // dim, dim, slots, rows[4] // dim, blocks, pages.data_ptr(), scales.data_ptr(),
-                                recent.data_ptr(), table.data_ptr(), length.data_ptr())
+        self.kv_heads = kv
+        self._desc = W12KvCache(W12_KV_INT8 if pages.dtype is torch.int8 else W12_KV_E4M3, layers, num_pages, kv,
+                                page // dim, dim, slots, rows[4] // dim, blocks, *ats)
         self._ref = ctypes.byref(self._desc)
+
+    @property
+    def device(self):
+        return self.pages.device
 
     def desc(self) -> W12KvCache:
         return self._desc
@@ -515,44 +514,31 @@ def kv_cache(layers: int, kv_heads: int, head_dim: int, num_pages: int, slots: i
         torch.zeros(slots, dtype=torch.int32, device=device), head_dim)
 
 
-def _step(cache: KvCache, row_off, slot, rows: int, name: str, more) -> int:
-    """Checks the step's arrays; returns the number of sequences."""
-    dev = cache.device
-    _check(dev, ("row_off", row_off, torch.int32, 1, None))
-    seqs = row_off.shape[0] - 1
-    if slot is not None:
-        _check(dev, ("slot", slot, torch.int32, 1, seqs))
-    if more is not None:
-        _check(dev, (name, more, torch.int32, 1, rows))
-    return seqs
-
-
 def w12_kv_append(cache: KvCache, layer: int, qkv: torch.Tensor, row_off: torch.Tensor, rope: torch.Tensor,
                   q_heads: int, slot: torch.Tensor | None = None, parent: torch.Tensor | None = None,
                   interleaved: bool = False, out: torch.Tensor | None = None) -> torch.Tensor:
     """Rotates q and k of qkv [rows, (q_heads + 2 kv_heads) * head_dim] (fp32
     or bf16) and appends k, v as the step's rows. rope [positions, rot_dim]
     fp32 holds cosines, then sines. Returns q [rows, q_heads, head_dim] bf16."""
-    if not isinstance(qkv, torch.Tensor) or qkv.dtype not in (torch.float32, torch.bfloat16):
+    if not isinstance(qkv, torch.Tensor) or qkv.dtype not in (_F32, _BF16):
         raise TypeError("qkv must be a float32 or bfloat16 tensor")
-    dev, dim, f32 = cache.device, cache.head_dim, qkv.dtype == torch.float32
-    _check(dev, ("qkv", qkv, qkv.dtype, 2, None), ("rope", rope, torch.float32, 2, None))
+    index, dim = cache.index, cache.head_dim
+    at_x, at_rope = _get(qkv, qkv.dtype, "qkv", 2, index), _get(rope, _F32, "rope", 2, index)
     rows, width = qkv.shape
     if width != (q_heads + 2 * cache.kv_heads) * dim:
         raise ValueError(f"qkv has {width} columns, {q_heads} + 2 * {cache.kv_heads} heads of "
                          f"{dim} need {(q_heads + 2 * cache.kv_heads) * dim}")
-    seqs = _step(cache, row_off, slot, rows, "parent", parent)
+    at_off = _get(row_off, _I32, "row_off", 1, index)
+    seqs = row_off.shape[0] - 1
     if out is None:
-        out = torch.empty(rows, q_heads, dim, dtype=torch.bfloat16, device=dev)
-    else:
-        _check(dev, ("out", out, torch.bfloat16, None, None))
-        if out.numel() < rows * q_heads * dim:
-            raise ValueError("out must hold [rows, q_heads, head_dim]")
-    with _On(dev) as stream:
-        _ok(lib().w12_kv_append(cache._ref, layer, seqs, _at(slot), row_off.data_ptr(), rows, _at(parent),
-                                qkv.data_ptr(), W12_Y_F32 if f32 else W12_Y_BF16, q_heads, rope.data_ptr(),
-                                rope.shape[0], rope.shape[1], 1 if interleaved else 0, out.data_ptr(), stream),
-            "w12_kv_append")
+        out = torch.empty(rows, q_heads, dim, dtype=_BF16, device=qkv.device)
+    elif out.numel() < rows * q_heads * dim:
+        raise ValueError("out must hold [rows, q_heads, head_dim]")
+    positions, rot = rope.shape
+    _run(index, "w12_kv_append", cache._ref, layer, seqs, 0 if slot is None else _get(slot, _I32, "slot", 1, index, seqs),
+         at_off, rows, 0 if parent is None else _get(parent, _I32, "parent", 1, index, rows), at_x,
+         W12_Y_F32 if qkv.dtype is _F32 else W12_Y_BF16, q_heads, at_rope, positions, rot, 1 if interleaved else 0,
+         _get(out, _BF16, "out", None, index))
     return out
 
 
@@ -560,12 +546,13 @@ _kv_ws: dict = {}  # workspace bytes of w12_kv_attention by device and sizes
 
 
 def _attention_workspace_bytes(cache: KvCache, seqs: int, rows: int, q_heads: int) -> int:
-    key = (cache.device.index, cache.head_dim, cache.kv_heads, seqs, rows, q_heads)
+    key = (cache.index, cache.head_dim, cache.kv_heads, seqs, rows, q_heads)
     need = _kv_ws.get(key)
     if need is None:
         out = ctypes.c_size_t(0)
-        _ok(lib().w12_kv_attention_workspace(cache._ref, seqs, rows, q_heads, ctypes.byref(out)),
-            "w12_kv_attention_workspace")
+        with torch.cuda.device(cache.index):
+            _ok(lib().w12_kv_attention_workspace(cache._ref, seqs, rows, q_heads, ctypes.byref(out)),
+                "w12_kv_attention_workspace")
         need = _kv_ws[key] = out.value
     return need
 
@@ -578,30 +565,30 @@ def w12_kv_attention(cache: KvCache, layer: int, q: torch.Tensor, row_off: torch
     head_dim ** -0.5. ws: a workspace of the caller's (its content is
     ignored); without one the call takes one kept per stream, or, while it is
     captured, one of its own (replays may overlap in time with other calls)."""
-    dev = cache.device
-    _check(dev, ("q", q, torch.bfloat16, 3, None))
+    index = cache.index
+    at_q = _get(q, _BF16, "q", 3, index)
     rows, q_heads, dim = q.shape
     if dim != cache.head_dim:
         raise ValueError(f"q has head_dim {dim}, the cache {cache.head_dim}")
-    seqs = _step(cache, row_off, slot, rows, "parent", parent)
+    at_off = _get(row_off, _I32, "row_off", 1, index)
+    seqs = row_off.shape[0] - 1
     if out is None:
-        out = torch.empty(rows, q_heads * dim, dtype=torch.bfloat16, device=dev)
-    else:
-        _check(dev, ("out", out, torch.bfloat16, None, None))
-        if out.numel() < rows * q_heads * dim:
-            raise ValueError("out must hold [rows, q_heads * head_dim]")
-    with _On(dev) as stream:
-        need = _attention_workspace_bytes(cache, seqs, rows, q_heads)
-        if ws is None:
-            if torch.cuda.is_current_stream_capturing():
-                ws = torch.empty(need, dtype=torch.uint8, device=dev)
-            else:
-                ws = _ws_cache.get((dev.index, stream, "kv"))
-                if ws is None or ws.numel() < need:
-                    ws = workspace(need, dev, "kv")
-        _ok(lib().w12_kv_attention(cache._ref, layer, seqs, _at(slot), row_off.data_ptr(), rows, _at(parent),
-                                   q.data_ptr(), q_heads, dim ** -0.5 if scale is None else scale, out.data_ptr(),
-                                   ws.data_ptr(), ws.numel() * ws.element_size(), stream), "w12_kv_attention")
+        out = torch.empty(rows, q_heads * dim, dtype=_BF16, device=q.device)
+    elif out.numel() < rows * q_heads * dim:
+        raise ValueError("out must hold [rows, q_heads * head_dim]")
+    need = _attention_workspace_bytes(cache, seqs, rows, q_heads)
+    if ws is None:
+        if torch.cuda.is_current_stream_capturing():
+            ws = torch.empty(need, dtype=torch.uint8, device=q.device)
+        else:
+            ws = _ws_cache.get((index, _raw_stream(index), "kv"))
+            if ws is None or ws.numel() < need:
+                ws = workspace(need, q.device, "kv")
+    _run(index, "w12_kv_attention", cache._ref, layer, seqs,
+         0 if slot is None else _get(slot, _I32, "slot", 1, index, seqs), at_off, rows,
+         0 if parent is None else _get(parent, _I32, "parent", 1, index, rows), at_q, q_heads,
+         dim ** -0.5 if scale is None else scale, _get(out, _BF16, "out", None, index),
+         _get(ws, ws.dtype, "ws", None, index), ws.numel() * ws.element_size())
     return out
 
 
@@ -611,20 +598,18 @@ def w12_kv_commit(cache: KvCache, row_off: torch.Tensor, accept_len: torch.Tenso
     path; path None: each sequence's first accept_len + 1 rows) in every
     layer. Writes the new lengths into length_out [slots] (the cache's own by
     default) and returns it."""
-    dev = cache.device
-    if path is not None:
-        _check(dev, ("path", path, torch.int32, 1, None))
-        rows = path.shape[0]
+    index = cache.index
+    at_off = _get(row_off, _I32, "row_off", 1, index)
+    seqs = row_off.shape[0] - 1
+    if path is None:
+        at_path, rows = 0, MAX_ROWS
     else:
-        rows = MAX_ROWS
-    seqs = _step(cache, row_off, slot, rows, "path", None)
+        at_path, rows = _get(path, _I32, "path", 1, index), path.shape[0]
     if length_out is None:
         length_out = cache.length
-    _check(dev, ("accept_len", accept_len, torch.int32, 1, seqs),
-           ("length_out", length_out, torch.int32, 1, cache.length.shape[0]))
-    with _On(dev) as stream:
-        _ok(lib().w12_kv_commit(cache._ref, seqs, _at(slot), row_off.data_ptr(), rows, accept_len.data_ptr(), _at(path),
-                                length_out.data_ptr(), stream), "w12_kv_commit")
+    _run(index, "w12_kv_commit", cache._ref, seqs, 0 if slot is None else _get(slot, _I32, "slot", 1, index, seqs), at_off,
+         rows, _get(accept_len, _I32, "accept_len", 1, index, seqs), at_path,
+         _get(length_out, _I32, "length_out", 1, index, cache._desc.slots))
     return length_out
 
 
@@ -635,34 +620,30 @@ def tree_accept_sampled(node_off: torch.Tensor, parent: torch.Tensor, token: tor
     bf16 (a row per node), random numbers u_accept [nodes] and u_bonus
     [trees], temperature [trees] or None (1), draft [nodes, vocab] fp32 or
     None (chosen drafts). Returns (accept_len, path, bonus) as tree_accept."""
-    if not isinstance(logits, torch.Tensor) or logits.dtype not in (torch.float32, torch.bfloat16):
+    if not isinstance(logits, torch.Tensor) or logits.dtype not in (_F32, _BF16):
         raise TypeError("logits must be a float32 or bfloat16 tensor")
-    dev, i32, f32 = logits.device, torch.int32, torch.float32
-    _check(dev, ("logits", logits, logits.dtype, 2, None), ("node_off", node_off, i32, 1, None))
+    at_x = _get(logits, logits.dtype, "logits", 2, None)
+    index, dev = logits.get_device(), logits.device
+    at_off = _get(node_off, _I32, "node_off", 1, index)
     total, vocab = logits.shape
     T = node_off.shape[0] - 1
-    _check(dev, ("parent", parent, i32, 1, total), ("token", token, i32, 1, total), ("u_accept", u_accept, f32, 1, total),
-           ("u_bonus", u_bonus, f32, 1, T))
-    if temperature is not None:
-        _check(dev, ("temperature", temperature, f32, 1, T))
-    if draft is not None:
-        _check(dev, ("draft", draft, f32, 2, None))
-        if draft.shape != logits.shape:
-            raise ValueError("draft and logits differ in shape")
     if T < 1:
         raise ValueError("tree_accept_sampled: no trees")
-    acc = torch.empty(T, dtype=i32, device=dev)
-    path = torch.empty(total, dtype=i32, device=dev)
-    bonus = torch.empty(T, dtype=i32, device=dev)
-    with _On(dev) as stream:
-        L = lib()
-        if ws is None:
-            need = ctypes.c_size_t(0)
-            _ok(L.tree_accept_sampled_workspace(T, total, vocab, ctypes.byref(need)), "tree_accept_sampled_workspace")
-            ws = torch.empty(need.value, dtype=torch.uint8, device=dev)
-        _ok(L.tree_accept_sampled(T, node_off.data_ptr(), total, parent.data_ptr(), token.data_ptr(), logits.data_ptr(),
-                                  W12_Y_F32 if logits.dtype == f32 else W12_Y_BF16, vocab, _at(temperature), _at(draft),
-                                  u_accept.data_ptr(), u_bonus.data_ptr(), acc.data_ptr(), path.data_ptr(),
-                                  bonus.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(), stream),
-            "tree_accept_sampled")
-    return acc, path, bonus
+    at = (_get(parent, _I32, "parent", 1, index, total), _get(token, _I32, "token", 1, index, total))
+    at_u = (_get(u_accept, _F32, "u_accept", 1, index, total), _get(u_bonus, _F32, "u_bonus", 1, index, T))
+    at_temp = 0 if temperature is None else _get(temperature, _F32, "temperature", 1, index, T)
+    at_draft = 0 if draft is None else _get(draft, _F32, "draft", 2, index)
+    if draft is not None and draft.shape != logits.shape:
+        raise ValueError("draft and logits differ in shape")
+    if ws is None:
+        need = ctypes.c_size_t(0)
+        _ok((_lib or lib()).tree_accept_sampled_workspace(T, total, vocab, ctypes.byref(need)),
+            "tree_accept_sampled_workspace")
+        ws = torch.empty(need.value, dtype=torch.uint8, device=dev)
+    # one allocation for the three outputs (bonus and accept_len first: T entries each)
+    out = torch.empty(2 * T + total, dtype=_I32, device=dev)
+    base = out.data_ptr()
+    _run(index, "tree_accept_sampled", T, at_off, total, *at, at_x, W12_Y_F32 if logits.dtype is _F32 else W12_Y_BF16,
+         vocab, at_temp, at_draft, *at_u, base, base + 8 * T, base + 4 * T, _get(ws, ws.dtype, "ws", None, index),
+         ws.numel() * ws.element_size())
+    return out[:T], out[2 * T:], out[T:2 * T]
