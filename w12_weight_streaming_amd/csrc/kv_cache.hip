@@ -192,8 +192,15 @@ __device__ __forceinline__ CommitView commit_view(const CommitArgs& a, int s, in
 // 16 values of chunk `ch` of a block of rows whose sources `src(i)` gives:
 // keys are 16 dims of one row, values one dim of 16 rows.
 template <typename Src>
-__device__ __forceinline__ void gather16(const uint16_t* __restrict__ base, int v, int dim, int ch, Src src,
+__device__ __forceinline__ void gather16(const uint16_t* __restrict__ base, int v, int dim, int ch, bool straight, Src src,
                                          uint32_t (&w)[8]) {
+  if (straight) {  // rows as they lie: the block has the recent rows' order
+    const uint4* p = reinterpret_cast<const uint4*>(base + (size_t)ch * 16);
+    const uint4 x = p[0], y = p[1];
+    w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+    w[4] = y.x; w[5] = y.y; w[6] = y.z; w[7] = y.w;
+    return;
+  }
   const int lane = ch & 63, db = (ch >> 6) % (dim >> 5), g = (ch >> 6) / (dim >> 5);
   if (!v) {
     const uint4* p = reinterpret_cast<const uint4*>(base + key_at(src(g * 32 + (lane & 31)), db * 32 + (lane >> 5) * 16, dim));
@@ -231,7 +238,7 @@ template <int kPer>
 __global__ __launch_bounds__(kCommitThreads) void kv_commit_kernel(CommitArgs a) {
   __shared__ int s_src[kStepRows];
   __shared__ int s_bad;
-  __shared__ uint32_t s_amax[kCommitThreads / 64];
+  __shared__ uint32_t s_amax[2][kCommitThreads / 64];  // by the block's parity: one barrier a block
   const int tid = threadIdx.x, s = blockIdx.y;
   const int v = blockIdx.x & 1, head = (blockIdx.x >> 1) % a.c.kv_heads, layer = (blockIdx.x >> 1) / a.c.kv_heads;
   const CommitView w = commit_view(a, s, s_src, &s_bad);
@@ -246,10 +253,12 @@ __global__ __launch_bounds__(kCommitThreads) void kv_commit_kernel(CommitArgs a)
       const int r = b * page + i;
       return r < tail ? r : s_src[r - tail];
     };
+    const bool straight = !a.path;
+    const uint16_t* from = straight ? base + (size_t)b * page * dim : base;
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
       const int ch = k * kCommitThreads + tid;
-      if (ch < chunks) gather16(base, v, dim, ch, src, to[k]);
+      if (ch < chunks) gather16(from, v, dim, ch, straight, src, to[k]);
     }
   };
   if (closed > 0) fetch(0, x);
@@ -269,11 +278,10 @@ __global__ __launch_bounds__(kCommitThreads) void kv_commit_kernel(CommitArgs a)
     }
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) most = max(most, (uint32_t)__shfl_xor((int)most, o, 64));
-    if ((tid & 63) == 0) s_amax[tid >> 6] = most;
+    if ((tid & 63) == 0) s_amax[b & 1][tid >> 6] = most;
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kCommitThreads / 64; ++i) most = max(most, s_amax[i]);
-    __syncthreads();
+    for (int i = 0; i < kCommitThreads / 64; ++i) most = max(most, s_amax[b & 1][i]);
     const float amax = __uint_as_float(most);
     // e4m3: the power of two that brings amax to 448 = 1.75 * 2^8 or below
     // (exact to divide by); int8: amax / 127. A block that holds an infinity
@@ -327,23 +335,31 @@ __global__ __launch_bounds__(kCommitThreads) void kv_commit_kernel(CommitArgs a)
   // it does not lie there already
   const int first = closed ? 0 : tail;  // without a closed block the tail stays
   __syncthreads();
-  // one round moves 8 dims of `per` rows; a row's place does not depend on other rows
-  const int cols = dim / 8, per = kCommitThreads / cols;
-  for (int i0 = first; i0 < left; i0 += per) {
-    const int i = i0 + tid / cols, d0 = tid % cols * 8;
-    const bool on = tid < per * cols && i < left;
-    uint16_t t[8];
-    int from = 0;
-    if (on) {
-      const int r = closed * page + i;
-      from = r < tail ? r : s_src[r - tail];
+  // a round moves 8 dims a thread of kTurns times `per` rows
+  constexpr int kTurns = 4;
+  const int cols = dim / 8, per = kCommitThreads / cols, d0 = tid % cols * 8;
+  for (int i0 = first; i0 < left; i0 += kTurns * per) {
+    uint16_t t[kTurns][8];
+    int from[kTurns];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) t[j] = base[v ? value_at(from, d0 + j, dim) : key_at(from, d0 + j, dim)];
+    for (int k = 0; k < kTurns; ++k) {
+      const int i = i0 + k * per + tid / cols;
+      from[k] = i;
+      if (i < left) {
+        const int r = closed * page + i;
+        from[k] = r < tail ? r : s_src[r - tail];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) t[k][j] = base[v ? value_at(from[k], d0 + j, dim) : key_at(from[k], d0 + j, dim)];
+      }
     }
     __syncthreads();
-    if (on && from != i) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) base[v ? value_at(i, d0 + j, dim) : key_at(i, d0 + j, dim)] = t[j];
+    for (int k = 0; k < kTurns; ++k) {
+      const int i = i0 + k * per + tid / cols;
+      if (from[k] != i) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) base[v ? value_at(i, d0 + j, dim) : key_at(i, d0 + j, dim)] = t[k][j];
+      }
     }
     __syncthreads();
   }
