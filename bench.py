@@ -404,6 +404,103 @@ def run_block(args, w12, synth, torch, dev):
     return run_pass(args, w12, synth, torch, dev)
 
 
+def run_step(args, w12, synth, torch, dev):
+    """A verify step with its KV cache: per layer the Wq|Wk|Wv product, the
+    rows' keys and values appended, attention over --context committed tokens
+    and the tree's own rows, Wo, Wgate|Wup and Wdown; then the LM-head product,
+    sampled acceptance of the 32-node tree and the accepted rows committed in
+    all layers. 48 query and 8 key/value heads of 128 dims (the 8192 and 6144
+    of the layer shapes), e4m3 pages of 64 tokens; the context is a prompt
+    that went through append and commit."""
+    import numpy as np
+
+    layers, q_heads, kv_heads, dim, page, context = args.layers, 48, 8, 128, 64, args.context
+    assert 1 <= context <= 65536, "--context must be in [1, 65536]"
+    mats, _, _ = pack_layers(w12, synth, torch, dev, layers)
+    head_pw, head_x, top16, _ = pack_head(w12, synth, torch, dev)
+    room = context + M_ROWS * (args.steps + args.warmup + 1) + page
+    blocks = -(-room // page)
+    cache = w12.kv_cache(layers, kv_heads, dim, blocks, 1, blocks, page, device=dev)
+    cache.page_table.copy_(torch.randperm(blocks, generator=torch.Generator().manual_seed(6)).int()[None])
+    angle = torch.arange(room + M_ROWS)[:, None] * 10000.0 ** (-torch.arange(0, dim, 2) / dim)
+    rope = torch.cat([angle.cos(), angle.sin()], 1).float().to(dev)
+    i32 = lambda a: torch.tensor(np.asarray(a), dtype=torch.int32, device=dev)
+    width = (q_heads + 2 * kv_heads) * dim
+    for at in range(0, context, 512):
+        n = min(512, context - at)
+        off, acc = i32([0, n]), i32([n - 1])
+        for li in range(layers):
+            qkv = synth.activations_bf16(n, width, seed=1_000_000 * 6 + 1000 * li + at // 512, device=dev)
+            w12.w12_kv_append(cache, li, qkv, off, rope, q_heads)
+        w12.w12_kv_commit(cache, off, acc)
+    log(f"context of {context} tokens: {cache.nbytes() / 2 ** 30:.2f} GiB of cache")
+
+    outs = {name: torch.empty(M_ROWS, n, dtype=torch.bfloat16, device=dev) for name, n, _ in LAYER_SHAPES}
+    logits = torch.empty(M_ROWS, head_pw.n, dtype=torch.float32, device=dev)
+    q = torch.empty(M_ROWS, q_heads, dim, dtype=torch.bfloat16, device=dev)
+    att = torch.empty(M_ROWS, q_heads * dim, dtype=torch.bfloat16, device=dev)
+    ws = w12.workspace(max([w12.gemm_workspace_bytes(n, k, M_ROWS) for _, n, k in LAYER_SHAPES] +
+                           [w12.gemm_workspace_bytes(head_pw.n, head_pw.k, M_ROWS)]), dev)
+    am = w12.w12_head_argmax(head_pw, head_x, ws=ws, with_max=False)[0].cpu().numpy().astype(np.int32)
+    parent, token = synth.random_tree(M_ROWS, 16, am, top16, 0.7, seed=4_000_000 + 9, vocab=VOCAB)
+    t_off, t_par, t_tok = i32([0, M_ROWS]), i32(parent), i32(token)
+    gen = torch.Generator(device=dev).manual_seed(7)
+    u = torch.rand(M_ROWS + 1, generator=gen, device=dev)
+    temp = torch.full((1,), 0.7, device=dev)
+    accepted = [None]
+
+    def launch(name, li=0):
+        if name == "APPEND":
+            w12.w12_kv_append(cache, li, outs[LAYER_SHAPES[0][0]], t_off, rope, q_heads, parent=t_par, out=q)
+        elif name == "ATTENTION":
+            w12.w12_kv_attention(cache, li, q, t_off, parent=t_par, out=att)
+        elif name == "HEAD":
+            w12.w12_gemm(head_pw, head_x, out=logits, ws=ws)
+        elif name == "SAMPLED":
+            accepted[0] = w12.tree_accept_sampled(t_off, t_par, t_tok, logits, u[:M_ROWS], u[M_ROWS:], temperature=temp)
+        elif name == "COMMIT":
+            w12.w12_kv_commit(cache, t_off, accepted[0][0], path=accepted[0][1])
+        else:
+            pw, x = mats[li][name]
+            w12.w12_gemm(pw, att if name == LAYER_SHAPES[1][0] else x, out=outs[name], ws=ws)
+
+    names = [name for name, _, _ in LAYER_SHAPES]
+    order = [names[0], "APPEND", "ATTENTION"] + names[1:]
+
+    def step():
+        for li in range(layers):
+            for name in order:
+                launch(name, li)
+        for name in ("HEAD", "SAMPLED", "COMMIT"):
+            launch(name)
+
+    for _ in range(args.warmup):
+        step()
+    torch.cuda.synchronize()
+    us = time_events(lambda i: step(), args.steps)
+    assert bool(torch.isfinite(att.float()).all()) and int(accepted[0][0]) >= 0
+    grown = int(cache.length[0])
+    assert context < grown <= context + M_ROWS * (args.steps + args.warmup)
+    per = {}
+    for name in order + ["HEAD", "SAMPLED"]:  # every layer its own weights and pages
+        n = layers if name in order else 1
+        launch(name)
+        per[name] = time_events(lambda i: [launch(name, li) for li in range(n)], max(2, min(args.steps, 5))) / n
+    line = {
+        "metric": f"W12 verify step with a KV cache: ms at M={M_ROWS} rows, {context} tokens of context",
+        "value": round(us / 1000.0, 4), "unit": "ms", "n_gpus": 1, "steps": args.steps, "warmup": args.warmup,
+        "ms_per_step": round(us / 1000.0, 4), "higher_is_better": False, "scaling": "weak", "vs_baseline": None,
+        "dtype": "bf16", "data": "synthetic",
+        "config": {"workload": f"verify step of a {layers}-layer 27B-class stack with {q_heads} query and {kv_heads} "
+                               f"key/value heads of {dim} dims over {context} cached tokens (e4m3 pages of {page}), "
+                               "LM-head product, sampled acceptance and commit; norms and activations are not part of it",
+                   "rows": M_ROWS, "layers": layers, "context": context, "cache_bytes": cache.nbytes()},
+        "call_us": {k: round(v, 2) for k, v in per.items()},
+        "length_after": grown,
+    }
+    print(json.dumps(line), flush=True)
+
+
 def main():
     ap = argparse.ArgumentParser(description=__doc__.split("\n")[0])
     ap.add_argument("--gpus", type=int, default=1)
@@ -418,7 +515,7 @@ def main():
     ap.add_argument("--graph", action="store_true", help="replay the step as a HIP graph")
     ap.add_argument("--copy-gib", type=float, default=1.0,
                     help="size of the calibration copy launched after timing (0 = none)")
-    ap.add_argument("--workload", choices=("pass", "block", "batched", "sweep", "qpass", "tree", "cert"),
+    ap.add_argument("--workload", choices=("pass", "block", "batched", "sweep", "qpass", "tree", "cert", "step"),
                     default="pass",
                     help="pass: 64 layers + LM head argmax + tree acceptance at M=32 (the headline line); "
                          "block: the same with one layer; "
@@ -427,7 +524,10 @@ def main():
                          "sweep: Wgate|Wup 34816x5120 over M = 1 ... 512; "
                          "qpass: one block + head through the Q pass (8-bit view only) next to the exact pass; "
                          "tree: best-first draft trees, 24 requests sharing 192 rows and one 32-row tree; "
-                         "cert: the certified INT8 LM head next to the W12 head at M=32")
+                         "cert: the certified INT8 LM head next to the W12 head at M=32; "
+                         "step: the pass with its KV cache of --context tokens, sampled acceptance and commit")
+    ap.add_argument("--context", type=int, default=8192,
+                    help="committed tokens of the step workload (default 8192, at most 65536)")
     args = ap.parse_args()
 
     world = int(os.environ.get("WORLD_SIZE", "1"))
@@ -448,7 +548,7 @@ def main():
     torch.cuda.set_device(dev)
     w12.lib()
     fn = {"pass": run_pass, "block": run_block, "batched": run_batched, "sweep": run_sweep,
-          "qpass": run_qpass, "tree": run_tree, "cert": run_cert}[args.workload]
+          "qpass": run_qpass, "tree": run_tree, "cert": run_cert, "step": run_step}[args.workload]
     return fn(args, w12, synth, torch, dev)
 
 

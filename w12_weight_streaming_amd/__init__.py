@@ -3,7 +3,9 @@ verification pass of greedy speculative decoding on MI355X (gfx950).
 
 Thin ctypes binding over libw12.so (C ABI in include/w12.h), with the same
 names as the C entry points: w12_pack, w12_decode, w12_check, w12_gemm,
-w12_head_argmax, tree_accept. Every step of the path runs in the library's
+w12_head_argmax, tree_accept, and for the pass's KV cache and sampling
+requests w12_kv_append, w12_kv_attention, w12_kv_commit and
+tree_accept_sampled. Every step of the path runs in the library's
 HIP kernels; this module only checks tensor dtypes/devices, passes device
 pointers and the current HIP stream, and keeps zero-filled workspaces.
 There is no CPU fallback: without the built library every call raises.
