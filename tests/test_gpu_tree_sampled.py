@@ -181,3 +181,26 @@ def test_chosen_drafts_agree_with_tree_accept_at_low_temperature(w12):
     am = f["lg"].argmax(1)
     ref = [x.cpu().numpy() for x in w12.tree_accept(t(f["off"]), t(f["parent"]), t(f["token"]), t(am))]
     assert np.array_equal(acc, ref[0]) and np.array_equal(path, ref[1]) and np.array_equal(bonus, ref[2])
+
+
+@pytest.mark.parametrize("drafted", [False, True])
+def test_temperatures_of_every_size(w12, drafted):
+    """Down to a denormal one (only the row's maxima are left) and up to where
+    a mask of the type's lowest value still has weight; ties at the maximum,
+    lowest values and -inf among the logits."""
+    import torch
+    say("temperatures", drafted)
+    temps = np.array([1e-40, 1e-30, 1e-12, 1e-6, 1e-2, 1e3, 1e20, 3e38], np.float32)
+    f = forest(17, [7] * len(temps), 2200, drafted, spread=30.0)
+    lg = f["lg"].copy()
+    lg[:, 300:900] = np.finfo(np.float32).min
+    lg[:, 1500:1600] = -np.inf
+    top = lg.max(1)
+    lg[:, 40] = lg[:, 2100] = top            # three at the maximum, in two chunks
+    lg[::3, 41] = np.nextafter(top[::3], np.float32(-np.inf), dtype=np.float32)
+    f["token"][1::2] = np.where(np.arange(len(f["token"][1::2])) % 2, 40, 2100)
+    f["lg"], f["logits"], f["temp"] = lg, torch.tensor(lg), temps
+    if drafted:
+        f["draft"][:, [40, 2100]] += np.float32(0.25)
+    got = both(w12, f)
+    assert (got[0] >= 0).all()

@@ -115,38 +115,74 @@ __device__ __forceinline__ void draft16(const SampledArgs& a, int row, int t, fl
 }
 
 constexpr double kLog2e = 1.442695040888963407359925;
-// exp((x - max) / temperature) in 64 bits: 2^(y / 32) = 2^(n / 32) 2^(f / 32)
-// with |f| <= 1/2 for y = 32 (x - max) it2, it2 = log2(e) / temperature (0
+constexpr int kTable = 128, kTableLog = 7;
+// exp((x - max) / temperature) in 64 bits: 2^(y / 128) = 2^(n / 128) 2^(f / 128)
+// with |f| <= 1/2 for y = 128 (x - max) it2, it2 = log2(e) / temperature (0
 // exactly at the maximum, at any temperature). n comes from adding 1.5 2^52,
-// whose low bits then hold it: 2^(n mod 32 / 32) from a table in LDS, the rest
-// of n straight into the exponent. 2^(f / 32) is its Taylor series to the 5th
-// power (0.0108^6 / 720 = 2e-15 relative). Below 2^-1000, and for -inf, 0.
-// 64-bit operations run at half rate and bound the first launch: 192 rows of
-// 152064 tokens take 52 us with the library's exp, 33 with a series to the
-// 11th power and no table.
+// whose low bits then hold it: 2^(n mod 128 / 128) from a table in LDS, the rest
+// of n straight into the exponent. 2^(f / 128) is its Taylor series to the 4th
+// power (1e-15 relative). Below 2^-1000, and for -inf, 0.
+// 64-bit arithmetic bounds the first launch: 192 rows of 152064 bf16 logits (58
+// MB, 10 us of reading) take 52 us with the library's exp, 33 with a series to
+// the 11th power and no table, 30 with 32 entries, the 5th power and separate
+// products and sums, 27 like this.
 struct Weigher {
-  const double* table;  // LDS, 32 entries
-  double mx, it32;
-  float least;  // logits at or below it weigh nothing
-  __device__ __forceinline__ Weigher(const double* t, float top, double it2) : table(t), mx(top), it32(32.0 * it2) {
-    least = (float)(mx - 1000.0 / it2);
+  const double* table;  // LDS, kTable entries
+  double mx, rate;
+  float least, finite;  // logits at or below `least` (itself below the maximum) weigh nothing
+  __device__ __forceinline__ Weigher(const double* t, float top, double it2) : table(t), mx(top), rate(kTable * it2) {
+    least = fminf((float)(mx - 1000.0 / it2), nextafterf(top, -__builtin_huge_valf()));
+    finite = fmaxf(least, -3.402823466e38f);
+  }
+  // n and the series of an x that is not below `finite` (others: any finite value)
+  __device__ __forceinline__ double series(float x, int32_t& n) const {
+    const double d = (double)x - mx;
+    const double t = __builtin_fma(d, rate, 0x1.8p52);
+    const double f = __builtin_fma(d, rate, 0x1.8p52 - t);
+    double p = 0x1.3b2ab6fba4e77p-35;  // (ln(2) / 128)^k / k!
+    p = __builtin_fma(p, f, 0x1.c6b08d704a0c0p-26);
+    p = __builtin_fma(p, f, 0x1.ebfbdff82c58fp-17);
+    p = __builtin_fma(p, f, 0x1.62e42fefa39efp-8);
+    p = __builtin_fma(p, f, 1.0);
+    n = (int32_t)__builtin_bit_cast(uint64_t, t);
+    return p;
+  }
+  // the power of two that goes with it, as its halves
+  __device__ __forceinline__ void power(int32_t n, uint32_t& hi, uint32_t& lo) const {
+    const uint64_t b = __builtin_bit_cast(uint64_t, table[n & (kTable - 1)]);
+    hi = (uint32_t)(b >> 32) + ((uint32_t)(n & -kTable) << (20 - kTableLog));
+    lo = (uint32_t)b;
   }
   __device__ __forceinline__ double operator()(float x) const {
-    const double y = ((double)x - mx) * it32;
-    const double t = y + 0x1.8p52;
-    const double f = y - (t - 0x1.8p52);
-    double p = 0x1.5d87fe78a6731p-35;  // (ln(2) / 32)^k / k!
-    p = __builtin_fma(p, f, 0x1.3b2ab6fba4e77p-27);
-    p = __builtin_fma(p, f, 0x1.c6b08d704a0c0p-20);
-    p = __builtin_fma(p, f, 0x1.ebfbdff82c58fp-13);
-    p = __builtin_fma(p, f, 0x1.62e42fefa39efp-6);
-    p = __builtin_fma(p, f, 1.0);
-    const int32_t n = (int32_t)__builtin_bit_cast(uint64_t, t);
-    p *= table[n & 31];
-    const uint64_t b = __builtin_bit_cast(uint64_t, p);
+    int32_t n;
+    uint32_t hi, lo;
+    const double p = series(fmaxf(x, finite), n);
+    power(n, hi, lo);
     const bool some = x > least;
-    const uint32_t hi = some ? (uint32_t)(b >> 32) + ((uint32_t)(n >> 5) << 20) : 0u, lo = some ? (uint32_t)b : 0u;
-    return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+    return p * __builtin_bit_cast(double, ((uint64_t)(some ? hi : 0u) << 32) | (some ? lo : 0u));
+  }
+  // Sum of N weights, the maximum's 1 among them. What lies 500 powers of two
+  // below it may then count as just that (a clamp in place of two selects an
+  // element), if the logits are fine enough for such a value and reach so far.
+  template <int N>
+  __device__ __forceinline__ double sum(const float (&x)[N]) const {
+    const float low = (float)(mx - 500.0 * kTable / rate);
+    const double depth = (mx - (double)low) * rate;
+    double r = 0.0;
+    if (depth > 200.0 * kTable && depth < 1000.0 * kTable) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        int32_t n;
+        uint32_t hi, lo;
+        const double p = series(__builtin_amdgcn_fmed3f(x[i], low, __builtin_huge_valf()), n);
+        power(n, hi, lo);
+        r = __builtin_fma(p, __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo), r);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) r += (*this)(x[i]);
+    }
+    return r;
   }
 };
 __device__ const double kPowers[32] = {
@@ -159,9 +195,10 @@ __device__ const double kPowers[32] = {
     0x1.ae89f995ad3adp+0, 0x1.b7f76f2fb5e47p+0, 0x1.c199bdd85529cp+0, 0x1.cb720dcef9069p+0,
     0x1.d5818dcfba487p+0, 0x1.dfc97337b9b5fp+0, 0x1.ea4afa2a490dap+0, 0x1.f50765b6e4540p+0,
 };
-// The table in LDS; the caller synchronises before its first use.
+__device__ const double kFine[4] = {0x1.0000000000000p+0, 0x1.0163da9fb3335p+0, 0x1.02c9a3e778061p+0, 0x1.04315e86e7f85p+0};  // 2^(k / 128)
+// The table in LDS, a product of the two above; the caller synchronises before its first use.
 __device__ __forceinline__ void load_powers(double* s_pow) {
-  if (threadIdx.x < 32) s_pow[threadIdx.x] = kPowers[threadIdx.x];
+  if (threadIdx.x < kTable) s_pow[threadIdx.x] = kPowers[threadIdx.x / 4] * kFine[threadIdx.x % 4];
 }
 
 // A lane's value from 1, 2, 4 or 8 lanes before it in its row of 16 (around).
@@ -308,7 +345,7 @@ __global__ __launch_bounds__(kThreads) void sampled_stat_kernel(SampledArgs a, i
   char* ws = static_cast<char*>(a.ws);
   if (row == 0 && blockIdx.x == 0)
     for (int t = threadIdx.x; t < a.num_trees; t += kThreads) reinterpret_cast<uint32_t*>(ws + L.off_cnt)[t] = 0;
-  __shared__ double s_pow[32];
+  __shared__ double s_pow[kTable];
   load_powers(s_pow);
   float x[kPer], next[kPer];
   if (first < end) logits16(a, row, first * kChunk + lane * kPer, x);
@@ -327,17 +364,15 @@ __global__ __launch_bounds__(kThreads) void sampled_stat_kernel(SampledArgs a, i
     float top = -__builtin_huge_valf();
     bool nan = false;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      top = fmaxf(top, x[i]);
-      nan = nan || x[i] != x[i];
+    for (int i = 0; i < kPer; i += 2) {
+      top = fmaxf(fmaxf(top, x[i]), x[i + 1]);
+      nan = nan || __builtin_isunordered(x[i], x[i + 1]);
     }
     top = wave_max(top);
     // a NaN or +inf must reach the row's sum; nothing but -inf has no weight
     double sum = nan || top == __builtin_huge_valf() ? __builtin_nan("") : 0.0;
     if (top > -__builtin_huge_valf() && top < __builtin_huge_valf()) {
-      const Weigher weigh(s_pow, top, it2);
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) sum += weigh(x[i]);
+      sum += Weigher(s_pow, top, it2).sum(x);
     }
     sum = wave_sum(sum);
     if (lane == 0) reinterpret_cast<double2*>(ws + L.off_stat)[(size_t)row * L.splits + split] = make_double2(top, sum);
@@ -346,18 +381,26 @@ __global__ __launch_bounds__(kThreads) void sampled_stat_kernel(SampledArgs a, i
   }
 }
 
-// Maximum and sum of a whole row from its chunks, by one wave.
+// Maximum and sum of a whole row from its chunks, by one wave: up to 256
+// chunks (262144 tokens) stay in its registers, so they are read once.
 __device__ __forceinline__ void row_stat(const double2* st, int splits, const double* s_pow, double it2, float& mx, double& sum) {
+  constexpr int kKeep = 4;
   const int lane = threadIdx.x & 63;
+  const double none = -__builtin_huge_val();
+  double2 v[kKeep];
+#pragma unroll
+  for (int i = 0; i < kKeep; ++i) v[i] = lane + i * 64 < splits ? st[lane + i * 64] : make_double2(none, 0.0);
   float m = -__builtin_huge_valf();
-  for (int i = lane; i < splits; i += 64) m = fmaxf(m, (float)st[i].x);
+#pragma unroll
+  for (int i = 0; i < kKeep; ++i) m = fmaxf(m, (float)v[i].x);
+  for (int i = lane + kKeep * 64; i < splits; i += 64) m = fmaxf(m, (float)st[i].x);
   m = wave_max(m);
   double s = 0.0;
   const Weigher weigh(s_pow, m, it2);
-  for (int i = lane; i < splits; i += 64) {
-    const double2 v = st[i];
-    s += v.x > -__builtin_huge_val() && v.x < __builtin_huge_val() ? v.y * weigh((float)v.x) : v.y;
-  }
+  auto add = [&](const double2 c) { s += c.x > none && c.x < -none ? c.y * weigh((float)c.x) : c.y; };
+#pragma unroll
+  for (int i = 0; i < kKeep; ++i) add(v[i]);
+  for (int i = lane + kKeep * 64; i < splits; i += 64) add(st[i]);
   mx = m;
   sum = wave_sum(s);
 }
@@ -369,7 +412,7 @@ __device__ __forceinline__ void row_stat(const double2* st, int splits, const do
 template <int NT>
 __global__ __launch_bounds__(NT) void sampled_walk_kernel(SampledArgs a) {
   constexpr int kWalkThreads = NT;
-  __shared__ double s_pow[32];
+  __shared__ double s_pow[kTable];
   load_powers(s_pow);
   __shared__ int s_parent[kTreeNodes], s_token[kTreeNodes], s_next[kTreeNodes], s_first[kTreeNodes];
   __shared__ float s_max[kTreeNodes], s_u[kTreeNodes], s_q[kTreeNodes];
@@ -401,6 +444,8 @@ __global__ __launch_bounds__(NT) void sampled_walk_kernel(SampledArgs a) {
   int last = 0, len = -1;
   double c = 0.0;
   if (!bad) {
+    // on its way while the rows are summed
+    const float first_logit = tid + 1 < n ? logit(a, b0 + s_parent[tid + 1], s_token[tid + 1]) : 0.f;
     for (int i = tid >> 6; i < n; i += kWalkThreads / 64) {
       float mx;
       double sum;
@@ -422,7 +467,7 @@ __global__ __launch_bounds__(NT) void sampled_walk_kernel(SampledArgs a) {
     __syncthreads();
     for (int i = tid + 1; i < n; i += kWalkThreads) {
       const int up = s_parent[i], row = b0 + up;
-      s_p[i] = Weigher(s_pow, s_max[up], it2)(logit(a, row, s_token[i])) / s_sum[up];
+      s_p[i] = Weigher(s_pow, s_max[up], it2)(i == tid + 1 ? first_logit : logit(a, row, s_token[i])) / s_sum[up];
       if (a.draft) s_q[i] = a.draft[(size_t)row * a.vocab + s_token[i]];
     }
     __syncthreads();
@@ -571,7 +616,7 @@ __global__ __launch_bounds__(NT) void sampled_walk_kernel(SampledArgs a) {
 // The next token of each tree whose drafts were drawn: from the last row's
 // max(p - c q, 0), or from p where nothing of that is left (by rounding).
 __global__ __launch_bounds__(kThreads) void sampled_draw_kernel(SampledArgs a) {
-  __shared__ double s_red[kWaves], s_rest, s_pow[32];
+  __shared__ double s_red[kWaves], s_rest, s_pow[kTable];
   __shared__ int s_last, s_int[2];
   const int t = blockIdx.y, tid = threadIdx.x, lane = tid & 63;
   const int split = blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane(tid >> 6);
