@@ -356,7 +356,8 @@ w12_status tree_accept(int32_t num_trees, const int32_t *node_off,
  *           8-bit codes of whole blocks of page_tokens committed tokens,
  *           W12_KV_E4M3 (OCP e4m3) or W12_KV_INT8;
  *   scales  [layers][num_pages][kv_heads][2] fp32: a code stands for
- *           code * scale, one scale per block, head and K or V;
+ *           code * scale, one scale per block, head and K or V, at least
+ *           2^-90 (or NaN: the block reads as NaN);
  *   recent  [layers][slots][kv_heads][2][recent_rows * head_dim] bf16: the
  *           committed tokens of a sequence's unfinished block (its first
  *           len % page_tokens rows), then the rows of the current step.
@@ -379,8 +380,10 @@ w12_status tree_accept(int32_t num_trees, const int32_t *node_off,
  * row_off[s + 1]) of total_rows (at most 512, at most 512 sequences), a tree
  * with tree-local parents as in tree_accept, or, with parent NULL, a chain
  * (row i follows row i - 1: prompts, plain decoding, chains of drafts). slot
- * [num_seq] names each sequence's slot (NULL: its own index). Rows of no
- * sequence are left as they are.
+ * [num_seq] names each sequence's slot (NULL: its own index). row_off
+ * ascends; a sequence whose range runs backwards, leaves [0, total_rows) or
+ * meets an earlier sequence's has no rows. Rows of no sequence are left as
+ * they are.
  */
 typedef enum { W12_KV_E4M3 = 0, W12_KV_INT8 = 1 } w12_kvtype;
 
@@ -406,7 +409,7 @@ typedef struct w12_kv_cache {
  *        position len + d. The first rot_dim dims (even) of each query and
  *        key head turn in pairs (i, i + rot_dim / 2), or (2 i, 2 i + 1) if
  *        interleaved; computed in fp32, rounded to bf16 once.
- *   q    [total_rows][q_heads][head_dim] bf16 out: the rotated queries.
+ *   q    [total_rows][q_heads][head_dim] bf16 out: the rotated queries; not qkv's memory.
  * Device-detected, reported as NaN queries: an invalid tree, a slot outside
  * [0, slots) or of an earlier sequence of the call, a length outside the
  * page table, more rows than recent_rows - len % page_tokens (nothing of such
@@ -433,12 +436,13 @@ w12_status w12_kv_attention_workspace(const w12_kv_cache *cache, int32_t num_seq
  * sequences over workgroups is in a fixed order: results are bitwise
  * reproducible.
  *   q    [total_rows][q_heads][head_dim] bf16 (w12_kv_append's output).
- *   out  [total_rows][q_heads * head_dim] bf16: the x of the Wo product.
+ *   out  [total_rows][q_heads * head_dim] bf16: the x of the Wo product; not q's memory.
  *   ws   workspace of >= w12_kv_attention_workspace bytes, 256-byte aligned,
  *        content ignored.
  * Device-detected, reported as NaN outputs of the sequence: what w12_kv_append
  * lists (a slot named twice is allowed here), and a page id outside
- * [0, num_pages). A block with a NaN scale reads as NaN.
+ * [0, num_pages). Weighted values are summed before they are normalised:
+ * values beyond 2^100 may come out as infinities or NaN.
  */
 w12_status w12_kv_attention(const w12_kv_cache *cache, int32_t layer, int32_t num_seq, const int32_t *slot,
                             const int32_t *row_off, int32_t total_rows, const int32_t *parent, const uint16_t *q,
@@ -452,14 +456,15 @@ w12_status w12_kv_attention(const w12_kv_cache *cache, int32_t layer, int32_t nu
  * accept_len + 1 rows) join its committed tokens in order. Every block that
  * becomes full is quantised into its page (page_table[slot][len / page_tokens
  * ...] must name pages for them): scale = the smallest power of two with
- * amax <= 448 scale (e4m3, at least 2^-126) or amax / 127 (int8), 1 for a block
+ * amax <= 448 scale (e4m3) or amax / 127 (int8), at least 2^-90, 1 for a block
  * of zeros; code = value / scale, rounded to nearest even. A block that holds
  * an infinity or NaN gets scale NaN. The rows left move to the front of the
  * recent rows.
  *   len_out [slots] out: the new length of each sequence's slot, other
  *           entries left as they are; may be the cache's own len.
  * accept_len -1 (a refused tree) keeps nothing. Device-detected, reported as
- * length -1 with nothing written: what w12_kv_append lists (trees aside), an
+ * length -1 with nothing written (a slot named twice: its first sequence
+ * stands): what w12_kv_append lists (trees aside), an
  * accept_len or path outside the sequence's rows or not ascending from row 0,
  * a page id outside [0, num_pages), no room in the page table.
  */

@@ -80,11 +80,11 @@ def quantise(x: np.ndarray, int8: bool):
     if amax == 0:
         return np.zeros_like(x, np.float64), np.float32(1)
     if int8:
-        scale = np.float32(np.float32(amax) / np.float32(127))
+        scale = max(np.float32(np.float32(amax) / np.float32(127)), np.float32(2.0 ** -90))
         # one fp32 division, then round half to even
         q = np.rint((x.astype(np.float32) / scale).astype(np.float64))
         return np.clip(q, -127, 127), scale
-    e = -126
+    e = -90
     while amax > 448 * 2.0 ** e:
         e += 1
     scale = 2.0 ** e
@@ -114,7 +114,8 @@ def attention(q: np.ndarray, k: np.ndarray, v: np.ndarray, see: np.ndarray, scal
 
 def attention_tolerance(out, av, sz, tokens: int, dim: int):
     """|got - out| of the device's attention, from its roundings: the
-    probabilities and the output are rounded to bf16 (2^-8 each); a score is
+    probabilities (times their value's scale) and the output are rounded to
+    bf16 (2^-8 each; the sum is taken over the rounded ones); a score is
     an fp32 sum of dim exact products, so off by dim 2^-24 sum |q k|, and
     scaled in fp32 (3 roundings of |score| <= sum |q k|); an exponent off by x
     changes a probability by e^x - 1, in the sums above and below (twice); the

@@ -19,6 +19,7 @@ def w12():
 FAKE = ctypes.c_void_p(0x1000)  # never dereferenced: validation fails first
 ODD = ctypes.c_void_p(0x1002)
 NULL = ctypes.c_void_p(0)
+FAR = ctypes.c_void_p(1 << 40)
 
 
 def cache(w12, **kw):
@@ -58,22 +59,23 @@ def test_no_cache(w12):
 def test_append_arguments(w12):
     L, d = w12.lib(), ctypes.byref(cache(w12))
 
-    def go(layer=0, seqs=1, off=FAKE, rows=4, qkv=FAKE, kind=0, heads=8, rope=FAKE, positions=16, rot=128, q=FAKE):
+    def go(layer=0, seqs=1, off=FAKE, rows=4, qkv=FAKE, kind=0, heads=8, rope=FAKE, positions=16, rot=128, q=FAR):
         return L.w12_kv_append(d, layer, seqs, NULL, off, rows, NULL, qkv, kind, heads, rope, positions, rot, 0, q, NULL)
     for kw in (dict(layer=-1), dict(layer=2), dict(seqs=0), dict(seqs=513), dict(off=NULL), dict(rows=0), dict(rows=513),
                dict(qkv=NULL), dict(qkv=ODD), dict(kind=2), dict(heads=0), dict(heads=6), dict(heads=260), dict(rope=NULL),
-               dict(positions=0), dict(rot=0), dict(rot=3), dict(rot=130), dict(q=NULL), dict(q=ODD)):
+               dict(positions=0), dict(rot=0), dict(rot=3), dict(rot=130), dict(q=NULL), dict(q=ctypes.c_void_p((1 << 40) + 2)),
+               dict(q=FAKE), dict(q=ctypes.c_void_p(0x1000 + 16))):  # over qkv
         assert go(**kw) == w12.W12_EINVAL, kw
 
 
 def test_attention_arguments(w12):
     L, d = w12.lib(), ctypes.byref(cache(w12))
 
-    def go(layer=0, seqs=1, off=FAKE, rows=4, q=FAKE, heads=8, scale=0.1, out=FAKE, ws=FAKE):
+    def go(layer=0, seqs=1, off=FAKE, rows=4, q=FAKE, heads=8, scale=0.1, out=FAR, ws=FAKE):
         return L.w12_kv_attention(d, layer, seqs, NULL, off, rows, NULL, q, heads, scale, out, ws, 0, NULL)
     for kw in (dict(layer=2), dict(seqs=0), dict(seqs=513), dict(off=NULL), dict(rows=0), dict(rows=513), dict(q=NULL),
                dict(q=ODD), dict(heads=0), dict(heads=7), dict(scale=0.0), dict(scale=-1.0), dict(scale=float("nan")),
-               dict(scale=float("inf")), dict(out=NULL), dict(out=ODD), dict(ws=NULL), dict(ws=ctypes.c_void_p(0x1010))):
+               dict(scale=float("inf")), dict(out=NULL), dict(out=ctypes.c_void_p((1 << 40) + 2)), dict(out=FAKE), dict(ws=NULL), dict(ws=ctypes.c_void_p(0x1010))):
         assert go(**kw) == w12.W12_EINVAL, kw
     sz = ctypes.c_size_t(0)
     for seqs, rows, heads in ((0, 4, 8), (1, 0, 8), (1, 513, 8), (1, 4, 9)):

@@ -537,3 +537,90 @@ def test_binding_refusals(w12):
         w12.KvCache(c.pages, c.scales[:, :3].contiguous(), c.recent, c.page_table, c.length, 64)
     with pytest.raises(TypeError):
         w12.KvCache(c.pages.view(torch.uint8), c.scales, c.recent, c.page_table, c.length, 64)
+
+
+def test_offsets_that_are_no_ranges(w12):
+    """Sequences whose range runs backwards, leaves the rows or meets an
+    earlier one's have no rows; the others stand, in every call."""
+    import torch
+    say("offsets")
+    sv = Serving(w12, 4, 1, 2, 64, 32, seed=21)
+    sv.step([20, 20, 20, 20])
+    x = torch.tensor(sv.rng.randn(12, 4 * 64), dtype=torch.float32, device=DEV)
+    slot, acc = i32(sv.slot), i32([2, 2, 2, 2])
+
+    def run(off):
+        start = [t.clone() for t in (sv.cache.recent, sv.cache.length)]
+        q = torch.full((12, 2, 64), 7.0, dtype=torch.bfloat16, device=DEV)
+        w12.w12_kv_append(sv.cache, 0, x, i32(off), sv.rope_t, 2, slot=slot, out=q)
+        out = torch.full((12, 128), 7.0, dtype=torch.bfloat16, device=DEV)
+        w12.w12_kv_attention(sv.cache, 0, q, i32(off), slot=slot, out=out)
+        length = w12.w12_kv_commit(sv.cache, i32(off), acc, slot=slot, length_out=sv.cache.length.clone(), rows=12)[slot.long()]
+        recent = sv.cache.recent.clone()
+        for t, b in zip((sv.cache.recent, sv.cache.length), start):
+            t.copy_(b)
+        return q, out, length.tolist(), recent
+    good = run([0, 3, 6, 9, 12])
+    assert good[2] == [23] * 4
+    # (offsets, rows of sequences that stand, lengths after)
+    for off, kept, length in (([0, 3, 99, 9, 12], [0, 1, 2, 9, 10, 11], [23, -1, -1, 23]),
+                              ([0, 3, -5, 9, 12], [0, 1, 2, 9, 10, 11], [23, -1, -1, 23]),
+                              ([0, 3, 1, 9, 12], [0, 1, 2, 9, 10, 11], [23, -1, -1, 23]),
+                              ([6, 9, 0, 6, 12], [], [23, -1, 23, -1])):
+        q, out, got, _ = run(off)
+        assert got == length, off
+        if kept:
+            rest = np.setdiff1d(np.arange(12), kept)
+            assert torch.equal(q[kept], good[0][kept]) and torch.equal(out[kept], good[1][kept]), off
+            assert (q[rest] == 7).all() and (out[rest] == 7).all(), off
+        else:  # rows 6 .. 9 are sequence 0's now, 0 .. 6 sequence 2's
+            assert torch.isfinite(out[:9].float()).all() and (out[:9] != 7).any(1).all() and (out[9:] == 7).all()
+
+
+def test_output_over_an_input_is_refused(w12):
+    import torch
+    say("overlap")
+    c = w12.kv_cache(1, 2, 64, 4, 1, 2, 32, 16, False, DEV)
+    off, rope = i32([0, 4]), torch.zeros(8, 64, device=DEV)
+    buf = torch.zeros(4, 8 * 64, dtype=torch.bfloat16, device=DEV)
+    with pytest.raises(w12.W12Error):
+        w12.w12_kv_append(c, 0, buf, off, rope, 4, out=buf)
+    q = torch.zeros(4, 4, 64, dtype=torch.bfloat16, device=DEV)
+    with pytest.raises(w12.W12Error):
+        w12.w12_kv_attention(c, 0, q, off, out=q)
+
+
+def test_a_cache_keeps_its_arrays(w12):
+    """The description holds addresses: another tensor in place of one of the
+    arrays would be passed by."""
+    c = w12.kv_cache(1, 2, 64, 4, 1, 2, 32, 16, False, DEV)
+    for name in ("pages", "scales", "recent", "page_table", "length", "head_dim"):
+        with pytest.raises(AttributeError):
+            setattr(c, name, getattr(c, name))
+
+
+@pytest.mark.parametrize("size", [2.0 ** -80, 2.0 ** -95, 2.0 ** -119, 2.0 ** -130])
+def test_tiny_blocks(w12, size):
+    """A block of tiny values next to an ordinary one: its tokens keep their
+    share of the softmax, whatever its scale."""
+    import torch
+    say("tiny", size)
+    for int8 in (False, True):
+        dim, page = 64, 32
+        sv = Serving(w12, 1, 1, 1, dim, page, int8, seed=22)
+        x = sv.rng.randn(2 * page, 3 * dim)
+        x[:page, 2 * dim:] *= size
+        rope = torch.tensor(np.concatenate([np.ones((256, dim // 2)), np.zeros((256, dim // 2))], 1), dtype=torch.float32, device=DEV)
+        xt, vals = bf16(x)
+        w12.w12_kv_append(sv.cache, 0, xt, i32([0, 2 * page]), rope, 1, slot=i32(sv.slot))
+        w12.w12_kv_commit(sv.cache, i32([0, 2 * page]), i32([2 * page - 1]), slot=i32(sv.slot))
+        sv.state[0][0][0].commit(vals[:, dim:2 * dim], vals[:, 2 * dim:])
+        sv.check()
+        # a last row with a zero query and value: every score is zero
+        q = w12.w12_kv_append(sv.cache, 0, bf16(np.zeros((1, 3 * dim)))[0], i32([0, 1]), rope, 1, slot=i32(sv.slot))
+        got = f64(w12.w12_kv_attention(sv.cache, 0, q, i32([0, 1]), slot=i32(sv.slot)))
+        seq, n = sv.state[0][0][0], 2 * page + 1
+        ref, av = seq.v.sum(0) / n, np.abs(seq.v).sum(0) / n
+        # scores of zero: no rounding but the probabilities', the sums' and the output's
+        lim = KV.attention_tolerance(ref, av[None], np.zeros(1), n, dim)[0]
+        assert (np.abs(got[0] - ref) <= lim).all()

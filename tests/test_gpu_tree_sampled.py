@@ -204,3 +204,18 @@ def test_temperatures_of_every_size(w12, drafted):
         f["draft"][:, [40, 2100]] += np.float32(0.25)
     got = both(w12, f)
     assert (got[0] >= 0).all()
+
+
+def test_offsets_that_are_no_ranges(w12):
+    """A tree whose range leaves the nodes or meets an earlier tree's is
+    refused, and takes no row from the others."""
+    say("offsets")
+    f = forest(18, [6] * 4, 1500, False)
+    want = both(w12, f)
+    f["off"] = np.array([0, 30, 6, 12, 18, 24, 6, 9], np.int32)  # out of range, backwards, trees 1 .. 3, backwards, rows of tree 1
+    f["temp"] = np.array([9.0, 9.0, *f["temp"][1:], 9.0, 9.0], np.float32)
+    f["ub"] = np.array([0.5, 0.5, *f["ub"][1:], 0.5, 0.5], np.float32)
+    got = call(w12, f)
+    assert got[0].tolist() == [-1, -1, *want[0][1:], -1, -1]
+    assert got[2].tolist() == [-1, -1, *want[2][1:], -1, -1]
+    assert np.array_equal(got[1][6:], want[1][6:])

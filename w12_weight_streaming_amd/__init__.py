@@ -457,13 +457,15 @@ def _run(index: int, what: str, *args) -> None:
         raise W12Error(status, what)
 
 
-@dataclass
+@dataclass(frozen=True, eq=False)  # the description holds the arrays' addresses
 class KvCache:
     """Device-resident KV cache: the arrays of include/w12.h. pages is
     [layers, num_pages, kv_heads, 2, page_tokens * head_dim] float8_e4m3fn or
     int8, scales its fp32 [layers, num_pages, kv_heads, 2], recent
     [layers, slots, kv_heads, 2, recent_rows * head_dim] bfloat16, page_table
-    [slots, max_pages] int32, length [slots] int32."""
+    [slots, max_pages] int32, length [slots] int32. The arrays stay the same;
+    their contents may be written at any time (a new sequence: its row of the
+    page table, its length 0)."""
     pages: torch.Tensor
     scales: torch.Tensor
     recent: torch.Tensor
@@ -477,7 +479,7 @@ class KvCache:
         pages, scales, recent, table, length, dim = (self.pages, self.scales, self.recent, self.page_table, self.length,
                                                      self.head_dim)
         at = _get(pages, pages.dtype, "pages", 5, None)
-        self.index = index = pages.get_device()
+        index = pages.get_device()
         ats = (at, _get(scales, _F32, "scales", 4, index), _get(recent, _BF16, "recent", 5, index),
                _get(table, _I32, "page_table", 2, index), _get(length, _I32, "length", 1, index))
         layers, num_pages, kv, two, page = pages.shape
@@ -486,10 +488,10 @@ class KvCache:
         if (two != 2 or dim < 1 or page % dim or scales.shape != (layers, num_pages, kv, 2) or length.shape[0] != slots
                 or rows[0] != layers or rows[1] != slots or rows[2] != kv or rows[3] != 2 or rows[4] % dim):
             raise ValueError("the cache's arrays differ in shape")
-        self.kv_heads = kv
-        self._desc = W12KvCache(W12_KV_INT8 if pages.dtype is torch.int8 else W12_KV_E4M3, layers, num_pages, kv,
+        desc = W12KvCache(W12_KV_INT8 if pages.dtype is torch.int8 else W12_KV_E4M3, layers, num_pages, kv,
                                 page // dim, dim, slots, rows[4] // dim, blocks, *ats)
-        self._ref = ctypes.byref(self._desc)
+        for name, value in (("index", index), ("kv_heads", kv), ("_desc", desc), ("_ref", ctypes.byref(desc))):
+            object.__setattr__(self, name, value)
 
     @property
     def device(self):
@@ -595,18 +597,21 @@ def w12_kv_attention(cache: KvCache, layer: int, q: torch.Tensor, row_off: torch
 
 
 def w12_kv_commit(cache: KvCache, row_off: torch.Tensor, accept_len: torch.Tensor, path: torch.Tensor | None = None,
-                  slot: torch.Tensor | None = None, length_out: torch.Tensor | None = None) -> torch.Tensor:
+                  slot: torch.Tensor | None = None, length_out: torch.Tensor | None = None,
+                  rows: int | None = None) -> torch.Tensor:
     """Keeps the accepted rows of the step (tree_accept's accept_len and
     path; path None: each sequence's first accept_len + 1 rows) in every
-    layer. Writes the new lengths into length_out [slots] (the cache's own by
+    layer. rows: how many the step had, known from path if there is one (at
+    most 512 otherwise). Writes the new lengths into length_out [slots] (the cache's own by
     default) and returns it."""
     index = cache.index
     at_off = _get(row_off, _I32, "row_off", 1, index)
     seqs = row_off.shape[0] - 1
-    if path is None:
-        at_path, rows = 0, MAX_ROWS
-    else:
-        at_path, rows = _get(path, _I32, "path", 1, index), path.shape[0]
+    at_path = 0
+    if path is not None:
+        at_path, rows = _get(path, _I32, "path", 1, index, rows), path.shape[0]
+    elif rows is None:
+        rows = MAX_ROWS
     if length_out is None:
         length_out = cache.length
     _run(index, "w12_kv_commit", cache._ref, seqs, 0 if slot is None else _get(slot, _I32, "slot", 1, index, seqs), at_off,

@@ -8,6 +8,10 @@
 namespace {
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+bool apart(const void* p, size_t np, const void* q, size_t nq) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return a + np <= b || b + nq <= a;
+}
 w12_status st(hipError_t e) { return e == hipSuccess ? W12_OK : W12_EHIP; }
 
 // Sizes of a cache that the kernels' indexing holds for.
@@ -64,6 +68,9 @@ w12_status w12_kv_append(const w12_kv_cache* cache, int32_t layer, int32_t num_s
   if (!qkv || !q || !rope || (qkv_type != W12_Y_F32 && qkv_type != W12_Y_BF16)) return W12_EINVAL;
   if (positions < 1 || rot_dim < 2 || rot_dim > cache->head_dim || rot_dim % 2 != 0) return W12_EINVAL;
   if (!aligned(qkv, 16) || !aligned(q, 16) || !aligned(rope, 4)) return W12_EINVAL;
+  const size_t heads = (size_t)total_rows * cache->head_dim;
+  if (!apart(q, heads * q_heads * 2, qkv, heads * (q_heads + 2 * cache->kv_heads) * (qkv_type == W12_Y_F32 ? 4 : 2)))
+    return W12_EINVAL;
   w12::AppendArgs a{};
   a.c = args_of(cache);
   a.st = {row_off, slot, parent, num_seq, total_rows};
@@ -86,7 +93,7 @@ w12_status w12_kv_attention_workspace(const w12_kv_cache* cache, int32_t num_seq
     return W12_EINVAL;
   const int cu = w12::device_cu_count();
   if (cu <= 0) return W12_EHIP;
-  *bytes = w12::plan_kv_attention(args_of(cache), num_seq, total_rows, q_heads, cu).ws_bytes;
+  *bytes = w12::plan_kv_attention(args_of(cache), cu).ws_bytes;
   return W12_OK;
 }
 
@@ -99,12 +106,15 @@ w12_status w12_kv_attention(const w12_kv_cache* cache, int32_t layer, int32_t nu
     return W12_EINVAL;
   if (!q || !out || !ws || !(scale > 0.0f && scale < __builtin_huge_valf())) return W12_EINVAL;
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(ws, 256)) return W12_EINVAL;
+  const size_t bytes = (size_t)total_rows * q_heads * cache->head_dim * 2;
+  if (!apart(q, bytes, out, bytes)) return W12_EINVAL;
   const int cu = w12::device_cu_count();
   if (cu <= 0) return W12_EHIP;
   w12::AttentionArgs a{};
   a.c = args_of(cache);
-  const w12::AttentionPlan p = w12::plan_kv_attention(a.c, num_seq, total_rows, q_heads, cu);
+  const w12::AttentionPlan p = w12::plan_kv_attention(a.c, cu);
   if (ws_bytes < p.ws_bytes) return W12_ENOSPC;
+  if (!apart(ws, p.ws_bytes, out, bytes) || !apart(ws, p.ws_bytes, q, bytes)) return W12_EINVAL;
   a.st = {row_off, slot, parent, num_seq, total_rows};
   a.layer = layer;
   a.q = q;

@@ -217,8 +217,16 @@ __global__ __launch_bounds__(kThreads, 2) void kv_attention_kernel(AttentionArgs
   {
     static_assert(kThreads == kStepRows);
     int64_t mine = 0;
+    SeqView v{};
+    int back = 0;
     if (tid < a.st.num_seq) {
-      const SeqView v = seq_view(a.c, a.st, tid);
+      v = seq_view(a.c, a.st, tid);
+      back = a.st.row_off[tid] > a.st.row_off[tid + 1];
+    }
+    if (__syncthreads_or(back))  // only then can two sequences share rows
+      for (int j = 0; j < tid && tid < a.st.num_seq; ++j)
+        if (rows_meet(a.st.row_off, a.st.total, j, v.row0, v.rows)) v.rows = 0;
+    if (tid < a.st.num_seq) {
       SeqInfo n;
       n.len = v.ok ? v.len : -1;
       n.slot = v.slot;
@@ -784,8 +792,7 @@ hipError_t launch_dim(const AttentionArgs& a, hipStream_t s) {
 
 }  // namespace
 
-AttentionPlan plan_kv_attention(const KvArgs& c, int num_seq, int total, int q_heads, int num_cu) {
-  (void)num_seq; (void)total; (void)q_heads;
+AttentionPlan plan_kv_attention(const KvArgs& c, int num_cu) {
   AttentionPlan p{};
   p.G = num_cu;
   p.off_part = ((size_t)p.G * sizeof(SplitItem) + 255) & ~size_t(255);

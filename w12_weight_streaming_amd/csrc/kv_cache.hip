@@ -56,16 +56,17 @@ __global__ __launch_bounds__(kAppendThreads) void kv_append_kernel(AppendArgs a)
   }
   __syncthreads();
   for (int s = tid; s < a.st.num_seq; s += kAppendThreads)
-    if (row >= a.st.row_off[s] && row < a.st.row_off[s + 1]) atomicMin(&s_seq, s);
+    if (rows_meet(a.st.row_off, a.st.total, s, row, 1)) atomicMin(&s_seq, s);
   __syncthreads();
   const int s = s_seq;
   if (s >= a.st.num_seq) return;  // a row of no sequence stays as it is
   const SeqView v = seq_view(a.c, a.st, s);
-  int bad = v.ok ? 0 : 1;
+  int bad = v.ok ? 0 : 1, none = 0;
   const int r = row - v.row0;
-  if (a.st.slot)  // a slot of an earlier sequence would be written twice
-    for (int j = tid; j < s; j += kAppendThreads)
-      if (a.st.slot[j] == v.slot) bad = 1;
+  for (int j = tid; j < s; j += kAppendThreads) {
+    if (rows_meet(a.st.row_off, a.st.total, j, v.row0, v.rows)) none = 1;
+    if (a.st.slot && a.st.slot[j] == v.slot) bad = 1;  // a slot of an earlier sequence would be written twice
+  }
   int depth = r;
   if (a.st.parent && v.ok) {
     for (int i = tid; i < v.rows; i += kAppendThreads) {
@@ -74,9 +75,11 @@ __global__ __launch_bounds__(kAppendThreads) void kv_append_kernel(AppendArgs a)
       if (i == 0 ? p != -1 : (p < 0 || p >= i)) bad = 1;
     }
   }
-  if (bad) s_bad = 1;
+  if (bad) atomicOr(&s_bad, 1);
+  if (none) atomicOr(&s_bad, 2);
   __syncthreads();
   bad = s_bad;
+  if (bad & 2) return;
   if (a.st.parent && !bad) {
     depth = 0;
     for (int i = r; i > 0; i = s_parent[i]) ++depth;
@@ -143,6 +146,9 @@ __global__ __launch_bounds__(kAppendThreads) void kv_append_kernel(AppendArgs a)
 // ---------------------------------------------------------------------------- commit
 
 constexpr int kCommitThreads = 256;
+// A block's least scale, as a power of two: the attention multiplies its
+// probabilities by the scale, and they must not fall out of fp32's range.
+constexpr int kLeastScale = -90;
 
 // What a sequence commits, the same in every workgroup: n accepted rows and
 // the recent place each comes from. Invalid where the path is no ascending
@@ -161,9 +167,8 @@ __device__ __forceinline__ CommitView commit_view(const CommitArgs& a, int s, in
   const int acc = a.accept_len[s];
   w.n = w.v.ok ? acc + 1 : 0;
   int bad = (!w.v.ok || acc < -1 || acc >= w.v.rows) ? 1 : 0;
-  if (a.st.slot)
-    for (int j = tid; j < s; j += blockDim.x)
-      if (a.st.slot[j] == w.v.slot) bad = 1;
+  for (int j = tid; j < s; j += blockDim.x)
+    if ((a.st.slot && a.st.slot[j] == w.v.slot) || rows_meet(a.st.row_off, a.st.total, j, w.v.row0, w.v.rows)) bad = 1;
   if (!bad) {
     for (int j = tid; j < w.n; j += blockDim.x) {
       int p = j;
@@ -293,9 +298,9 @@ __global__ __launch_bounds__(kCommitThreads) void kv_commit_kernel(CommitArgs a)
       if (a.c.kind == 0) {
         int e;
         const float f = frexpf(amax, &e);
-        scale = ldexpf(1.0f, max(e - 9 + (f > 0.875f ? 1 : 0), -126));
+        scale = ldexpf(1.0f, max(e - 9 + (f > 0.875f ? 1 : 0), kLeastScale));
       } else {
-        scale = __fdiv_rn(amax, 127.0f);
+        scale = fmaxf(__fdiv_rn(amax, 127.0f), ldexpf(1.0f, kLeastScale));
       }
     }
     const int id = a.c.table[(size_t)w.v.slot * a.c.max_pages + w.v.full + b];

@@ -92,14 +92,14 @@ struct AttentionPlan {
   int G;
   size_t off_part, off_ml, ws_bytes;
 };
-AttentionPlan plan_kv_attention(const KvArgs& c, int num_seq, int total, int q_heads, int num_cu);
+AttentionPlan plan_kv_attention(const KvArgs& c, int num_cu);
 hipError_t launch_kv_attention(const AttentionArgs& a, hipStream_t s);
 
 size_t tree_sampled_ws_bytes(int num_trees, int total, int vocab);
 hipError_t launch_tree_sampled(const SampledArgs& a, hipStream_t s);
 
 #ifdef __HIPCC__
-// Byte-free places of a row's dims in the fragment order that pages and
+// Places (in elements) of a row's dims in the fragment order that pages and
 // recent rows share: keys of 32 tokens x 32 dims are [2 halves of 16
 // dims][32 tokens][16 dims], values [2 halves][32 dims][16 tokens], half h of
 // the values holding tokens 8 i + 4 h + j (j < 4) at i * 4 + j. A fragment is
@@ -147,6 +147,12 @@ __device__ __forceinline__ SeqView seq_view(const KvArgs& c, const StepArgs& st,
   v.tail = v.len - v.full * c.page;
   if (v.tail + v.rows > c.recent_rows) v.ok = false;
   return v;
+}
+// Rows [row0, row0 + rows) meet those of sequence j (where offsets run
+// backwards): the later of the two has no rows then, as one whose range is none.
+__device__ __forceinline__ bool rows_meet(const int32_t* off, int total, int j, int row0, int rows) {
+  const int b0 = off[j], b1 = off[j + 1];
+  return b0 >= 0 && b1 <= total && b0 < b1 && b0 < row0 + rows && b1 > row0;
 }
 #endif
 

@@ -353,7 +353,7 @@ __global__ __launch_bounds__(kThreads) void sampled_stat_kernel(SampledArgs a, i
   if (first >= end) return;
   int tree = -1;  // the first that holds the row
   for (int t = 0; t < a.num_trees && tree < 0; t += 64) {
-    const bool in = t + lane < a.num_trees && row >= a.node_off[t + lane] && row < a.node_off[t + lane + 1];
+    const bool in = t + lane < a.num_trees && rows_meet(a.node_off, a.total, t + lane, row, 1);
     const uint64_t hit = __ballot(in);
     if (hit) tree = t + __builtin_ctzll(hit);
   }
@@ -425,7 +425,11 @@ __global__ __launch_bounds__(NT) void sampled_walk_kernel(SampledArgs a) {
   char* ws = static_cast<char*>(a.ws);
   State* state = reinterpret_cast<State*>(ws + L.off_state) + t;
   const int b0 = a.node_off[t], b1 = a.node_off[t + 1];
-  const bool range_ok = b0 >= 0 && b0 <= b1 && b1 <= a.total;
+  bool range_ok = b0 >= 0 && b0 <= b1 && b1 <= a.total;
+  int meets = 0;
+  if (range_ok)
+    for (int j = tid; j < t; j += kWalkThreads) meets |= rows_meet(a.node_off, a.total, j, b0, b1 - b0);
+  range_ok = !__syncthreads_or(meets) && range_ok;
   const int n = range_ok ? b1 - b0 : 0;
   const double it = inv_temperature(a, t), it2 = it * kLog2e;
   if (tid == 0) s_bad = (n < 1 || n > kTreeNodes || !(it > 0.0 && it < __builtin_huge_val())) ? 1 : 0;
