@@ -141,15 +141,17 @@ __device__ __forceinline__ void softmax_step(f32x16 (&o)[NB], float& m, float& l
   }
 }
 
-// Most tiles of a block: their queries take 32 KB of LDS.
+// Most tiles of a block. More of them read a page for more rows but split the
+// tokens among fewer waves; at one workgroup a CU the pages come from the caches
+// the second time, so few tiles win (512 prompt rows, 64-dim heads: 97 us with up
+// to 2 or 8 tiles, 94 with 4; 128 dims: 84, 86 with 4).
 template <int DIM>
-constexpr int kBlockTiles = 512 / DIM;
+constexpr int kBlockTiles = DIM == 64 ? 4 : 2;
 
-// Waves along the rows for n tiles: as many as there are (the tokens are read
-// once for all of them) unless that leaves over a seventh of them idle.
-template <int MAX>
-__device__ __forceinline__ int waves_along_rows(int n) {
-  int wr = MAX;
+// Waves along the rows for n tiles: `most`, unless that leaves over a seventh of
+// them idle (6 tiles of 128 dims over 8192 tokens: 39 us as 4 + 2, 30 by twos).
+__device__ __forceinline__ int waves_along_rows(int n, int most) {
+  int wr = most;
   while (wr > 1 && (n <= wr / 2 || ((n + wr - 1) / wr * wr - n) * 7 > n)) wr >>= 1;
   return wr;
 }
@@ -189,7 +191,6 @@ struct Shared {
 template <int DIM, int KIND, bool STREAM>
 __global__ __launch_bounds__(kThreads, 2) void kv_attention_kernel(AttentionArgs a) {
   constexpr int NB = DIM / 32;
-  constexpr int kMaxWr = kBlockTiles<DIM>;
   constexpr int U = DIM == 256 ? 1 : 2;       // groups of 32 tokens a wave takes at a time
   constexpr bool kQueryRegs = DIM <= 128;     // its query operands stay in registers
   __shared__ Shared<DIM> sh;
@@ -205,7 +206,7 @@ __global__ __launch_bounds__(kThreads, 2) void kv_attention_kernel(AttentionArgs
   auto shape_of = [&](const SeqInfo& v) __attribute__((always_inline)) {
     Shape h;
     const int tiles = (v.rows * group + kTile - 1) / kTile;
-    h.wr = waves_along_rows<kMaxWr>(tiles);
+    h.wr = waves_along_rows(tiles, a.most_tiles);
     h.blocks = (tiles + h.wr - 1) / h.wr;
     const int full = v.len / a.c.page, tail = v.len - full * a.c.page;
     h.page_units = v.len < 0 ? 0 : full * per_page;
@@ -801,9 +802,20 @@ AttentionPlan plan_kv_attention(const KvArgs& c, int num_cu) {
   return p;
 }
 
-hipError_t launch_kv_attention(const AttentionArgs& a, hipStream_t s) {
-  // sequences of about one tile read every page once: past the caches
-  const bool stream = (int64_t)a.st.total * (a.q_heads / a.c.kv_heads) <= (int64_t)a.st.num_seq * kTile;
+hipError_t launch_kv_attention(const AttentionArgs& in, hipStream_t s) {
+  AttentionArgs a = in;
+  const int64_t rows = (int64_t)a.st.total * (a.q_heads / a.c.kv_heads);
+  // Items that four or more workgroups share are cut into single tiles: their
+  // pages' second readings are cache hits, and a partial sum is half as large (a
+  // 32-node tree over 32000 tokens, 6 tiles of 256 dims: 59 -> 53 us; of 128
+  // dims over 8192 tokens: 30 -> 25). Where items fill the card, single tiles cost
+  // re-reading (8 trees of 4 tiles over 16000 tokens: 56 -> 77).
+  const bool few = (rows + kTile - 1) / kTile * a.c.kv_heads * 4 <= a.G;
+  a.most_tiles = few ? 1 : a.c.dim == 64 ? 4 : 2;
+  // Sequences whose rows make one block read every page once: past the caches
+  // (batch decode 105 -> 95 us, 24 trees of 2 tiles 70 -> 65), unless more than two
+  // waves share the loads, or two that hold 256 dims and so drift apart (49 -> 55).
+  const bool stream = rows <= (int64_t)a.st.num_seq * kTile * (few || a.c.dim == 256 ? 1 : 2);
   switch (a.c.dim) {
     case 64: return stream ? launch_dim<64, true>(a, s) : launch_dim<64, false>(a, s);
     case 128: return stream ? launch_dim<128, true>(a, s) : launch_dim<128, false>(a, s);

@@ -53,9 +53,10 @@ struct AttentionArgs {
   float scale;
   uint16_t* out;
   void* items;     // [G] the item each workgroup begins and others go on with
-  float* part;     // [2 G][128 rows][dim] partial sums, not normalised
-  float* part_ml;  // [2 G][128 rows][2] their running maxima and sums
+  float* part;     // [2 G][rows of a block][dim] partial sums, not normalised
+  float* part_ml;  // [2 G][rows of a block][2] their running maxima and sums
   int G;           // workgroups
+  int most_tiles;  // of 32 query rows in a block
 };
 
 struct CommitArgs {
