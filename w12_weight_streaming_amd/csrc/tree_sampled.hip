@@ -270,6 +270,40 @@ __device__ __forceinline__ double running_sum(double v, double* s_scan, double& 
   return v;
 }
 
+// What the threads of a workgroup found, one entry a wave. Lanes are told apart
+// by ballots: LDS atomics on one address with a value a lane run lane by lane (a
+// search took 5 us with them, under 1 so).
+template <int NT>
+struct Search {
+  int first[NT / 64], last[NT / 64];
+  double rest[NT / 64];
+};
+constexpr int kNone = 1 << 30;
+// The least `first` and the greatest `last` over the workgroup; both grow with the
+// thread (kNone, -1: none), and `rest` belongs to `first`.
+template <int NT>
+__device__ __forceinline__ void search_join(int& first, int& last, double& rest, Search<NT>& s) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const uint64_t has = __ballot(first != kNone), any = __ballot(last >= 0);
+  if (lane == (has ? __builtin_ctzll(has) : 0)) {
+    s.first[wave] = first;
+    s.rest[wave] = rest;
+  }
+  if (lane == (any ? 63 - __builtin_clzll(any) : 0)) s.last[wave] = last;
+  __syncthreads();
+  first = kNone;
+  last = -1;
+#pragma unroll
+  for (int w = NT / 64 - 1; w >= 0; --w) {
+    if (s.first[w] != kNone) {
+      first = s.first[w];
+      rest = s.rest[w];
+    }
+    if (last < 0) last = s.last[w];
+  }
+  __syncthreads();
+}
+
 // The first of `splits` chunks, value(i) each, at which the running sum passes
 // `target`, and what of the target is left in it; else the last chunk that
 // holds anything, with an infinite rest.
@@ -278,61 +312,48 @@ struct Found {
   double rest;
 };
 template <int NT, typename F>
-__device__ __forceinline__ Found find_chunk(F value, int splits, double target, double* s_scan, int* s_int, double* s_rest) {
+__device__ __forceinline__ Found find_chunk(F value, int splits, double target, double* s_scan, Search<NT>& s) {
   const int tid = threadIdx.x;
-  if (tid == 0) {
-    s_int[0] = splits;
-    s_int[1] = -1;
-    *s_rest = __builtin_huge_val();
-  }
-  __syncthreads();
   double before = 0.0;
+  Found f{0, __builtin_huge_val()};
   for (int i0 = 0; i0 < splits; i0 += NT) {
-    const double v = i0 + tid < splits ? value(i0 + tid) : 0.0;
+    const int i = i0 + tid;
+    const double v = i < splits ? value(i) : 0.0;
     double whole;
     const double upto = before + running_sum<NT>(v, s_scan, whole);
-    if (v > 0.0) {
-      atomicMax(&s_int[1], i0 + tid);
-      if (upto > target) atomicMin(&s_int[0], i0 + tid);
+    int first = v > 0.0 && upto > target ? i : kNone, last = v > 0.0 ? i : -1;
+    double rest = target - (upto - v);
+    search_join<NT>(first, last, rest, s);
+    if (first != kNone) {
+      f.chunk = first;
+      f.rest = rest;
+      break;
     }
-    __syncthreads();
-    if (s_int[0] == i0 + tid && s_int[0] < splits) *s_rest = target - (upto - v);
-    __syncthreads();
-    if (s_int[0] < splits) break;
+    if (last >= 0) f.chunk = last;
     before += whole;
   }
-  Found f;
-  f.chunk = max(0, s_int[0] < splits ? s_int[0] : s_int[1]);
-  f.rest = *s_rest;
   return f;
 }
 // The first of N tokens a thread (weights w, in order over the threads) at
 // which the running sum passes `rest`; else the last with any weight.
 template <int NT, int N>
-__device__ __forceinline__ int find_token(const double (&w)[N], double rest, double* s_scan, int* s_int) {
+__device__ __forceinline__ int find_token(const double (&w)[N], double rest, double* s_scan, Search<NT>& s) {
   const int tid = threadIdx.x;
   double own = 0.0, whole;
 #pragma unroll
   for (int i = 0; i < N; ++i) own += w[i];
-  __syncthreads();
-  if (tid == 0) {
-    s_int[0] = NT * N;
-    s_int[1] = -1;
-  }
   double cum = running_sum<NT>(own, s_scan, whole) - own;
-  int pick = NT * N, end = -1;
+  int first = kNone, last = -1;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     cum += w[i];
     if (w[i] > 0.0) {
-      end = tid * N + i;
-      if (pick == NT * N && cum > rest) pick = end;
+      last = tid * N + i;
+      if (first == kNone && cum > rest) first = last;
     }
   }
-  if (pick < NT * N) atomicMin(&s_int[0], pick);
-  if (end >= 0) atomicMax(&s_int[1], end);
-  __syncthreads();
-  return s_int[0] < NT * N ? s_int[0] : s_int[1];
+  search_join<NT>(first, last, rest, s);
+  return first != kNone ? first : last;
 }
 
 // (max, sum of exp(x - max)) of chunks of a row: `each` neighbouring ones a
@@ -409,7 +430,7 @@ __device__ __forceinline__ void row_stat(const double2* st, int splits, const do
 // the nodes' probabilities (a thread each) come first, so that the walk itself
 // reads nothing but LDS, save where a drawn draft is rejected and has siblings
 // (a pass over the row: these trees get 1024 threads, the others 256). Bound by
-// its chain of dependent loads: 20 us for 24 trees of 8 nodes.
+// its chain of dependent loads: 14 us for 24 trees of 8 nodes.
 template <int NT>
 __global__ __launch_bounds__(NT) void sampled_walk_kernel(SampledArgs a) {
   constexpr int kWalkThreads = NT;
@@ -418,9 +439,10 @@ __global__ __launch_bounds__(NT) void sampled_walk_kernel(SampledArgs a) {
   __shared__ int s_parent[kTreeNodes], s_token[kTreeNodes], s_next[kTreeNodes], s_first[kTreeNodes];
   __shared__ float s_max[kTreeNodes], s_u[kTreeNodes], s_q[kTreeNodes];
   __shared__ double s_sum[kTreeNodes], s_p[kTreeNodes];
-  __shared__ double s_red[kWalkThreads / 64], s_fix[kTreeNodes], s_rest;
+  __shared__ double s_red[kWalkThreads / 64], s_fix[kTreeNodes];
+  __shared__ Search<NT> s_search;
   __shared__ uint32_t s_gone[kWalkThreads / 64][kChunk / 32];
-  __shared__ int s_bad, s_kids, s_int[2];
+  __shared__ int s_bad, s_kids;
   const int t = blockIdx.x, tid = threadIdx.x;
   const Layout L = layout_of(a.num_trees, a.total, a.vocab);
   char* ws = static_cast<char*>(a.ws);
@@ -602,7 +624,7 @@ __global__ __launch_bounds__(NT) void sampled_walk_kernel(SampledArgs a) {
     for (int i = tid; i < L.splits; i += kWalkThreads) total += chunk_sum(i);
     total = block_sum<kWalkThreads>(total, s_red);
   }
-  const Found f = find_chunk<kWalkThreads>(chunk_sum, L.splits, (double)a.u_bonus[t] * total, s_red, s_int, &s_rest);
+  const Found f = find_chunk<kWalkThreads>(chunk_sum, L.splits, (double)a.u_bonus[t] * total, s_red, s_search);
   if (tid < kChunk / 32) s_gone[0][tid] = 0;
   __syncthreads();
   if (taken) mark(s_gone[0], f.chunk, tid, kWalkThreads);
@@ -614,15 +636,16 @@ __global__ __launch_bounds__(NT) void sampled_walk_kernel(SampledArgs a) {
     const int j = tid * N + i, tok = f.chunk * kChunk + j;
     w[i] = tok < a.vocab && !((s_gone[0][j >> 5] >> (j & 31)) & 1) ? weigh(logit(a, row, tok)) : 0.0;
   }
-  const int pick = find_token<NT>(w, f.rest, s_red, s_int);
+  const int pick = find_token<NT>(w, f.rest, s_red, s_search);
   if (tid == 0) a.bonus[t] = f.chunk * kChunk + pick;
 }
 
 // The next token of each tree whose drafts were drawn: from the last row's
 // max(p - c q, 0), or from p where nothing of that is left (by rounding).
 __global__ __launch_bounds__(kThreads) void sampled_draw_kernel(SampledArgs a) {
-  __shared__ double s_red[kWaves], s_rest, s_pow[kTable];
-  __shared__ int s_last, s_int[2];
+  __shared__ double s_red[kWaves], s_pow[kTable];
+  __shared__ Search<kThreads> s_search;
+  __shared__ int s_last;
   const int t = blockIdx.y, tid = threadIdx.x, lane = tid & 63;
   const int split = blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane(tid >> 6);
   const Layout L = layout_of(a.num_trees, a.total, a.vocab);
@@ -675,7 +698,7 @@ __global__ __launch_bounds__(kThreads) void sampled_draw_kernel(SampledArgs a) {
     for (int i = tid; i < L.splits; i += kThreads) total += sum_of(i);
     total = block_sum<kThreads>(total, s_red);
   }
-  const Found f = find_chunk<kThreads>(sum_of, L.splits, (double)a.u_bonus[t] * total, s_red, s_int, &s_rest);
+  const Found f = find_chunk<kThreads>(sum_of, L.splits, (double)a.u_bonus[t] * total, s_red, s_search);
   constexpr int N = kChunk / kThreads;
   double w[N];
 #pragma unroll
@@ -687,7 +710,7 @@ __global__ __launch_bounds__(kThreads) void sampled_draw_kernel(SampledArgs a) {
       if (residual) w[i] = fmax(w[i] - st.c * (double)a.draft[(size_t)st.row * a.vocab + tok], 0.0);
     }
   }
-  const int pick = find_token<kThreads>(w, f.rest, s_red, s_int);
+  const int pick = find_token<kThreads>(w, f.rest, s_red, s_search);
   if (tid == 0) a.bonus[t] = f.chunk * kChunk + pick;
 }
 
