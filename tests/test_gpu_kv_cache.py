@@ -624,3 +624,19 @@ def test_tiny_blocks(w12, size):
         # scores of zero: no rounding but the probabilities', the sums' and the output's
         lim = KV.attention_tolerance(ref, av[None], np.zeros(1), n, dim)[0]
         assert (np.abs(got[0] - ref) <= lim).all()
+
+
+@pytest.mark.parametrize("dim,kv,group", [(64, 8, 6), (64, 16, 1), (128, 4, 6), (128, 8, 3), (256, 4, 5)])
+@pytest.mark.parametrize("int8", [False, True])
+def test_blocks_of_several_tiles(w12, dim, kv, group, int8):
+    """Enough query rows that waves share a block's tiles, full, in part and
+    not at all (sequences of unlike sizes in one call), over pages, tails and
+    the step's own rows."""
+    say("blocks", dim, kv, group, int8)
+    sv = Serving(w12, 3, kv, group, dim, 64, int8, seed=23, step_rows=256)
+    sv.step([200, 67, 130])
+    sv.step([170, 9, 250])
+    rng = np.random.RandomState(24)
+    sizes = [100, 256, 41]
+    sv.step(sizes, parents=[random_parents(rng, n) for n in sizes])
+    sv.step([255, 1, 256])

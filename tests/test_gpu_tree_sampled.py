@@ -219,3 +219,15 @@ def test_offsets_that_are_no_ranges(w12):
     assert got[0].tolist() == [-1, -1, *want[0][1:], -1, -1]
     assert got[2].tolist() == [-1, -1, *want[2][1:], -1, -1]
     assert np.array_equal(got[1][6:], want[1][6:])
+
+
+@pytest.mark.parametrize("drafted", [False, True])
+@pytest.mark.parametrize("vocab", [262144, 262145, 600001])
+def test_vocabularies_of_more_chunks_than_threads(w12, vocab, drafted):
+    """A search for the drawn token that takes several turns, found in each
+    of them and at their ends."""
+    say("long rows", vocab, drafted)
+    f = forest(19, [3] * 6, vocab, drafted, f32=not drafted, spread=1.0)
+    f["ub"][:] = [0.0, 0.3, 0.4369, 0.6, 0.9, np.float32(1) - np.float32(2.0 ** -24)]
+    f["temp"][:] = 5.0
+    both(w12, f)
