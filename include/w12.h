@@ -438,7 +438,7 @@ w12_status w12_kv_attention_workspace(const w12_kv_cache *cache, int32_t num_seq
  *   q    [total_rows][q_heads][head_dim] bf16 (w12_kv_append's output).
  *   out  [total_rows][q_heads * head_dim] bf16: the x of the Wo product; not q's memory.
  *   ws   workspace of >= w12_kv_attention_workspace bytes, 256-byte aligned,
- *        content ignored.
+ *        content ignored; of one call at a time (two streams, two captured graphs: one each).
  * Device-detected, reported as NaN outputs of the sequence: what w12_kv_append
  * lists (a slot named twice is allowed here), and a page id outside
  * [0, num_pages). Weighted values are summed before they are normalised:
@@ -498,7 +498,7 @@ w12_status tree_accept_sampled_workspace(int32_t num_trees, int32_t total_nodes,
  *           fp32 or NULL (rows of nodes without children are not read);
  *   u_accept [total_nodes], u_bonus [num_trees] fp32 in [0, 1).
  *   accept_len, path, bonus: as tree_accept's.
- *   ws      workspace, 16-byte aligned, content ignored.
+ *   ws      workspace, 16-byte aligned, content ignored; of one call at a time.
  * Device-detected, reported as accept_len = bonus = -1 and a path of -1: what
  * tree_accept lists, a drafted token outside [0, vocab), more than 1024
  * nodes, a temperature that is not positive and finite, and a row on the walk
