@@ -231,3 +231,20 @@ def test_vocabularies_of_more_chunks_than_threads(w12, vocab, drafted):
     f["ub"][:] = [0.0, 0.3, 0.4369, 0.6, 0.9, np.float32(1) - np.float32(2.0 ** -24)]
     f["temp"][:] = 5.0
     both(w12, f)
+
+
+def test_draft_rows_of_nodes_without_children_are_not_read(w12):
+    """Whatever such a row holds (here zeros, NaN, infinities, the largest
+    value), the walk that ends at its node draws from the target's row."""
+    say("drafts of leaves")
+    f = forest(20, [1] * 12 + [6] * 4, 3000, True, chain=True, spread=1.0)
+    f["u"][:] = 0.0  # every draft that the target allows is accepted: each walk ends at its leaf
+    leaves = np.append(np.arange(12), f["off"][13:] - 1)
+    want = call(w12, f)
+    draft, odd = f["draft"].copy(), np.random.RandomState(20)
+    for i in leaves:
+        draft[i] = odd.choice(np.array([0, np.nan, np.inf, -np.inf, np.finfo(np.float32).max], np.float32), 3000)
+    f["draft"] = draft
+    got = both(w12, f)
+    assert got[0].tolist() == [0] * 12 + [5] * 4
+    assert all(np.array_equal(a, b) for a, b in zip(got, want))

@@ -641,7 +641,9 @@ __global__ __launch_bounds__(NT) void sampled_walk_kernel(SampledArgs a) {
 }
 
 // The next token of each tree whose drafts were drawn: from the last row's
-// max(p - c q, 0), or from p where nothing of that is left (by rounding).
+// max(p - c q, 0), or from p where nothing of that is left (by rounding). A walk
+// that ends at a node without children has c = 0 (others at least 1): its row of
+// q is not read, so what it holds, NaN or infinities (0 inf = NaN) too, takes no weight.
 __global__ __launch_bounds__(kThreads) void sampled_draw_kernel(SampledArgs a) {
   __shared__ double s_red[kWaves], s_pow[kTable];
   __shared__ Search<kThreads> s_search;
@@ -653,14 +655,15 @@ __global__ __launch_bounds__(kThreads) void sampled_draw_kernel(SampledArgs a) {
   const State st = reinterpret_cast<const State*>(ws + L.off_state)[t];
   if (st.row < 0) return;
   const double it2 = inv_temperature(a, t) * kLog2e, inv = 1.0 / st.sum;
+  const bool rejected = st.c != 0.0;
   load_powers(s_pow);
   __syncthreads();
   const Weigher weigh(s_pow, st.max, it2);
   double2* sums = reinterpret_cast<double2*>(ws + L.off_sum) + (size_t)t * L.splits;
   if (split < L.splits) {
-    float x[kPer], q[kPer];
+    float x[kPer], q[kPer] = {};
     logits16(a, st.row, split * kChunk + lane * kPer, x);
-    draft16(a, st.row, split * kChunk + lane * kPer, q);
+    if (rejected) draft16(a, st.row, split * kChunk + lane * kPer, q);
     double r = 0.0, p = 0.0;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
@@ -707,7 +710,7 @@ __global__ __launch_bounds__(kThreads) void sampled_draw_kernel(SampledArgs a) {
     w[i] = 0.0;
     if (tok < a.vocab) {
       w[i] = weigh(logit(a, st.row, tok)) * inv;
-      if (residual) w[i] = fmax(w[i] - st.c * (double)a.draft[(size_t)st.row * a.vocab + tok], 0.0);
+      if (residual && rejected) w[i] = fmax(w[i] - st.c * (double)a.draft[(size_t)st.row * a.vocab + tok], 0.0);
     }
   }
   const int pick = find_token<kThreads>(w, f.rest, s_red, s_search);
