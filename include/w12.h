@@ -466,7 +466,8 @@ w12_status w12_kv_attention(const w12_kv_cache *cache, int32_t layer, int32_t nu
  * length -1 with nothing written (a slot named twice: its first sequence
  * stands): what w12_kv_append lists (trees aside), an
  * accept_len or path outside the sequence's rows or not ascending from row 0,
- * a page id outside [0, num_pages), no room in the page table.
+ * a page id outside [0, num_pages), a new length beyond max_pages *
+ * page_tokens.
  */
 w12_status w12_kv_commit(const w12_kv_cache *cache, int32_t num_seq, const int32_t *slot, const int32_t *row_off,
                          int32_t total_rows, const int32_t *accept_len, const int32_t *path, int32_t *len_out,

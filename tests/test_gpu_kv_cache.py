@@ -640,3 +640,29 @@ def test_blocks_of_several_tiles(w12, dim, kv, group, int8):
     sizes = [100, 256, 41]
     sv.step(sizes, parents=[random_parents(rng, n) for n in sizes])
     sv.step([255, 1, 256])
+
+
+def test_commit_keeps_no_more_than_the_page_table_holds(w12):
+    """A length past the page table's pages is refused by every call, so the
+    commit that would lead to one is: the last token that has a page is kept,
+    the next one is not."""
+    import torch
+    say("full page table")
+    page, blocks = 32, 2
+    sv = Serving(w12, 2, 1, 2, 64, page, seed=25, blocks=blocks)
+    sv.step([60, 50])
+    before = [t.clone() for t in (sv.cache.pages.view(torch.uint8), sv.cache.scales, sv.cache.recent)]
+    off, x = i32([0, 6, 12]), torch.ones(12, 4 * 64, device=DEV)
+    w12.w12_kv_append(sv.cache, 0, x, off, sv.rope_t, 2, slot=i32(sv.slot))
+    recent = sv.cache.recent.clone()
+    for acc, want in (([4, 0], [-1, 51]), ([5, -1], [-1, 50])):  # 65 and 66 tokens of 64
+        got = w12.w12_kv_commit(sv.cache, off, i32(acc), slot=i32(sv.slot), length_out=sv.cache.length.clone())
+        assert got[sv.slot].tolist() == want, acc
+        assert torch.equal(sv.cache.pages.view(torch.uint8), before[0])
+        assert torch.equal(sv.cache.scales.view(torch.uint8), before[1].view(torch.uint8))
+        assert torch.equal(sv.cache.recent.view(torch.int16), recent.view(torch.int16))
+    sv.cache.recent.copy_(before[2])
+    sv.step([4, 5])  # 64 of 64, 55 of 64
+    # a full sequence is still read: its last row is the step's own
+    q, _ = bf16(np.ones((1, 2, 64)))
+    assert np.isfinite(attend(w12, sv, q, [0, 1], slot=i32(sv.slot[:1]))[:1]).all()

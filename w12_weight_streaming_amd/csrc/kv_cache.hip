@@ -182,8 +182,8 @@ __device__ __forceinline__ CommitView commit_view(const CommitArgs& a, int s, in
       s_src[j] = w.v.tail + p;
     }
     const int closed = (w.v.tail + w.n) / a.c.page;
-    if (w.v.full + closed > a.c.max_pages) {
-      bad = 1;
+    if (w.v.len + w.n > a.c.max_pages * (long long)a.c.page) {
+      bad = 1;  // an unfinished block needs its page too: no call takes a length past the page table
     } else {
       for (int b = tid; b < closed; b += blockDim.x) {
         const int id = a.c.table[(size_t)w.v.slot * a.c.max_pages + w.v.full + b];
