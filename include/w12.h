@@ -438,7 +438,8 @@ w12_status w12_kv_attention_workspace(const w12_kv_cache *cache, int32_t num_seq
  *   q    [total_rows][q_heads][head_dim] bf16 (w12_kv_append's output).
  *   out  [total_rows][q_heads * head_dim] bf16: the x of the Wo product; not q's memory.
  *   ws   workspace of >= w12_kv_attention_workspace bytes, 256-byte aligned,
- *        content ignored; of one call at a time (two streams, two captured graphs: one each).
+ *        content ignored; of one call at a time (two streams, two captured
+ *        graphs, two host threads whose calls overlap: one each).
  * Device-detected, reported as NaN outputs of the sequence: what w12_kv_append
  * lists (a slot named twice is allowed here), and a page id outside
  * [0, num_pages). Weighted values are summed before they are normalised:

@@ -1,0 +1,57 @@
+"""Workspaces that the binding takes for its caller: calls of two host threads
+on one stream, whose launches may come in any order, never share one. The
+library itself is not called: no GPU is needed."""
+import threading
+from types import SimpleNamespace
+
+import pytest
+import torch
+
+import w12_weight_streaming_amd as w12
+
+
+def in_two_threads(fn):
+    """fn(i) in two threads; what they return, or the first exception."""
+    got, errors = [None, None], []
+
+    def go(i):
+        try:
+            got[i] = fn(i)
+        except Exception as e:  # noqa: BLE001 - handed to the test
+            errors.append(e)
+    threads = [threading.Thread(target=go, args=(i,)) for i in (0, 1)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(60)
+    if errors:
+        raise errors[0]
+    return got
+
+
+@pytest.fixture
+def one_stream(monkeypatch):
+    """Tensors of the CPU in place of a GPU's, every thread on stream 0."""
+    monkeypatch.setattr(w12, "_get", lambda t, *a, **k: t.data_ptr())
+    monkeypatch.setattr(w12, "_raw_stream", lambda index: 0)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: SimpleNamespace(cuda_stream=0))
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+
+
+def test_attention_calls_of_two_threads_have_a_workspace_each(one_stream, monkeypatch):
+    need, meet = 4096, threading.Barrier(2, timeout=30)
+    monkeypatch.setattr(w12, "_attention_workspace_bytes", lambda *a: need)
+    used = {}
+
+    def run(index, what, *args):
+        assert what == "w12_kv_attention" and args[-1] >= need
+        used[threading.get_ident()] = args[-2]
+        meet.wait()  # both calls are in progress
+    monkeypatch.setattr(w12, "_run", run)
+    cache = SimpleNamespace(index=0, head_dim=64, kv_heads=2, _ref=None)
+    q, off = torch.zeros(3, 4, 64, dtype=torch.bfloat16), torch.tensor([0, 3], dtype=torch.int32)
+    for _ in range(3):
+        used.clear()
+        in_two_threads(lambda i: w12.w12_kv_attention(cache, 0, q, off))
+        a, b = used.values()
+        assert abs(a - b) >= need

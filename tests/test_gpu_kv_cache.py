@@ -666,3 +666,42 @@ def test_commit_keeps_no_more_than_the_page_table_holds(w12):
     # a full sequence is still read: its last row is the step's own
     q, _ = bf16(np.ones((1, 2, 64)))
     assert np.isfinite(attend(w12, sv, q, [0, 1], slot=i32(sv.slot[:1]))[:1]).all()
+
+
+def test_two_host_threads_on_one_stream(w12):
+    """Calls of unlike shapes, long enough to be split among workgroups, made
+    by two threads at once on the default stream: each gets its own results,
+    the same bits as alone, and leaves the rows behind its own."""
+    import threading
+
+    import torch
+    say("two threads")
+    sv = Serving(w12, 2, 2, 4, 64, 32, seed=26, step_rows=256, blocks=40, positions=2048)
+    for _ in range(4):
+        sv.step([250, 120], check=False)
+    slot = i32(sv.slot)
+    shapes = [(slot[:1], [0, 5]), (slot, [0, 100, 131])]
+    args = []
+    for sl, off in shapes:
+        q, _ = bf16(sv.rng.randn(off[-1], 8, 64))
+        args.append((q, off, sl))
+    want = [attend(w12, sv, q, off, slot=sl) for q, off, sl in args]
+    bad = []
+
+    def go(i):
+        try:
+            q, off, sl = args[i]
+            off_t = i32(off)
+            outs = [torch.full((q.shape[0] + 2, 512), 7.0, dtype=torch.bfloat16, device=DEV) for _ in range(200)]
+            for out in outs:
+                w12.w12_kv_attention(sv.cache, 0, q, off_t, slot=sl, out=out)
+            torch.cuda.synchronize()
+            bad.extend((i, k) for k, out in enumerate(outs) if not np.array_equal(f64(out), want[i]))
+        except Exception as e:  # noqa: BLE001 - told by the assertion below
+            bad.append((i, repr(e)))
+    threads = [threading.Thread(target=go, args=(i,)) for i in (0, 1)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(100)
+    assert not bad

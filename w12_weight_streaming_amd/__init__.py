@@ -567,8 +567,9 @@ def w12_kv_attention(cache: KvCache, layer: int, q: torch.Tensor, row_off: torch
     """Attention of the step's rows q [rows, q_heads, head_dim] bf16 over the
     cache; returns [rows, q_heads * head_dim] bf16. scale defaults to
     head_dim ** -0.5. ws: a workspace of the caller's (its content is
-    ignored); without one the call takes one kept per stream, or, while it is
-    captured, one of its own (replays may overlap in time with other calls)."""
+    ignored), of one call at a time; without one the call allocates its own:
+    it makes two launches, and those of another host thread on the same stream,
+    or of a captured graph's replay, may come between them."""
     index = cache.index
     at_q = _get(q, _BF16, "q", 3, index)
     rows, q_heads, dim = q.shape
@@ -582,12 +583,7 @@ def w12_kv_attention(cache: KvCache, layer: int, q: torch.Tensor, row_off: torch
         raise ValueError("out must hold [rows, q_heads * head_dim]")
     need = _attention_workspace_bytes(cache, seqs, rows, q_heads)
     if ws is None:
-        if torch.cuda.is_current_stream_capturing():
-            ws = torch.empty(need, dtype=torch.uint8, device=q.device)
-        else:
-            ws = _ws_cache.get((index, _raw_stream(index), "kv"))
-            if ws is None or ws.numel() < need:
-                ws = workspace(need, q.device, "kv")
+        ws = torch.empty(need, dtype=torch.uint8, device=q.device)
     _run(index, "w12_kv_attention", cache._ref, layer, seqs,
          0 if slot is None else _get(slot, _I32, "slot", 1, index, seqs), at_off, rows,
          0 if parent is None else _get(parent, _I32, "parent", 1, index, rows), at_q, q_heads,
