@@ -55,3 +55,21 @@ def test_attention_calls_of_two_threads_have_a_workspace_each(one_stream, monkey
         in_two_threads(lambda i: w12.w12_kv_attention(cache, 0, q, off))
         a, b = used.values()
         assert abs(a - b) >= need
+
+
+@pytest.mark.parametrize("tag", ["gemm", "head", "cert"])
+def test_kept_workspaces_belong_to_one_thread(one_stream, tag):
+    """The products' workspaces are kept from call to call, for each thread by
+    itself; a larger one replaces a smaller one."""
+    dev, meet = torch.device("cpu"), threading.Barrier(2, timeout=30)
+
+    def take(i):
+        a = w12.workspace(1000, dev, tag)
+        assert w12.workspace(500, dev, tag) is a and not a.any()
+        meet.wait()
+        b = w12.workspace(5000, dev, tag)
+        assert b.numel() >= 5000 and w12.workspace(1000, dev, tag) is b
+        return a, b
+    first, second = in_two_threads(take)
+    for a, b in zip(first, second):
+        assert abs(a.data_ptr() - b.data_ptr()) >= a.numel()

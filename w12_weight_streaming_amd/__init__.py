@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import threading
 from dataclasses import dataclass
 
 import torch
@@ -170,17 +171,19 @@ class PackedW12:
 
 # ------------------------------------------------------------------ workspaces
 
-_ws_cache: dict = {}
+_ws_kept = threading.local()  # .cache: this host thread's workspaces
 
 
 def workspace(nbytes: int, device: torch.device, tag: str = "gemm") -> torch.Tensor:
-    """Zero-filled device workspace, grown on demand and kept per (device,
-    stream, tag). The library leaves it zero-filled after every call."""
+    """Zero-filled device workspace of the products and heads, grown on demand
+    and kept per (host thread, device, stream, tag): a call of theirs may be
+    several launches, and another thread's on the same stream may come between
+    them. The library leaves it zero-filled after every call."""
+    cache = _ws_kept.__dict__.setdefault("cache", {})
     key = (device.index, torch.cuda.current_stream(device).cuda_stream, tag)
-    ws = _ws_cache.get(key)
+    ws = cache.get(key)
     if ws is None or ws.numel() < nbytes:
-        ws = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=device)
-        _ws_cache[key] = ws
+        ws = cache[key] = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=device)
     return ws
 
 
