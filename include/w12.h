@@ -33,7 +33,9 @@
  *     workspace holds arrival counters, which every completed call returns
  *     to zero, and partial sums, which a call writes before it reads them;
  *     so one allocation serves any number of calls.  Calls that overlap in
- *     time must not share a workspace.
+ *     time must not share a workspace.  Where a call says "content ignored"
+ *     it leaves any content behind: such a workspace goes to no product or
+ *     head afterwards, unless it is zero-filled again.
  *
  * W12 layout (readings of [S1] 4.1 and [S2] for gfx950):
  *   N output channels x K inputs, N % 32 == 0, K % 256 == 0, K <= 2^20.

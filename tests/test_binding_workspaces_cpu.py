@@ -73,3 +73,33 @@ def test_kept_workspaces_belong_to_one_thread(one_stream, tag):
     first, second = in_two_threads(take)
     for a, b in zip(first, second):
         assert abs(a.data_ptr() - b.data_ptr()) >= a.numel()
+
+
+def test_scratch_is_no_zero_filled_workspace(one_stream, monkeypatch):
+    """A workspace that a call leaves dirty must not be one that a later
+    product takes for zero-filled; the caller's own memory may be."""
+    ran, dev = [], torch.device("cpu")
+    monkeypatch.setattr(w12, "_attention_workspace_bytes", lambda *a: 4096)
+    monkeypatch.setattr(w12, "_run", lambda index, what, *args: ran.append(args[-2]))
+    cache = SimpleNamespace(index=0, head_dim=64, kv_heads=2, _ref=None)
+    q, off = torch.zeros(3, 4, 64, dtype=torch.bfloat16), torch.tensor([0, 3], dtype=torch.int32)
+    ints = torch.tensor([-1, 0, 0], dtype=torch.int32)
+
+    def both(ws):
+        w12.w12_kv_attention(cache, 0, q, off, ws=ws)
+        w12.tree_accept_sampled(off, ints, ints, torch.zeros(3, 8), torch.zeros(3), torch.zeros(1), ws=ws)
+    for tag in ("gemm", "head", "cert"):
+        kept = w12.workspace(10000, dev, tag)
+        for ws in (kept, kept[256:], kept.view(torch.int32)):
+            with pytest.raises(ValueError, match="zero-filled"):
+                w12.w12_kv_attention(cache, 0, q, off, ws=ws)
+            with pytest.raises(ValueError, match="zero-filled"):
+                w12.tree_accept_sampled(off, ints, ints, torch.zeros(3, 8), torch.zeros(3), torch.zeros(1), ws=ws)
+        w12.workspace(20000, dev, tag)  # replaced: still what its holder may give a product
+        with pytest.raises(ValueError, match="zero-filled"):
+            w12.w12_kv_attention(cache, 0, q, off, ws=kept)
+    assert not ran
+    for ws in (torch.empty(10000, dtype=torch.uint8), w12.workspace(10000, dev, "of my own")):
+        both(ws)
+        assert ran == [ws.data_ptr()] * 2
+        ran.clear()

@@ -15,6 +15,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
+import weakref
 from dataclasses import dataclass
 
 import torch
@@ -172,18 +173,22 @@ class PackedW12:
 # ------------------------------------------------------------------ workspaces
 
 _ws_kept = threading.local()  # .cache: this host thread's workspaces
+_zero_filled = weakref.WeakValueDictionary()  # address -> workspace that the products and heads expect zero-filled
 
 
 def workspace(nbytes: int, device: torch.device, tag: str = "gemm") -> torch.Tensor:
     """Zero-filled device workspace of the products and heads, grown on demand
     and kept per (host thread, device, stream, tag): a call of theirs may be
     several launches, and another thread's on the same stream may come between
-    them. The library leaves it zero-filled after every call."""
+    them. Those calls leave it zero-filled; w12_kv_attention and
+    tree_accept_sampled would not, and refuse it."""
     cache = _ws_kept.__dict__.setdefault("cache", {})
     key = (device.index, torch.cuda.current_stream(device).cuda_stream, tag)
     ws = cache.get(key)
     if ws is None or ws.numel() < nbytes:
         ws = cache[key] = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=device)
+        if tag in ("gemm", "head", "cert"):  # what the calls without ws= take
+            _zero_filled[ws.data_ptr()] = ws
     return ws
 
 
@@ -460,6 +465,15 @@ def _run(index: int, what: str, *args) -> None:
         raise W12Error(status, what)
 
 
+def _scratch(ws, index: int) -> tuple[int, int]:
+    """Address and bytes of a workspace whose content is ignored and left as
+    it comes: never one that a later product takes for zero-filled."""
+    at = _get(ws, getattr(ws, "dtype", None), "ws", None, index)
+    if ws.untyped_storage().data_ptr() in _zero_filled:
+        raise ValueError("ws is a zero-filled workspace of the products or heads, which this call would leave dirty")
+    return at, ws.numel() * ws.element_size()
+
+
 @dataclass(frozen=True, eq=False)  # the description holds the arrays' addresses
 class KvCache:
     """Device-resident KV cache: the arrays of include/w12.h. pages is
@@ -569,10 +583,10 @@ def w12_kv_attention(cache: KvCache, layer: int, q: torch.Tensor, row_off: torch
                      out: torch.Tensor | None = None, ws: torch.Tensor | None = None) -> torch.Tensor:
     """Attention of the step's rows q [rows, q_heads, head_dim] bf16 over the
     cache; returns [rows, q_heads * head_dim] bf16. scale defaults to
-    head_dim ** -0.5. ws: a workspace of the caller's (its content is
-    ignored), of one call at a time; without one the call allocates its own:
-    it makes two launches, and those of another host thread on the same stream,
-    or of a captured graph's replay, may come between them."""
+    head_dim ** -0.5. ws: a workspace of the caller's, of one call at a time
+    (its content is ignored, and is not zeros afterwards); without one the call
+    allocates its own: it makes two launches, and those of another host thread
+    on the same stream, or of a captured graph's replay, may come between them."""
     index = cache.index
     at_q = _get(q, _BF16, "q", 3, index)
     rows, q_heads, dim = q.shape
@@ -587,11 +601,14 @@ def w12_kv_attention(cache: KvCache, layer: int, q: torch.Tensor, row_off: torch
     need = _attention_workspace_bytes(cache, seqs, rows, q_heads)
     if ws is None:
         ws = torch.empty(need, dtype=torch.uint8, device=q.device)
+        scratch = ws.data_ptr(), need
+    else:
+        scratch = _scratch(ws, index)
     _run(index, "w12_kv_attention", cache._ref, layer, seqs,
          0 if slot is None else _get(slot, _I32, "slot", 1, index, seqs), at_off, rows,
          0 if parent is None else _get(parent, _I32, "parent", 1, index, rows), at_q, q_heads,
          dim ** -0.5 if scale is None else scale, _get(out, _BF16, "out", None, index),
-         _get(ws, ws.dtype, "ws", None, index), ws.numel() * ws.element_size())
+         *scratch)
     return out
 
 
@@ -625,7 +642,8 @@ def tree_accept_sampled(node_off: torch.Tensor, parent: torch.Tensor, token: tor
     """Tree acceptance of sampling requests: logits [nodes, vocab] fp32 or
     bf16 (a row per node), random numbers u_accept [nodes] and u_bonus
     [trees], temperature [trees] or None (1), draft [nodes, vocab] fp32 or
-    None (chosen drafts). Returns (accept_len, path, bonus) as tree_accept."""
+    None (chosen drafts); ws as w12_kv_attention's. Returns (accept_len, path,
+    bonus) as tree_accept."""
     if not isinstance(logits, torch.Tensor) or logits.dtype not in (_F32, _BF16):
         raise TypeError("logits must be a float32 or bfloat16 tensor")
     at_x = _get(logits, logits.dtype, "logits", 2, None)
@@ -646,10 +664,12 @@ def tree_accept_sampled(node_off: torch.Tensor, parent: torch.Tensor, token: tor
         _ok((_lib or lib()).tree_accept_sampled_workspace(T, total, vocab, ctypes.byref(need)),
             "tree_accept_sampled_workspace")
         ws = torch.empty(need.value, dtype=torch.uint8, device=dev)
+        scratch = ws.data_ptr(), need.value
+    else:
+        scratch = _scratch(ws, index)
     # one allocation for the three outputs (bonus and accept_len first: T entries each)
     out = torch.empty(2 * T + total, dtype=_I32, device=dev)
     base = out.data_ptr()
     _run(index, "tree_accept_sampled", T, at_off, total, *at, at_x, W12_Y_F32 if logits.dtype is _F32 else W12_Y_BF16,
-         vocab, at_temp, at_draft, *at_u, base, base + 8 * T, base + 4 * T, _get(ws, ws.dtype, "ws", None, index),
-         ws.numel() * ws.element_size())
+         vocab, at_temp, at_draft, *at_u, base, base + 8 * T, base + 4 * T, *scratch)
     return out[:T], out[2 * T:], out[T:2 * T]
