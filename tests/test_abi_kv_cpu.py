@@ -120,3 +120,30 @@ def test_binding_refuses_cpu_tensors(w12):
         w12.tree_accept_sampled(z(2, dt=torch.int32), z(3, dt=torch.int32), z(3, dt=torch.int32), z(3, 8), z(3), z(1))
     with pytest.raises(TypeError):
         w12.tree_accept_sampled(z(2, dt=torch.int32), z(3, dt=torch.int32), z(3, dt=torch.int32), z(3, 8).half(), z(3), z(1))
+
+
+# Addresses that no two arguments share, so that only the cache can be what a call refuses.
+APART = [ctypes.c_void_p((i + 1) << 40) for i in range(4)]
+
+
+def call_apart(w12, c, ws_bytes=1 << 40):
+    L, d = w12.lib(), ctypes.byref(c)
+    qkv, q, out, ws = APART
+    return (lambda: L.w12_kv_append(d, 0, 1, NULL, FAKE, 4, NULL, qkv, 0, 8, FAKE, 16, 128, 0, q, NULL),
+            lambda: L.w12_kv_attention(d, 0, 1, NULL, FAKE, 4, NULL, q, 8, 0.1, out, ws, ws_bytes, NULL))
+
+
+@pytest.mark.parametrize("kw", BAD_CACHES +
+                         [dict(layers=1025), dict(slots=(1 << 20) + 1), dict(scales=0), dict(recent=0), dict(len=0),
+                          dict(page_table=0x1002), dict(recent_rows=1056)], ids=str)
+def test_bad_caches_with_arguments_that_lie_apart(w12, kw):
+    append, attention = call_apart(w12, cache(w12, **kw))
+    assert append() == w12.W12_EINVAL
+    assert attention() == w12.W12_EINVAL
+
+
+def test_a_good_cache_passes_the_checks(w12):
+    """What the test above refuses is the cache: with a good one the call
+    goes on to its workspace's size (to the missing GPU where there is none)."""
+    _, attention = call_apart(w12, cache(w12), ws_bytes=0)
+    assert attention() in (w12.W12_ENOSPC, w12.W12_EHIP)
