@@ -705,3 +705,165 @@ def test_two_host_threads_on_one_stream(w12):
     for t in threads:
         t.join(100)
     assert not bad
+
+
+def filled(w12, lengths, tail_rows, kv, dim, page, int8, seed):
+    """A cache with random codes and scales for these lengths (one a slot),
+    random recent rows up to tail_rows behind the tail, NaN wherever nothing
+    was written; and its keys and values [slot][head] as the codes stand for
+    them, in 64 bits."""
+    import torch
+    rng, gen = np.random.RandomState(seed), torch.Generator(device=DEV).manual_seed(seed)
+    blocks = max(lengths) // page + 2
+    pages = len(lengths) * blocks + 1
+    c = w12.kv_cache(1, kv, dim, pages, len(lengths), blocks, page, 256, int8, DEV)
+    ids = rng.permutation(pages)[:len(lengths) * blocks].reshape(len(lengths), blocks)
+    c.page_table.copy_(i32(ids))
+    c.length.copy_(i32(lengths))
+    c.scales.fill_(float("nan"))
+    c.recent.fill_(float("nan"))
+    kv_of = []
+    for s, n in enumerate(lengths):
+        full = n // page
+        own = torch.tensor(ids[s, :full], device=DEV)
+        x = torch.randn((full, kv, 2, page * dim), generator=gen, device=DEV)
+        codes = (x * 40).round().clamp(-127, 127).to(torch.int8) if int8 else (x * 100).clamp(-448, 448).to(torch.float8_e4m3fn)
+        scale = torch.exp(0.4 * torch.randn((full, kv, 2), generator=gen, device=DEV)) / (40 if int8 else 100)
+        c.pages.view(torch.uint8)[0, own] = codes.view(torch.uint8)
+        c.scales[0, own] = scale
+        tail = n % page + tail_rows
+        rec = torch.randn((kv, 2, tail, dim), generator=gen, device=DEV).bfloat16()
+        got, sc, rc = codes.float().cpu().numpy().astype(np.float64), f64(scale), f64(rec)
+        heads = []
+        for h in range(kv):
+            both = []
+            for v in (0, 1):
+                at = torch.tensor(KV.places(v, tail, dim), device=DEV)
+                c.recent[0, s, h, v].view(-1)[at] = rec[h, v]
+                paged = got[:, h, v][:, KV.places(v, page, dim)] * sc[:, h, v][:, None, None]
+                both.append(np.concatenate([paged.reshape(-1, dim), rc[h, v]]))
+            heads.append(both)
+        kv_of.append(heads)
+    return c, kv_of
+
+
+# (lengths of the slots, sequences, rows of each, query heads, kv heads, dim, page, int8, scale); what
+# makes the run of one wave's pages longer than the 64 whose ids it holds at a time is beside each
+LONG = [
+    ((17100,), 512, 1, 1, 1, 64, 32, False, None),      # a tile a block: eight waves share 534 groups of tokens, 67 each or 66
+    ((4322,), 256, 2, 64, 1, 64, 64, True, 0.07),       # four tiles: two waves share 134
+    ((8650,), 256, 2, 32, 1, 128, 96, True, None),      # two tiles: four waves share 270, 68 each or 67
+    ((8700, 9001), 256, 2, 32, 1, 128, 64, False, 0.2),  # 272 and 280, at two lengths: runs end inside a sequence
+    ((8577,), 256, 2, 32, 1, 256, 128, False, 0.02),    # 268 among four, 67 each
+    ((17170,), 512, 1, 4, 1, 256, 96, True, None),      # 534 among eight
+    ((33000,), 128, 1, 12, 2, 128, 64, False, None),    # 1030 among eight, 129 each or 128: three turns
+]
+
+
+@pytest.mark.parametrize("lengths,seqs,rows,q_heads,kv,dim,page,int8,scale", LONG)
+def test_runs_of_many_pages(w12, lengths, seqs, rows, q_heads, kv, dim, page, int8, scale):
+    """Contexts so long, for so many sequences, that a wave walks more pages
+    than it holds the ids of. The sequences share the slots in turn (which
+    attention allows), so the oracle's keys and values are few. Every query
+    points at one token, two thirds of them near the pages' end, which takes
+    most of its weight: a page left out or read twice shows."""
+    say("long runs", lengths, seqs, dim, page, int8)
+    c, kv_of = filled(w12, lengths, rows, kv, dim, page, int8, seed=dim + page)
+    rng = np.random.RandomState(27)
+    slot = np.arange(seqs) % len(lengths)
+    off = np.arange(seqs + 1) * rows
+    group = q_heads // kv
+    scale_of = dim ** -0.5 if scale is None else scale
+    x = np.zeros((seqs * rows, q_heads, dim))
+    for i in range(seqs * rows):
+        n = lengths[slot[i // rows]] // page * page
+        for h in range(q_heads):
+            k = kv_of[slot[i // rows]][h // group][0][rng.randint(n - int(n * rng.choice([1, 0.04, 0.005])), n)]
+            x[i, h] = k * (2 / scale_of / np.linalg.norm(k))  # a score of 2 |k|, others' of spread 2
+    q, qv = bf16(x)
+    got = f64(w12.w12_kv_attention(c, 0, q, i32(off), slot=i32(slot), scale=scale)).reshape(seqs * rows, q_heads, dim)
+    assert np.isfinite(got).all()
+    for s in sorted({0, 1, seqs // 2, seqs - 2, seqs - 1, *rng.randint(0, seqs, 6).tolist()}):
+        n, r = lengths[slot[s]], slice(off[s], off[s + 1])
+        see = np.concatenate([np.ones((rows, n), bool), KV.ancestors(KV.chain(rows))], 1)
+        for h in range(kv):
+            heads = slice(h * group, (h + 1) * group)
+            k, v = kv_of[slot[s]][h]
+            ref, av, sz = KV.attention(qv[r, heads], k, v, see, scale_of)
+            err = np.abs(got[r, heads] - ref) / KV.attention_tolerance(ref, av, sz, n + rows, dim)
+            assert (err <= 1).all(), (s, h, float(err.max()))
+
+
+@pytest.mark.parametrize("page", [96, 128])
+@pytest.mark.parametrize("int8", [False, True])
+def test_large_pages_of_256_dims(w12, page, int8):
+    """The largest blocks: closed several at a time as they lie (chains, a
+    prompt of 512 rows), and gathered from a tree's path."""
+    say("256 dims", page, int8)
+    sv = Serving(w12, 2, 2, 3, 256, page, int8, seed=28, step_rows=256, layers=2)
+    sv.step([page - 5, 256])
+    sv.step([250, 1])
+    for _ in range(4):
+        rows = [40, 40]
+        sv.step(rows, parents=[np.array([-1] + [max(0, i - 1 - int(sv.rng.rand() < 0.2)) for i in range(1, n)], np.int32) for n in rows])
+    sv = Serving(w12, 1, 1, 2, 256, page, int8, seed=29, step_rows=512)
+    sv.step([45])
+    sv.step([512])
+    sv.step([3])
+
+
+def test_one_kv_head_for_256_query_heads(w12):
+    say("256 query heads")
+    sv = Serving(w12, 2, 1, 256, 64, 32, seed=30)
+    sv.step([40, 3])
+    sv.step([3, 1], parents=[np.array([-1, 0, 0]), np.array([-1])])
+
+
+def test_offsets_past_32_bits(w12):
+    """Pages and recent rows more than 2^32 bytes (and 2^31 values) into their
+    arrays: the same bits as in a small cache."""
+    import torch
+    say("32 bits")
+    dim, page, kv, heads = 256, 128, 1, 3
+    rng = np.random.RandomState(31)
+    big = w12.kv_cache(2, kv, dim, 40000, 30000, 4, page, 32, False, DEV)  # 5 GB of pages, 10 GB of recent rows
+    small = w12.kv_cache(1, kv, dim, 8, 2, 4, page, 32, False, DEV)
+    assert big.pages.numel() > 1 << 32 and big.recent.numel() > 1 << 32
+    at, slots = np.array([[39999, 39990, 39001, 39000], [3, 39998, 5, 39997]]), [29999, 29998]
+    big.page_table[slots] = i32(at)
+    small.page_table.copy_(i32([[0, 1, 2, 3], [4, 5, 6, 7]]))
+    rope = torch.tensor(rope_table(600, dim), device=DEV)
+    for n in (32, 32, 32, 32, 32, 1, 32, 32, 32, 32, 7):
+        off = i32([0, n, 2 * n])
+        x = torch.tensor(rng.randn(2 * n, (heads + 2 * kv) * dim), dtype=torch.float32, device=DEV)
+        res = []
+        for c, layer, slot in ((big, 1, i32(slots)), (small, 0, None)):
+            q = w12.w12_kv_append(c, layer, x, off, rope, heads, slot=slot)
+            res.append(w12.w12_kv_attention(c, layer, q, off, slot=slot))
+            w12.w12_kv_commit(c, off, i32([n - 1, n - 1]), slot=slot)
+        assert torch.isfinite(res[0].float()).all() and torch.equal(res[0], res[1])
+    assert big.length[slots].tolist() == small.length.tolist() == [296, 296]
+    for s in (0, 1):
+        for b in (0, 1):
+            assert torch.equal(big.pages[1, at[s, b]].view(torch.uint8), small.pages[0, 4 * s + b].view(torch.uint8))
+            assert torch.equal(big.scales[1, at[s, b]], small.scales[0, 4 * s + b])
+
+
+def test_workspace_over_queries_or_output_is_refused(w12):
+    import torch
+    say("workspace overlap")
+    c = w12.kv_cache(1, 2, 64, 4, 1, 2, 32, 16, False, DEV)
+    off, n = i32([0, 4]), 4 * 4 * 64 * 2
+    free = torch.zeros(96 << 20, dtype=torch.uint8, device=DEV)
+    ws = free[1 << 20:65 << 20]
+    q = torch.ones(4, 4, 64, dtype=torch.bfloat16, device=DEV)
+    c.recent.zero_()
+    w12.w12_kv_attention(c, 0, q, off, ws=ws)
+    for at in ((1 << 20) - 256, 1 << 20, 8 << 20):
+        over = free[at:at + n].view(torch.bfloat16)
+        with pytest.raises(w12.W12Error, match="EINVAL"):
+            w12.w12_kv_attention(c, 0, q, off, ws=ws, out=over)
+        over.copy_(q.view(-1))
+        with pytest.raises(w12.W12Error, match="EINVAL"):
+            w12.w12_kv_attention(c, 0, over.view(4, 4, 64), off, ws=ws)
+    w12.w12_kv_attention(c, 0, q, off, ws=ws, out=free[(1 << 20) - n:1 << 20].view(torch.bfloat16))

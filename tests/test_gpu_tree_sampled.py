@@ -248,3 +248,46 @@ def test_draft_rows_of_nodes_without_children_are_not_read(w12):
     got = both(w12, f)
     assert got[0].tolist() == [0] * 12 + [5] * 4
     assert all(np.array_equal(a, b) for a, b in zip(got, want))
+
+
+def test_rows_past_32_bits(w12):
+    """Logits of more than 2^32 bytes and 2^31 values: trees at both ends draw
+    what they draw alone."""
+    import torch
+    say("32 bits")
+    vocab, trees = 152064, 15000
+    gen = torch.Generator(device=DEV).manual_seed(21)
+    logits = torch.randn((trees, vocab), generator=gen, device=DEV, dtype=torch.bfloat16)  # 4.6 GB
+    logits *= 3
+    # the last tree: a root and four children
+    sizes = [1] * (trees - 5) + [5]
+    off = np.concatenate([[0], np.cumsum(sizes)]).astype(np.int32)
+    parent = np.full(trees, -1, np.int32)
+    parent[-4:] = 0
+    r = np.random.RandomState(22)
+    token = np.zeros(trees, np.int32)
+    token[-4:] = logits[-5].float().topk(4).indices.cpu().numpy()
+    u, ub = r.rand(trees).astype(np.float32), r.rand(len(sizes)).astype(np.float32)
+    t = lambda a: torch.tensor(a, device=DEV)
+    got = [x.cpu().numpy() for x in w12.tree_accept_sampled(t(off), t(parent), t(token), logits, t(u), t(ub))]
+    for tree in (0, 1, 7000, 14123, 14124, trees - 6, trees - 5):
+        a, b = off[tree], off[tree + 1]
+        lg = logits[a:b].float().cpu().numpy()
+        acc, way, bonus = TS.walk(parent[a:b], token[a:b], lg, 1.0, None, u[a:b], ub[tree])
+        assert got[0][tree] == acc and got[1][a:a + len(way)].tolist() == way and got[2][tree] == bonus, tree
+
+
+def test_no_trees_and_many_empty_ones(w12):
+    """Trees without nodes are refused one by one; the others stand."""
+    say("empty")
+    f = forest(23, [4, 3], 500, False)
+    want = both(w12, f)
+    f["off"] = np.array([0] * 70 + [4] * 70 + [7] * 3, np.int32)
+    n = len(f["off"]) - 1
+    temp, ub = np.ones(n, np.float32), np.zeros(n, np.float32)
+    temp[[69, 139]], ub[[69, 139]] = f["temp"], f["ub"]
+    f["temp"], f["ub"] = temp, ub
+    got = call(w12, f)
+    keep = np.isin(np.arange(n), [69, 139])
+    assert got[0][keep].tolist() == want[0].tolist() and got[2][keep].tolist() == want[2].tolist()
+    assert (got[0][~keep] == -1).all() and (got[2][~keep] == -1).all() and np.array_equal(got[1], want[1])
