@@ -15,8 +15,6 @@
 namespace w12 {
 namespace {
 
-typedef uint32_t u32x4v __attribute__((ext_vector_type(4)));
-
 __device__ __forceinline__ float bf16_f32(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
 
 // ---------------------------------------------------------------------------- append

@@ -9,7 +9,6 @@
 namespace w12 {
 
 constexpr int kStepRows = 512;  // rows (and so sequences) of one step, as in w12_gemm
-constexpr int kMaxPage = 128;   // tokens per page: 32, 64, 96 or 128
 constexpr int kMaxHeads = 256;  // query heads
 constexpr int kGroup = 32;      // tokens per fragment group
 

@@ -37,6 +37,13 @@ constexpr int kThreads = 256;  // of the launches over chunks: four chunks a wor
 constexpr int kWaves = kThreads / 64;
 constexpr int kTreeNodes = 1024;  // most nodes of a tree
 
+// Where a tree's walk ended.
+struct alignas(16) State {
+  double sum, c;  // of the last row; c: the residual is max(p - c q, 0)
+  float max;
+  int row;  // last row, -1: no token to draw
+};
+
 struct Layout {
   int splits;
   size_t off_stat, off_sum, off_state, off_cnt, total;  // in the workspace
@@ -47,18 +54,10 @@ __host__ __device__ __forceinline__ Layout layout_of(int num_trees, int total, i
   l.off_stat = 0;                                               // [total][splits] (max, sum)
   l.off_sum = l.off_stat + (size_t)total * l.splits * 16;       // [num_trees][splits] (residual, p)
   l.off_state = l.off_sum + (size_t)num_trees * l.splits * 16;  // [num_trees] State
-  l.off_cnt = l.off_state + (size_t)num_trees * 48;
+  l.off_cnt = l.off_state + (size_t)num_trees * sizeof(State);
   l.total = l.off_cnt + (((size_t)num_trees * 4 + 15) & ~size_t(15));
   return l;
 }
-
-// Where a tree's walk ended.
-struct State {
-  double sum, c;  // of the last row; c: the residual is max(p - c q, 0)
-  float max;
-  int row, node;  // last row, -1: no token to draw; its node in the tree
-  int pad[3];
-};
 
 __device__ __forceinline__ float logit(const SampledArgs& a, int row, int t) {
   const size_t at = (size_t)row * a.vocab + t;
@@ -564,7 +563,6 @@ __global__ __launch_bounds__(NT) void sampled_walk_kernel(SampledArgs a) {
       s.sum = bad ? 0.0 : s_sum[last];
       s.c = c;
       s.row = bad ? -1 : b0 + last;
-      s.node = last;
       *state = s;
     }
     s_kids = 0;
