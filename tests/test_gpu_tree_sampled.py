@@ -291,3 +291,20 @@ def test_no_trees_and_many_empty_ones(w12):
     keep = np.isin(np.arange(n), [69, 139])
     assert got[0][keep].tolist() == want[0].tolist() and got[2][keep].tolist() == want[2].tolist()
     assert (got[0][~keep] == -1).all() and (got[2][~keep] == -1).all() and np.array_equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("vocab,kids", [(5000, 1023), (300, 1023), (70000, 200)])
+def test_many_siblings_that_share_tokens(w12, vocab, kids):
+    """A node of as many children as a tree can have, most of them with a
+    token that an earlier sibling had, several in a chunk of the vocabulary:
+    accepted early, late and not at all."""
+    say("siblings", vocab, kids)
+    r = np.random.RandomState(24)
+    for u in (0.0, 0.9, 0.995, np.float32(1) - np.float32(2.0 ** -20)):
+        f = forest(25, [kids + 1, 3], vocab, False, spread=1.0)
+        f["parent"][1:kids + 1] = 0
+        f["token"][1:kids + 1] = r.choice(r.permutation(vocab)[:vocab // 20], kids)
+        f["u"][:] = u
+        f["temp"][:] = 1.0
+        got = both(w12, f)
+    assert got[0][0] == 0  # the last of them

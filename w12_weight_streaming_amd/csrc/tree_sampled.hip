@@ -494,7 +494,13 @@ __global__ __launch_bounds__(NT) void sampled_walk_kernel(SampledArgs a) {
     for (int i = tid + 1; i < n; i += kWalkThreads) {
       const int up = s_parent[i], row = b0 + up;
       s_p[i] = Weigher(s_pow, s_max[up], it2)(i == tid + 1 ? first_logit : logit(a, row, s_token[i])) / s_sum[up];
-      if (a.draft) s_q[i] = a.draft[(size_t)row * a.vocab + s_token[i]];
+      if (a.draft) {
+        s_q[i] = a.draft[(size_t)row * a.vocab + s_token[i]];
+      } else {  // a token that an earlier sibling's rejection takes out of p: nothing is left of it
+        bool again = false;
+        for (int j = 1; j < i; ++j) again = again || (s_parent[j] == up && s_token[j] == s_token[i]);
+        if (again) s_p[i] = 0.0;
+      }
     }
     __syncthreads();
     int node = 0;
@@ -533,15 +539,11 @@ __global__ __launch_bounds__(NT) void sampled_walk_kernel(SampledArgs a) {
           }
           left = block_sum<kWalkThreads>(r, s_red);
         } else {
-          bool again = false;
-          for (int j = s_first[node]; j != k; j = s_next[j]) again = again || s_token[j] == s_token[k];
-          if (!again) {
-            if (u * left < p) {
-              chosen = k;
-              break;
-            }
-            left -= p;
+          if (p > 0.0 && u * left < p) {
+            chosen = k;
+            break;
           }
+          left -= p;
         }
       }
       node = chosen;
@@ -585,9 +587,13 @@ __global__ __launch_bounds__(NT) void sampled_walk_kernel(SampledArgs a) {
       if (j >= 0 && j < kChunk) atomicOr(&gone[j >> 5], 1u << (j & 31));
     }
   };
-  // chunks with a child's token, summed anew by a wave each
+  // chunks with a child's token, summed anew by a wave each, for the first of
+  // their children on the list
   for (int k = wave; k < kids; k += kWalkThreads / 64) {
     const int chunk = s_list[k] / kChunk;
+    bool done = false;
+    for (int j = lane; j < k; j += 64) done = done || s_list[j] / kChunk == chunk;
+    if (__any(done)) continue;
     uint32_t* gone = s_gone[wave];
     if (lane < kChunk / 32) gone[lane] = 0;
     wave_lds_sync();
@@ -610,7 +616,10 @@ __global__ __launch_bounds__(NT) void sampled_walk_kernel(SampledArgs a) {
     double r = v.x > -__builtin_huge_val() ? v.y * weigh((float)v.x) : 0.0;
     if (taken)
       for (int k = 0; k < kids; ++k)
-        if (s_list[k] / kChunk == i) r = s_fix[k];
+        if (s_list[k] / kChunk == i) {
+          r = s_fix[k];
+          break;
+        }
     return r;
   };
   double total = 0.0;
