@@ -867,3 +867,22 @@ def test_workspace_over_queries_or_output_is_refused(w12):
         with pytest.raises(w12.W12Error, match="EINVAL"):
             w12.w12_kv_attention(c, 0, over.view(4, 4, 64), off, ws=ws)
     w12.w12_kv_attention(c, 0, q, off, ws=ws, out=free[(1 << 20) - n:1 << 20].view(torch.bfloat16))
+
+
+def test_commit_of_512_sequences_that_share_slots(w12):
+    """The first sequence of a slot stands, refused or not, however far the
+    others are behind it; slots of none are left as they are."""
+    say("shared slots")
+    slots, seqs = 400, 512
+    c = w12.kv_cache(1, 1, 64, 8, slots, 1, 32, 16, False, DEV)
+    rng = np.random.RandomState(32)
+    slot = rng.randint(-3, slots + 3, seqs)
+    acc = rng.choice([-1, 0, 0, 0, 1], seqs)  # of one row each: 1 is refused
+    length = rng.randint(0, 20, slots)
+    c.length.copy_(i32(length))
+    want = np.full(slots, 77)
+    for s in reversed(range(seqs)):
+        if 0 <= slot[s] < slots:
+            want[slot[s]] = -1 if acc[s] == 1 else length[slot[s]] + acc[s] + 1
+    out = w12.w12_kv_commit(c, i32(np.arange(seqs + 1)), i32(acc), slot=i32(slot), length_out=i32(np.full(slots, 77)), rows=seqs)
+    assert out.tolist() == want.tolist()

@@ -158,6 +158,7 @@ struct CommitView {
   SeqView v;
   int n;  // accepted rows, root included
   bool ok;
+  bool again;  // an earlier sequence names its slot, and speaks for it
 };
 __device__ __forceinline__ CommitView commit_view(const CommitArgs& a, int s, int* s_src, int* s_bad) {
   const int tid = threadIdx.x;
@@ -168,8 +169,10 @@ __device__ __forceinline__ CommitView commit_view(const CommitArgs& a, int s, in
   const int acc = a.accept_len[s];
   w.n = w.v.ok ? acc + 1 : 0;
   int bad = (!w.v.ok || acc < -1 || acc >= w.v.rows) ? 1 : 0;
-  for (int j = tid; j < s; j += blockDim.x)
-    if ((a.st.slot && a.st.slot[j] == w.v.slot) || rows_meet(a.st.row_off, a.st.total, j, w.v.row0, w.v.rows)) bad = 1;
+  for (int j = tid; j < s; j += blockDim.x) {
+    if (a.st.slot && a.st.slot[j] == w.v.slot) bad |= 2;
+    if (rows_meet(a.st.row_off, a.st.total, j, w.v.row0, w.v.rows)) bad |= 1;
+  }
   if (!bad) {
     for (int j = tid; j < w.n; j += blockDim.x) {
       int p = j;
@@ -189,9 +192,10 @@ __device__ __forceinline__ CommitView commit_view(const CommitArgs& a, int s, in
       }
     }
   }
-  if (bad) *s_bad = 1;
+  if (bad) atomicOr(s_bad, bad);
   __syncthreads();
   w.ok = *s_bad == 0;
+  w.again = *s_bad & 2;
   return w;
 }
 
@@ -383,10 +387,7 @@ __global__ __launch_bounds__(64) void kv_commit_len_kernel(CommitArgs a) {
   const int s = blockIdx.x;
   const CommitView w = commit_view(a, s, s_src, &s_bad);
   const int slot = a.st.slot ? a.st.slot[s] : s;
-  if (threadIdx.x != 0 || slot < 0 || slot >= a.c.slots) return;
-  if (a.st.slot)
-    for (int j = 0; j < s; ++j)
-      if (a.st.slot[j] == slot) return;  // the first sequence of a slot speaks for it
+  if (threadIdx.x != 0 || slot < 0 || slot >= a.c.slots || w.again) return;
   a.len_out[slot] = w.ok ? w.v.len + w.n : -1;
 }
 
