@@ -489,18 +489,22 @@ __global__ __launch_bounds__(NT) void sampled_walk_kernel(SampledArgs a) {
       }
       s_first[i] = first;
       s_next[i] = i == 0 ? -1 : next;
+      if (!a.draft) {  // a token that an earlier sibling's rejection takes out of p: nothing is left of it
+        const int up = s_parent[i], tok = s_token[i];
+        int again = 0;
+#pragma unroll 4
+        for (int j = 1; j < i; ++j) again |= (s_parent[j] == up) & (s_token[j] == tok);
+        s_q[i] = again ? 0.f : 1.f;
+      }
     }
     __syncthreads();
     for (int i = tid + 1; i < n; i += kWalkThreads) {
       const int up = s_parent[i], row = b0 + up;
       s_p[i] = Weigher(s_pow, s_max[up], it2)(i == tid + 1 ? first_logit : logit(a, row, s_token[i])) / s_sum[up];
-      if (a.draft) {
+      if (a.draft)
         s_q[i] = a.draft[(size_t)row * a.vocab + s_token[i]];
-      } else {  // a token that an earlier sibling's rejection takes out of p: nothing is left of it
-        bool again = false;
-        for (int j = 1; j < i; ++j) again = again || (s_parent[j] == up && s_token[j] == s_token[i]);
-        if (again) s_p[i] = 0.0;
-      }
+      else if (s_q[i] == 0.f)
+        s_p[i] = 0.0;
     }
     __syncthreads();
     int node = 0;
