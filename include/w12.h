@@ -375,8 +375,8 @@ w12_status tree_accept(int32_t num_trees, const int32_t *node_off,
  * such fragments are ordered by 32 tokens, then by 32 dims.
  * Sizes: page_tokens 32, 64, 96 or 128; head_dim 64, 128 or 256; recent_rows
  * a multiple of 32 in [page_tokens, 1024]; kv_heads <= 256; slots <= 2^20;
- * max_pages * page_tokens <= 2^30. pages and recent 16-byte, scales 8-byte
- * aligned.
+ * max_pages * page_tokens <= 2^30; layers <= 1024; query heads a multiple of
+ * kv_heads, at most 256. pages and recent 16-byte, scales 8-byte aligned.
  *
  * A step's calls share its rows: sequence s owns rows [row_off[s],
  * row_off[s + 1]) of total_rows (at most 512, at most 512 sequences), a tree
@@ -432,8 +432,10 @@ w12_status w12_kv_attention_workspace(const w12_kv_cache *cache, int32_t num_seq
  * sequence's committed tokens and to its own ancestors among the step's rows,
  * itself included,
  *   out[i, h] = softmax(scale q[i, h] . K) V,  kv head h / (q_heads / kv_heads),
+ *   scale > 0, finite,
  * with fp32 scores, sums and accumulation; probabilities and 8-bit codes
- * enter the matrix products as bf16 (the codes exactly). Infinities and NaN
+ * enter the matrix products as bf16 (the codes exactly, a probability off by
+ * up to 2^-8 of itself, in the sum as in the product). Infinities and NaN
  * in rows that a row does not see never reach it. The split of long
  * sequences over workgroups is in a fixed order: results are bitwise
  * reproducible.
@@ -495,7 +497,8 @@ w12_status tree_accept_sampled_workspace(int32_t num_trees, int32_t total_nodes,
  * token is the lowest t whose cumulative sum of p exceeds u_bonus[tree] times
  * the whole sum (the last token with p > 0 if none does). The tokens that come
  * out are distributed as if drawn from the target alone.
- * Probabilities, sums and comparisons are held in 64 bits.
+ * Probabilities, sums and comparisons are held in 64 bits; an exponential
+ * e^-a is off by up to 2e-15 + 2e-16 a of itself, some of its last bits.
  *   logits  [total_nodes][vocab] fp32 or bf16 (logits_type a w12_ydtype),
  *           w12_gemm's y of the head; vocab <= 2^28.
  *   temperature [num_trees] fp32 > 0, or NULL (1); draft [total_nodes][vocab]
