@@ -478,6 +478,135 @@ w12_status w12_kv_commit(const w12_kv_cache *cache, int32_t num_seq, const int32
                          int32_t total_rows, const int32_t *accept_len, const int32_t *path, int32_t *len_out,
                          hipStream_t stream);
 
+/*
+ * Recurrent layers of the verify pass (gated delta rule; [S1] 4.2: most
+ * layers of the target are recurrent, their state is recomputed along each
+ * root path, without a snapshot for each node, and the accepted path is
+ * replayed into it). Per layer a step calls w12_delta_append, then
+ * w12_delta_rule; w12_delta_commit keeps the accepted rows of all layers.
+ *   state [layers][slots][value_heads][key_dim][value_dim] fp32: the state S
+ *         of each sequence's committed tokens (zeros: none);
+ *   conv  [layers][slots][conv_width - 1][channels] bf16: the convolution's
+ *         window, the last inputs of the committed tokens, oldest first
+ *         (zeros: before the first token), channels = 2 key_heads key_dim +
+ *         value_heads value_dim;
+ * and what the rows of one step leave for the calls behind, by the step's row:
+ *   raw   [layers][step_rows][channels] bf16: the convolution's inputs;
+ *   kv    [layers][step_rows][key_heads key_dim + value_heads value_dim]
+ *         bf16: key heads, value heads;
+ *   gates [layers][step_rows][2][value_heads] fp32: g (log of the decay, <= 0)
+ *         and beta (strength) of each value head;
+ *   delta [layers][step_rows][value_heads][value_dim] fp32: what a row adds
+ *         to the state, S += k delta^T.
+ * Value head h goes with key head h / (value_heads / key_heads). The rows of
+ * a step are described as for the KV cache above: row_off, slot, parent (NULL:
+ * chains), at most 512 rows and at most step_rows. These four arrays belong
+ * to one step at a time: two steps in flight have a description each, over
+ * the same state and conv. A slot may be named by several sequences of a
+ * step, except where a call keeps rows.
+ * Sizes: key_dim and value_dim 64 or 128; value_heads a multiple of
+ * key_heads, at most 256; conv_width 2, 3 or 4; layers <= 1024; slots <=
+ * 2^20; step_rows <= 65536. All arrays 16-byte aligned, and apart.
+ */
+typedef struct w12_delta_cache {
+  int32_t layers, slots, step_rows, key_heads, value_heads, key_dim, value_dim, conv_width;
+  float *state;
+  uint16_t *conv;
+  uint16_t *raw;
+  uint16_t *kv;
+  float *gates;
+  float *delta;
+} w12_delta_cache;
+
+/*
+ * w12_delta_append -- the inputs of a recurrent layer's rows. With x_0 a
+ * row's input (qkv, rounded to bf16), x_1 its parent's, and so on, past the
+ * root the slot's window from its newest entry back,
+ *   y[c] = conv_bias[c] + sum_t conv_weight[c][conv_width - 1 - t] x_t[c],
+ *   s = y / (1 + e^-y); query and key heads: s / sqrt(sum s^2 + 1e-6);
+ *   beta = 1 / (1 + e^-b),  g = -e^a_log log(1 + e^(a + dt_bias)),
+ * in fp32; queries, keys and values rounded to bf16 once.
+ *   qkv  [total_rows] rows of channels values, qkv_stride values apart (a
+ *        multiple of 16 bytes): query heads, key heads, value heads;
+ *   ba   [total_rows] rows of 2 value_heads values, ba_stride apart: b, then
+ *        a; both fp32 or both bf16 (type a w12_ydtype): columns of one fused
+ *        product as they lie;
+ *   conv_weight [channels][conv_width] fp32, the row's own tap last;
+ *   conv_bias [channels] fp32 or NULL; a_log, dt_bias [value_heads] fp32;
+ *   q    [total_rows][key_heads][key_dim] bf16 out, apart from qkv and ba.
+ * Writes raw, kv and gates of its rows; state and conv are read at most.
+ * Device-detected, reported as NaN queries with nothing staged: an invalid
+ * tree, a slot outside [0, slots).
+ */
+w12_status w12_delta_append(const w12_delta_cache *cache, int32_t layer, int32_t num_seq, const int32_t *slot,
+                            const int32_t *row_off, int32_t total_rows, const int32_t *parent, const void *qkv,
+                            int64_t qkv_stride, const void *ba, int64_t ba_stride, int type, const float *conv_weight,
+                            const float *conv_bias, const float *a_log, const float *dt_bias, uint16_t *q,
+                            hipStream_t stream);
+
+/*
+ * w12_delta_rule -- the gated delta rule over the step's rows. Along a row's
+ * root path, from its slot's state,
+ *   S <- e^g S;  delta = beta (v - S^T k);  S <- S + k delta^T;
+ *   out[i, h] = scale S^T q[i],  scale finite,
+ * with fp32 states, deltas and accumulation (a factor that is not bf16 enters
+ * the matrix products whole: in fp32, or in three bf16 pieces that hold its 24 bits)
+ * and decays summed in 64 bits. A row sees its ancestors and itself: an
+ * infinity or NaN in a row's q, k, v or gates reaches only its own outputs
+ * and those behind it (whole heads of them), never other rows'.
+ *   q    [total_rows][key_heads][key_dim] bf16 (w12_delta_append's output);
+ *   out  [total_rows][value_heads * value_dim] bf16, apart from q;
+ *   keep 0: writes the rows' delta; state and conv stay, and w12_delta_commit
+ *        keeps the accepted rows. Not 0 (parent NULL only: prompts, plain
+ *        decoding): every row is kept, state and conv become those behind the
+ *        last row, and delta is not written.
+ * Device-detected, reported as NaN outputs of the sequence with nothing else
+ * written: what w12_delta_append lists, and with keep a slot of an earlier
+ * sequence of the call. Results are bitwise reproducible.
+ */
+w12_status w12_delta_rule(const w12_delta_cache *cache, int32_t layer, int32_t num_seq, const int32_t *slot,
+                          const int32_t *row_off, int32_t total_rows, const int32_t *parent, const uint16_t *q,
+                          float scale, int32_t keep, uint16_t *out, hipStream_t stream);
+
+/*
+ * w12_delta_commit -- keeps the accepted rows of a step, in all layers at
+ * once: rows path[0 .. accept_len] of each sequence (tree_accept's outputs, as
+ * for w12_kv_commit; NULL: the first accept_len + 1 rows) join the state,
+ *   S <- e^G_n S + sum_j e^(G_n - G_j) k_j delta_j^T,  G_j = g_0 + ... + g_j
+ * along the path, and the window.
+ *   kept [num_seq] out: rows kept; accept_len -1 (a refused tree) keeps none.
+ * Device-detected, reported as kept -1 with nothing written: a slot outside
+ * [0, slots) or of an earlier sequence, an accept_len or path outside the
+ * sequence's rows or not ascending from row 0.
+ */
+w12_status w12_delta_commit(const w12_delta_cache *cache, int32_t num_seq, const int32_t *slot, const int32_t *row_off,
+                            int32_t total_rows, const int32_t *accept_len, const int32_t *path, int32_t *kept,
+                            hipStream_t stream);
+
+/*
+ * w12_norm -- what stands between two products: the norm behind a block, its
+ * gate, the residual and its scale, the norm before the next block. For each
+ * row and each of its groups of width values, with rms(x) = x / sqrt(mean x^2
+ * + eps) and every absent part left out,
+ *   t = y;  t = rms(t) post_weight;  t = t gate / (1 + e^-gate);
+ *   h = h + scale t, rounded to h's type;  out = rms(u) weight,
+ * u = h as it is stored, or t where there is no h; out rounded to bf16 once,
+ * all else in fp32. So the norm before a block is (y, h, weight); the gated
+ * norm of a recurrent layer's heads (y, post_weight, gate) with groups =
+ * value_heads; the product between Wgate|Wup and Wdown (y, gate).
+ *   y    [rows] rows of groups * width values, y_stride values apart; NULL
+ *        (with h): h stays as it is, and there is no post_weight and no gate;
+ *   gate as y, or NULL; y_type and gate_type w12_ydtypes;
+ *   h    [rows][groups * width], h_type a w12_ydtype, or NULL;
+ *   post_weight, weight [width] fp32 or NULL; eps > 0, scale finite;
+ *   out  [rows][groups * width] bf16. out, h and the inputs are apart.
+ * rows <= 2^24, groups <= 1024, width <= 32768. Any width and stride; the
+ * fastest where rows and groups begin at multiples of 16 bytes.
+ */
+w12_status w12_norm(int64_t rows, int32_t groups, int32_t width, const void *y, int y_type, int64_t y_stride,
+                    const float *post_weight, const void *gate, int gate_type, int64_t gate_stride, float scale,
+                    void *h, int h_type, const float *weight, float eps, uint16_t *out, hipStream_t stream);
+
 /* Workspace bytes tree_accept_sampled needs (host output). */
 w12_status tree_accept_sampled_workspace(int32_t num_trees, int32_t total_nodes, int32_t vocab, size_t *bytes);
 

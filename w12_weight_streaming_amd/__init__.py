@@ -5,7 +5,8 @@ Thin ctypes binding over libw12.so (C ABI in include/w12.h), with the same
 names as the C entry points: w12_pack, w12_decode, w12_check, w12_gemm,
 w12_head_argmax, tree_accept, and for the pass's KV cache and sampling
 requests w12_kv_append, w12_kv_attention, w12_kv_commit and
-tree_accept_sampled. Every step of the path runs in the library's
+tree_accept_sampled; for its recurrent layers w12_delta_append,
+w12_delta_rule and w12_delta_commit, and w12_norm between products. Every step of the path runs in the library's
 HIP kernels; this module only checks tensor dtypes/devices, passes device
 pointers and the current HIP stream, and keeps zero-filled workspaces.
 There is no CPU fallback: without the built library every call raises.
@@ -55,6 +56,12 @@ class W12KvCache(ctypes.Structure):
                [(n, ctypes.c_void_p) for n in ("pages", "scales", "recent", "page_table", "len")]
 
 
+class W12DeltaCache(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("layers", "slots", "step_rows", "key_heads", "value_heads", "key_dim",
+                                              "value_dim", "conv_width")] + \
+               [(n, ctypes.c_void_p) for n in ("state", "conv", "raw", "kv", "gates", "delta")]
+
+
 def lib() -> ctypes.CDLL:
     """The loaded libw12.so; raises if it has not been built."""
     global _lib
@@ -67,6 +74,7 @@ def lib() -> ctypes.CDLL:
         vp, i64, i32, sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t
         mp = ctypes.POINTER(W12Matrix)
         kp = ctypes.POINTER(W12KvCache)
+        dp = ctypes.POINTER(W12DeltaCache)
         sig = {
             "w12_strerror": (ctypes.c_char_p, [ctypes.c_int]),
             "w12_abi_version": (ctypes.c_int, []),
@@ -99,6 +107,12 @@ def lib() -> ctypes.CDLL:
             "tree_accept_sampled_workspace": (ctypes.c_int, [i32, i32, i32, ctypes.POINTER(sz)]),
             "tree_accept_sampled": (ctypes.c_int, [i32, vp, i32, vp, vp, vp, ctypes.c_int, i32, vp, vp, vp, vp, vp, vp,
                                                    vp, vp, sz, vp]),
+            "w12_delta_append": (ctypes.c_int, [dp, i32, i32, vp, vp, i32, vp, vp, i64, vp, i64, ctypes.c_int, vp, vp, vp,
+                                                vp, vp, vp]),
+            "w12_delta_rule": (ctypes.c_int, [dp, i32, i32, vp, vp, i32, vp, vp, ctypes.c_float, i32, vp, vp]),
+            "w12_delta_commit": (ctypes.c_int, [dp, i32, vp, vp, i32, vp, vp, vp, vp]),
+            "w12_norm": (ctypes.c_int, [i64, i32, i32, vp, ctypes.c_int, i64, vp, vp, ctypes.c_int, i64, ctypes.c_float,
+                                        vp, ctypes.c_int, vp, ctypes.c_float, vp, vp]),
         }
         for name, (res, args) in sig.items():
             f = getattr(L, name)
@@ -116,7 +130,7 @@ def exported_symbols():
             "w12_gemm_noalloc", "w12_cert8_pack", "w12_head_argmax_certified_workspace",
             "w12_head_argmax_certified", "w12_kv_append", "w12_kv_attention_workspace",
             "w12_kv_attention", "w12_kv_commit", "tree_accept_sampled_workspace",
-            "tree_accept_sampled"]
+            "tree_accept_sampled", "w12_delta_append", "w12_delta_rule", "w12_delta_commit", "w12_norm"]
 
 
 def _ok(status: int, what: str):
@@ -673,3 +687,209 @@ def tree_accept_sampled(node_off: torch.Tensor, parent: torch.Tensor, token: tor
     _run(index, "tree_accept_sampled", T, at_off, total, *at, at_x, W12_Y_F32 if logits.dtype is _F32 else W12_Y_BF16,
          vocab, at_temp, at_draft, *at_u, base, base + 8 * T, base + 4 * T, *scratch)
     return out[:T], out[2 * T:], out[T:2 * T]
+
+
+# ------------------------------------------------------------------ recurrent layers of the verify pass
+
+@dataclass(frozen=True, eq=False)  # the description holds the arrays' addresses
+class DeltaCache:
+    """Device-resident state of the recurrent layers: the arrays of
+    include/w12.h. state is [layers, slots, value_heads, key_dim, value_dim]
+    float32, conv [layers, slots, conv_width - 1, channels] bfloat16; of one
+    step at a time raw [layers, step_rows, channels] bfloat16, kv [layers,
+    step_rows, key_heads * key_dim + value_heads * value_dim] bfloat16, gates
+    [layers, step_rows, 2, value_heads] float32, delta [layers, step_rows,
+    value_heads, value_dim] float32. The arrays stay the same; their contents
+    may be written at any time (a new sequence: its slot of state and conv
+    zeroed)."""
+    state: torch.Tensor
+    conv: torch.Tensor
+    raw: torch.Tensor
+    kv: torch.Tensor
+    gates: torch.Tensor
+    delta: torch.Tensor
+    key_heads: int
+
+    def __post_init__(self):
+        at = _get(self.state, _F32, "state", 5, None)
+        index = self.state.get_device()
+        ats = (at, _get(self.conv, _BF16, "conv", 4, index), _get(self.raw, _BF16, "raw", 3, index),
+               _get(self.kv, _BF16, "kv", 3, index), _get(self.gates, _F32, "gates", 4, index),
+               _get(self.delta, _F32, "delta", 4, index))
+        layers, slots, hv, kd, vd = self.state.shape
+        rows = self.raw.shape[1]
+        kv_width = self.key_heads * kd + hv * vd
+        channels = kv_width + self.key_heads * kd
+        width = self.conv.shape[2] + 1
+        if (self.conv.shape != (layers, slots, width - 1, channels) or self.raw.shape != (layers, rows, channels)
+                or self.kv.shape != (layers, rows, kv_width) or self.gates.shape != (layers, rows, 2, hv)
+                or self.delta.shape != (layers, rows, hv, vd)):
+            raise ValueError("the recurrent state's arrays differ in shape")
+        desc = W12DeltaCache(layers, slots, rows, self.key_heads, hv, kd, vd, width, *ats)
+        for name, value in (("index", index), ("value_heads", hv), ("key_dim", kd), ("value_dim", vd),
+                            ("channels", channels), ("conv_width", width), ("_desc", desc), ("_ref", ctypes.byref(desc))):
+            object.__setattr__(self, name, value)
+
+    @property
+    def device(self):
+        return self.state.device
+
+    def desc(self) -> W12DeltaCache:
+        return self._desc
+
+    def nbytes(self) -> int:
+        return sum(t.numel() * t.element_size()
+                   for t in (self.state, self.conv, self.raw, self.kv, self.gates, self.delta))
+
+
+def delta_cache(layers: int, slots: int, key_heads: int, value_heads: int, key_dim: int, value_dim: int,
+                conv_width: int = 4, step_rows: int = MAX_ROWS, device="cuda") -> DeltaCache:
+    """Recurrent layers' state of `slots` fresh sequences, for steps of up to step_rows rows in all."""
+    kv_width = key_heads * key_dim + value_heads * value_dim
+    channels = kv_width + key_heads * key_dim
+    f, b = dict(dtype=torch.float32, device=device), dict(dtype=torch.bfloat16, device=device)
+    return DeltaCache(torch.zeros(layers, slots, value_heads, key_dim, value_dim, **f),
+                      torch.zeros(layers, slots, conv_width - 1, channels, **b),
+                      torch.zeros(layers, step_rows, channels, **b), torch.zeros(layers, step_rows, kv_width, **b),
+                      torch.zeros(layers, step_rows, 2, value_heads, **f),
+                      torch.zeros(layers, step_rows, value_heads, value_dim, **f), key_heads)
+
+
+def _rows_of(t, name: str, columns: int, index: int | None) -> tuple[int, int, int]:
+    """Address, row stride and type of a [rows, columns] fp32 or bf16 tensor
+    whose rows lie apart (columns of a wider product)."""
+    if not isinstance(t, torch.Tensor) or t.dtype not in (_F32, _BF16):
+        raise TypeError(f"{name} must be a float32 or bfloat16 tensor")
+    if t.dim() != 2 or t.shape[1] != columns:
+        raise ValueError(f"{name} must be [rows, {columns}] (got {tuple(t.shape)})")
+    if t.get_device() < 0 or (index is not None and t.get_device() != index):
+        raise ValueError(f"{name} must be on {'a GPU' if index is None else f'cuda:{index}'} (got {t.device})")
+    step, unit = t.stride()
+    if (unit != 1 and columns > 1) or (t.shape[0] > 1 and step < columns):
+        raise ValueError(f"{name}'s rows must be contiguous and apart (strides {t.stride()})")
+    return t.data_ptr(), max(step, columns) if t.shape[0] > 1 else -(-columns // 8) * 8, W12_Y_F32 if t.dtype is _F32 else W12_Y_BF16
+
+
+def w12_delta_append(cache: DeltaCache, layer: int, qkv: torch.Tensor, ba: torch.Tensor, row_off: torch.Tensor,
+                     conv_weight: torch.Tensor, a_log: torch.Tensor, dt_bias: torch.Tensor,
+                     conv_bias: torch.Tensor | None = None, slot: torch.Tensor | None = None,
+                     parent: torch.Tensor | None = None, out: torch.Tensor | None = None) -> torch.Tensor:
+    """Convolution, SiLU, normalised heads and gates of the step's rows, staged
+    for w12_delta_rule and w12_delta_commit. qkv [rows, channels] and ba [rows,
+    2 * value_heads] (b, then a), both fp32 or both bf16, may be columns of one
+    product; conv_weight [channels, conv_width], conv_bias [channels], a_log
+    and dt_bias [value_heads] fp32. Returns q [rows, key_heads, key_dim] bf16."""
+    index, hv, hk, kd = cache.index, cache.value_heads, cache.key_heads, cache.key_dim
+    at_x, step_x, kind = _rows_of(qkv, "qkv", cache.channels, index)
+    at_b, step_b, kind_b = _rows_of(ba, "ba", 2 * hv, index)
+    rows = qkv.shape[0]
+    if kind_b != kind or ba.shape[0] != rows:
+        raise ValueError("qkv and ba differ in type or rows")
+    at_off = _get(row_off, _I32, "row_off", 1, index)
+    seqs = row_off.shape[0] - 1
+    if conv_weight.shape != (cache.channels, cache.conv_width):
+        raise ValueError(f"conv_weight must be [{cache.channels}, {cache.conv_width}]")
+    at_w = _get(conv_weight, _F32, "conv_weight", 2, index)
+    at_c = 0 if conv_bias is None else _get(conv_bias, _F32, "conv_bias", 1, index, cache.channels)
+    at_a, at_d = _get(a_log, _F32, "a_log", 1, index, hv), _get(dt_bias, _F32, "dt_bias", 1, index, hv)
+    if out is None:
+        out = torch.empty(rows, hk, kd, dtype=_BF16, device=qkv.device)
+    elif out.numel() < rows * hk * kd:
+        raise ValueError("out must hold [rows, key_heads, key_dim]")
+    _run(index, "w12_delta_append", cache._ref, layer, seqs,
+         0 if slot is None else _get(slot, _I32, "slot", 1, index, seqs), at_off, rows,
+         0 if parent is None else _get(parent, _I32, "parent", 1, index, rows), at_x, step_x, at_b, step_b, kind, at_w,
+         at_c, at_a, at_d, _get(out, _BF16, "out", None, index))
+    return out
+
+
+def w12_delta_rule(cache: DeltaCache, layer: int, q: torch.Tensor, row_off: torch.Tensor,
+                   slot: torch.Tensor | None = None, parent: torch.Tensor | None = None, scale: float | None = None,
+                   keep: bool = False, out: torch.Tensor | None = None) -> torch.Tensor:
+    """The gated delta rule over the step's staged rows, q [rows, key_heads,
+    key_dim] bf16; returns [rows, value_heads * value_dim] bf16. scale defaults
+    to key_dim ** -0.5. keep (chains only: prompts, plain decoding): every row
+    joins the state and the window, and w12_delta_commit is not called."""
+    index = cache.index
+    at_q = _get(q, _BF16, "q", 3, index)
+    rows, hk, kd = q.shape
+    if hk != cache.key_heads or kd != cache.key_dim:
+        raise ValueError(f"q has {hk} heads of {kd}, the state {cache.key_heads} of {cache.key_dim}")
+    if keep and parent is not None:
+        raise ValueError("keep is for chains: the rows of a tree are kept by w12_delta_commit")
+    at_off = _get(row_off, _I32, "row_off", 1, index)
+    seqs = row_off.shape[0] - 1
+    wide = cache.value_heads * cache.value_dim
+    if out is None:
+        out = torch.empty(rows, wide, dtype=_BF16, device=q.device)
+    elif out.numel() < rows * wide:
+        raise ValueError("out must hold [rows, value_heads * value_dim]")
+    _run(index, "w12_delta_rule", cache._ref, layer, seqs,
+         0 if slot is None else _get(slot, _I32, "slot", 1, index, seqs), at_off, rows,
+         0 if parent is None else _get(parent, _I32, "parent", 1, index, rows), at_q,
+         kd ** -0.5 if scale is None else scale, 1 if keep else 0, _get(out, _BF16, "out", None, index))
+    return out
+
+
+def w12_delta_commit(cache: DeltaCache, row_off: torch.Tensor, accept_len: torch.Tensor,
+                     path: torch.Tensor | None = None, slot: torch.Tensor | None = None,
+                     rows: int | None = None) -> torch.Tensor:
+    """Keeps the accepted rows of the step (tree_accept's accept_len and path;
+    path None: each sequence's first accept_len + 1 rows) in every layer. rows:
+    how many the step had, known from path if there is one (otherwise at most
+    512 and what the staging holds). Returns the rows kept of each sequence
+    [seqs] int32, -1 where it was refused."""
+    index = cache.index
+    at_off = _get(row_off, _I32, "row_off", 1, index)
+    seqs = row_off.shape[0] - 1
+    at_path = 0
+    if path is not None:
+        at_path, rows = _get(path, _I32, "path", 1, index, rows), path.shape[0]
+    elif rows is None:
+        rows = min(MAX_ROWS, cache._desc.step_rows)
+    kept = torch.empty(max(seqs, 0), dtype=_I32, device=cache.device)
+    _run(index, "w12_delta_commit", cache._ref, seqs, 0 if slot is None else _get(slot, _I32, "slot", 1, index, seqs),
+         at_off, rows, _get(accept_len, _I32, "accept_len", 1, index, seqs), at_path, kept.data_ptr())
+    return kept
+
+
+# ------------------------------------------------------------------ norms between products
+
+def w12_norm(y: torch.Tensor | None, weight: torch.Tensor | None = None, post_weight: torch.Tensor | None = None,
+             gate: torch.Tensor | None = None, h: torch.Tensor | None = None, scale: float = 1.0, groups: int = 1,
+             eps: float = 1e-6, out: torch.Tensor | None = None) -> torch.Tensor:
+    """Norm of a block's output y (post_weight), its gate (SiLU), the residual
+    h += scale * that, in place, and the norm before the next block (weight);
+    each part but one of y and h may be absent. y and gate [rows, groups *
+    width] fp32 or bf16 may be columns of wider products, h [rows, groups *
+    width] fp32 or bf16, the weights [width] fp32. Returns bf16 [rows, groups *
+    width]."""
+    first = y if y is not None else h
+    if not isinstance(first, torch.Tensor) or first.dim() != 2:
+        raise TypeError("w12_norm needs y or h, [rows, groups * width]")
+    index, (rows, wide) = first.get_device(), first.shape
+    if groups < 1 or wide % groups:
+        raise ValueError(f"{wide} columns are not {groups} groups")
+    if y is None and (post_weight is not None or gate is not None):
+        raise ValueError("without y there is no post_weight and no gate")
+    width = wide // groups
+    none = (0, wide, W12_Y_F32)
+    at_y = none if y is None else _rows_of(y, "y", wide, index)
+    at_g = none if gate is None else _rows_of(gate, "gate", wide, index)
+    at_h, kind_h = 0, W12_Y_F32
+    if h is not None:
+        if h.dtype not in (_F32, _BF16):
+            raise TypeError("h must be a float32 or bfloat16 tensor")
+        at_h, kind_h = _get(h, h.dtype, "h", 2, index), W12_Y_F32 if h.dtype is _F32 else W12_Y_BF16
+    for t in (gate, h):
+        if t is not None and t.shape != first.shape:
+            raise ValueError("y, gate and h differ in shape")
+    at_p = 0 if post_weight is None else _get(post_weight, _F32, "post_weight", 1, index, width)
+    at_w = 0 if weight is None else _get(weight, _F32, "weight", 1, index, width)
+    if out is None:
+        out = torch.empty(rows, wide, dtype=_BF16, device=first.device)
+    elif out.numel() < rows * wide:
+        raise ValueError("out must hold [rows, groups * width]")
+    _run(index, "w12_norm", rows, groups, width, at_y[0], at_y[2], at_y[1], at_p, at_g[0], at_g[2], at_g[1], scale, at_h,
+         kind_h, at_w, eps, _get(out, _BF16, "out", None, index))
+    return out
