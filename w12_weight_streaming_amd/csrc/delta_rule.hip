@@ -76,6 +76,14 @@ __device__ __forceinline__ uint4 fragment(const uint16_t* p) {
   return make_uint4(a.x, a.y, b.x, b.y);
 }
 
+// The thread's place, derived anew in each phase of the kernel: kept from one
+// phase to the next, addresses made of it take more registers than the states.
+__device__ __forceinline__ int thread_now() {
+  int t = threadIdx.x;
+  asm volatile("" : "+v"(t));
+  return t;
+}
+
 template <int KD, int RT>
 struct Shared {
   static constexpr int R = 16 * RT;
@@ -108,7 +116,7 @@ __device__ __forceinline__ void load_rows(const DeltaRuleArgs& a, Shared<KD, RT>
                                           unsigned long long* odd) {
   using Sh = Shared<KD, RT>;
   constexpr int kPairs = Sh::R / 2, kChunks = KD / 8;
-  for (int e = threadIdx.x; e < kPairs * kChunks; e += kThreads) {
+  for (int e = thread_now(); e < kPairs * kChunks; e += kThreads) {
     const int r = (e % kPairs) * 2, c = (e / kPairs) * 8;
     uint4 x[2];
 #pragma unroll
@@ -136,7 +144,7 @@ template <int KD, int RT>
 __device__ __forceinline__ void load_queries(const DeltaRuleArgs& a, Shared<KD, RT>& s, int row0, int n, int key) {
   using Sh = Shared<KD, RT>;
   constexpr int kChunks = KD / 8;
-  for (int e = threadIdx.x; e < Sh::R * kChunks; e += kThreads) {
+  for (int e = thread_now(); e < Sh::R * kChunks; e += kThreads) {
     const int r = e / kChunks, c = (e % kChunks) * 8;
     uint4 x = make_uint4(0, 0, 0, 0);
     if (r < n) {
@@ -154,7 +162,7 @@ __device__ __forceinline__ void load_queries(const DeltaRuleArgs& a, Shared<KD, 
 template <int KD, int RT>
 __device__ __forceinline__ f32x4 pair_tile(const uint16_t* x, const uint16_t* k, int bi, int bj) {
   constexpr int KS = Shared<KD, RT>::KS;
-  const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
+  const int lane = thread_now() & 63, col = lane & 15, g = lane >> 4;
   f32x4 acc = {0, 0, 0, 0};
 #pragma unroll
   for (int t = 0; t < KD / 32; ++t)
@@ -163,12 +171,13 @@ __device__ __forceinline__ f32x4 pair_tile(const uint16_t* x, const uint16_t* k,
 }
 
 // (I + L)^-1 of a diagonal tile from -L, a column per lane of the first 16, forward substitution.
-__device__ __forceinline__ void invert(const f32x4* low, f32x4* inv) {
-  const int lane = threadIdx.x & 63, c = lane & 15;
+__device__ __forceinline__ void invert(const f32x4* low, f32x4* inv, int n) {
+  const int lane = thread_now() & 63, c = lane & 15;
   float x[16];
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
     float y = i == c ? 1.0f : 0.0f;
+    if (i < n)  // the same for all lanes
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
       if (4 * g < i) {
@@ -179,6 +188,7 @@ __device__ __forceinline__ void invert(const f32x4* low, f32x4* inv) {
       }
     }
     x[i] = y;
+    if (i % 4 == 3) __builtin_amdgcn_sched_barrier(0);  // all rows of L at once would take 160 registers
   }
   if (lane < 16) {
     float* o = reinterpret_cast<float*>(inv);
@@ -187,28 +197,34 @@ __device__ __forceinline__ void invert(const f32x4* low, f32x4* inv) {
   }
 }
 
-template <int KD, int RT, int NC>
-__global__ __launch_bounds__(kThreads) void delta_rule_kernel(DeltaRuleArgs a) {
+template <int KD, int VD, int RT, int NC>
+__global__ __launch_bounds__(kThreads, RT == 1 ? 4 : RT == 2 ? 2 : 1) void delta_rule_kernel(DeltaRuleArgs a) {
   using Sh = Shared<KD, RT>;
   constexpr int R = Sh::R, KS = Sh::KS, TS = Sh::TS, KT = KD / 16;
   __shared__ Sh s;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, col = lane & 15, g = lane >> 4;
-  const int hv = a.c.value_heads, vd = a.c.value_dim;
-  const int slabs = vd / (kWaves * 16 * NC);
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int hv = a.c.value_heads;
+  constexpr int slabs = VD / (kWaves * 16 * NC);
   const int head = blockIdx.x / slabs, key = head / (hv / a.c.key_heads), seq = blockIdx.y;
-  const int v0 = (blockIdx.x - head * slabs) * (kWaves * 16 * NC) + wave * (16 * NC) + col * NC;  // the lane's first value dim
+  const int vw = (blockIdx.x - head * slabs) * (kWaves * 16 * NC) + wave * (16 * NC);  // the wave's first value dim
   const RowsView v = rows_view(a.c, a.st, seq);
   if (v.rows == 0) return;
   if (tid < kStepRows / R) s.odd[tid] = 0;
   if (tid == 0) s.odd_q = 0, s.bad = 0;
 
+  // addresses: a uniform part, and the lane's in 32 bits
   float* state = a.c.state + state_at(a.c, a.layer, v.slot, head);
+  const auto state_place = [&]() {
+    const int lane = thread_now() & 63;
+    return (uint32_t)(4 * (lane >> 4) * VD + vw + (lane & 15) * NC);
+  };
   f32x4 S[KT][NC];
+  const uint32_t at_state = state_place();
 #pragma unroll
   for (int t = 0; t < KT; ++t)
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      const float* p = state + (size_t)(16 * t + 4 * g + r) * vd + v0;
+      const float* p = state + (16 * t + r) * VD + at_state;
       if constexpr (NC == 2) {
         const float2 x = *reinterpret_cast<const float2*>(p);
         S[t][0][r] = x.x;
@@ -240,6 +256,7 @@ __global__ __launch_bounds__(kThreads) void delta_rule_kernel(DeltaRuleArgs a) {
       __syncthreads();
       if (tid == 0) s.odd_q = 0;
       if (!chain && wave == 0) {
+        const int lane = thread_now();
         const bool no = lane < R && ((s.in[(b - 1) * R + min(lane, R - 1)] & s.odd[b - 1]) || s.behind[min(lane, R - 1)]);
         const unsigned long long all = __ballot(no);
         if (lane == 0) s.odd[b - 1] = all;
@@ -254,27 +271,24 @@ __global__ __launch_bounds__(kThreads) void delta_rule_kernel(DeltaRuleArgs a) {
     // values, in the layout of the products
     f32x4 rhs[RT][NC];
     {
+      const int lane = thread_now() & 63, col = lane & 15, g = lane >> 4, v0 = vw + col * NC;
       unsigned long long odd = 0;
+      const uint16_t* values = a.c.kv + kv_at(a.c, a.layer, row0) + (a.c.key_heads * KD + head * VD);
 #pragma unroll
       for (int m = 0; m < RT; ++m)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const int i = 16 * m + 4 * g + r;
-          uint32_t x = 0;
-          if (i < n) {
-            const uint16_t* p = a.c.kv + kv_at(a.c, a.layer, row0 + i) + (size_t)a.c.key_heads * KD + (size_t)head * vd + v0;
-            x = NC == 2 ? *reinterpret_cast<const uint32_t*>(p) : *p;
-            if (odd16(x)) {
-              odd |= 1ull << i;
-              x = 0;
-            }
-          }
+          const uint16_t* p = values + ((uint32_t)min(i, n - 1) * a.c.kv_width + v0);
+          uint32_t x = NC == 2 ? *reinterpret_cast<const uint32_t*>(p) : *p;
+          if (odd16(x) && i < n) odd |= 1ull << i;
+          if (odd16(x) || i >= n) x = 0;
           rhs[m][0][r] = __uint_as_float(x << 16);
           if constexpr (NC == 2) rhs[m][1][r] = __uint_as_float(x & 0xFFFF0000u);
         }
       if (odd) atomicOr(&s.odd[b], odd);
     }
-    if (wave == 0 && lane < R) {  // paths within the block, by doubling; a lane is a row
+    if (const int lane = thread_now(); lane < R) {  // paths within the block, by doubling; a lane is a row
       float gate = 0, beta = 0;
       int cur = -1, leave = -1;
       if (lane < n) {
@@ -319,9 +333,8 @@ __global__ __launch_bounds__(kThreads) void delta_rule_kernel(DeltaRuleArgs a) {
     __syncthreads();
     if (s.bad) {
       if (!(s.bad & 2))
-        for (int i = g; i < v.rows; i += 4)
-#pragma unroll
-          for (int c = 0; c < NC; ++c) a.out[((size_t)(v.row0 + i) * hv + head) * vd + v0 + c] = 0x7FC0;
+        for (int e = thread_now(); e < v.rows * (64 * NC); e += kThreads)
+          a.out[((size_t)(v.row0 + e / (64 * NC)) * hv + head) * VD + (vw - wave * (16 * NC)) + e % (64 * NC)] = 0x7FC0;
       return;
     }
     const int base = chain ? 0 : b * R;  // where the block's rows stand in the tables
@@ -329,6 +342,7 @@ __global__ __launch_bounds__(kThreads) void delta_rule_kernel(DeltaRuleArgs a) {
     // tiles of the block: diagonal ones of L first, each inverted by the wave that made it
     const auto tile = [&](bool of_low, int bi, int bj) {
       f32x4 x = pair_tile<KD, RT>(of_low ? s.k : s.q, s.k, bi, bj);
+      const int lane = thread_now() & 63, col = lane & 15, g = lane >> 4;
       const int i = 16 * bi + col;
       const unsigned long long in = s.in[base + i];
       const double gi = s.sum[base + i];
@@ -344,7 +358,7 @@ __global__ __launch_bounds__(kThreads) void delta_rule_kernel(DeltaRuleArgs a) {
     if (wave < RT) {
       tile(true, wave, wave);
       wave_lds_sync();
-      invert(s.low[wave * RT + wave], s.inv[wave]);
+      invert(s.low[wave * RT + wave], s.inv[wave], n - 16 * wave);
     }
     {
       int u = RT;
@@ -360,6 +374,7 @@ __global__ __launch_bounds__(kThreads) void delta_rule_kernel(DeltaRuleArgs a) {
     // the rows' products with the old state
     f32x4 acc[RT][NC];
     {
+      const int lane = thread_now() & 63, col = lane & 15, g = lane >> 4;
       f32x4 w[RT][NC];
 #pragma unroll
       for (int m = 0; m < RT; ++m)
@@ -382,6 +397,7 @@ __global__ __launch_bounds__(kThreads) void delta_rule_kernel(DeltaRuleArgs a) {
               acc[m][c] = mfma_bf16(fq, piece[c][p], acc[m][c]);
             }
         }
+        __builtin_amdgcn_sched_barrier(0);  // the pieces of one step at a time
       }
 #pragma unroll
       for (int m = 0; m < RT; ++m)
@@ -401,6 +417,7 @@ __global__ __launch_bounds__(kThreads) void delta_rule_kernel(DeltaRuleArgs a) {
     if (!chain) {
       for (int e = b - 1; e >= 0; --e) {
         __syncthreads();
+        const int lane = thread_now() & 63, col = lane & 15, g = lane >> 4, v0 = vw + col * NC;
         load_rows<KD, RT, false>(a, s, v.row0 + e * R, R, key, s.t, &s.odd[e]);
         if (tid < R) {
           const int p = s.next[tid];
@@ -429,13 +446,14 @@ __global__ __launch_bounds__(kThreads) void delta_rule_kernel(DeltaRuleArgs a) {
         }
         __syncthreads();
         const unsigned long long odd = s.odd[e];
+        const float* deltas = a.c.delta + delta_at(a.c, a.layer, v.row0 + e * R, head);  // as this lane wrote them
 #pragma unroll
         for (int mj = 0; mj < RT; ++mj) {
           f32x4 d[NC];
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             const int j = 16 * mj + 4 * g + r;
-            const float* p = a.c.delta + delta_at(a.c, a.layer, v.row0 + e * R + j, head) + v0;  // this lane wrote it
+            const float* p = deltas + ((uint32_t)j * hv * VD + v0);
 #pragma unroll
             for (int c = 0; c < NC; ++c) d[c][r] = (odd >> j) & 1 ? 0.0f : p[c];
           }
@@ -452,6 +470,7 @@ __global__ __launch_bounds__(kThreads) void delta_rule_kernel(DeltaRuleArgs a) {
     __syncthreads();
 
     // the triangular system, and the outputs
+    const int lane = thread_now() & 63, col = lane & 15, g = lane >> 4, v0 = vw + col * NC;
 #pragma unroll
     for (int m = 0; m < RT; ++m)
 #pragma unroll
@@ -465,6 +484,8 @@ __global__ __launch_bounds__(kThreads) void delta_rule_kernel(DeltaRuleArgs a) {
         }
       }
     const unsigned long long odd = s.odd[b], odd_q = s.odd_q;
+    uint16_t* outs = a.out + ((size_t)row0 * hv + head) * VD;
+    float* deltas = a.c.delta + delta_at(a.c, a.layer, row0, head);
 #pragma unroll
     for (int m = 0; m < RT; ++m)
 #pragma unroll
@@ -476,15 +497,15 @@ __global__ __launch_bounds__(kThreads) void delta_rule_kernel(DeltaRuleArgs a) {
           uint16_t o[NC];
 #pragma unroll
           for (int c = 0; c < NC; ++c) o[c] = no_q ? 0x7FC0 : f32_to_bf16_rne(a.scale * acc[m][c][r]);
-          uint16_t* p = a.out + ((size_t)(row0 + i) * hv + head) * vd + v0;
+          const uint32_t at = (uint32_t)i * hv * VD + v0;
+          uint16_t* p = outs + at;
           if constexpr (NC == 2)
             *reinterpret_cast<uint32_t*>(p) = o[0] | ((uint32_t)o[1] << 16);
           else
             *p = o[0];
           if (!a.keep) {
-            float* dp = a.c.delta + delta_at(a.c, a.layer, row0 + i, head) + v0;
 #pragma unroll
-            for (int c = 0; c < NC; ++c) dp[c] = no ? __builtin_nanf("") : rhs[m][c][r];
+            for (int c = 0; c < NC; ++c) deltas[at + c] = no ? __builtin_nanf("") : rhs[m][c][r];
           }
         }
       }
@@ -492,6 +513,7 @@ __global__ __launch_bounds__(kThreads) void delta_rule_kernel(DeltaRuleArgs a) {
 
     // chains: the state behind the block
     if (chain && (a.keep || b + 1 < blocks)) {
+      const int lane = thread_now() & 63, col = lane & 15, g = lane >> 4;
       const float keep = s.grow[n - 1];
 #pragma unroll
       for (int t = 0; t < KT; ++t)
@@ -531,11 +553,12 @@ __global__ __launch_bounds__(kThreads) void delta_rule_kernel(DeltaRuleArgs a) {
     }
   }
   if (!a.keep) return;
+  const uint32_t to_state = state_place();
 #pragma unroll
   for (int t = 0; t < KT; ++t)
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      float* p = state + (size_t)(16 * t + 4 * g + r) * vd + v0;
+      float* p = state + (16 * t + r) * VD + to_state;
 #pragma unroll
       for (int c = 0; c < NC; ++c) p[c] = before ? __builtin_nanf("") : S[t][c][r];
     }
@@ -544,30 +567,25 @@ __global__ __launch_bounds__(kThreads) void delta_rule_kernel(DeltaRuleArgs a) {
                  [&](int j) { return v.row0 + j; });
 }
 
-template <int KD>
+template <int KD, int VD>
 void launch(const DeltaRuleArgs& a, hipStream_t s) {
   const int rows = (a.st.total + a.st.num_seq - 1) / a.st.num_seq;
-  const int heads = a.c.value_heads, wide = a.c.value_dim / 128;
-  const bool pairs = wide > 0 && (int64_t)heads * a.st.num_seq > 512;
-  if (rows <= 16) {
-    if (pairs)
-      delta_rule_kernel<KD, 1, 2><<<dim3(heads, a.st.num_seq), kThreads, 0, s>>>(a);
-    else
-      delta_rule_kernel<KD, 1, 1><<<dim3(heads * (a.c.value_dim / 64), a.st.num_seq), kThreads, 0, s>>>(a);
-  } else if (rows <= 32) {
-    delta_rule_kernel<KD, 2, 1><<<dim3(heads * (a.c.value_dim / 64), a.st.num_seq), kThreads, 0, s>>>(a);
-  } else {
-    delta_rule_kernel<KD, 4, 1><<<dim3(heads * (a.c.value_dim / 64), a.st.num_seq), kThreads, 0, s>>>(a);
-  }
+  const dim3 grid(a.c.value_heads * (VD / 64), a.st.num_seq);
+  if (rows <= 16)
+    delta_rule_kernel<KD, VD, 1, 1><<<grid, kThreads, 0, s>>>(a);
+  else if (rows <= 32)
+    delta_rule_kernel<KD, VD, 2, 1><<<grid, kThreads, 0, s>>>(a);
+  else
+    delta_rule_kernel<KD, VD, 4, 1><<<grid, kThreads, 0, s>>>(a);
 }
 
 }  // namespace
 
 hipError_t launch_delta_rule(const DeltaRuleArgs& a, hipStream_t s) {
   if (a.c.key_dim == 64)
-    launch<64>(a, s);
+    a.c.value_dim == 64 ? launch<64, 64>(a, s) : launch<64, 128>(a, s);
   else
-    launch<128>(a, s);
+    a.c.value_dim == 64 ? launch<128, 64>(a, s) : launch<128, 128>(a, s);
   return hipGetLastError();
 }
 
