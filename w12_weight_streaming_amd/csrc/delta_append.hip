@@ -9,6 +9,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kPer = 8;  // neighbouring channels a thread
+constexpr int kWaves = kThreads / 64;
 constexpr float kHeadEps = 1e-6f;
 
 // 8 inputs of a row, rounded to bf16 as they are staged: the convolution is of
@@ -24,111 +25,173 @@ __device__ __forceinline__ uint4 load_bf16x8(const void* p, int f32, size_t at) 
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// One workgroup per row and 2048 of its channels; a thread takes 8
-// neighbouring ones, so a head is 8 or 16 neighbouring lanes of one wave.
+// Where a row's inputs come from. tap[t]: the row of the step t above it, or
+// (below 0) the window's entry -1 - tap.
+struct Place {
+  int tap[4];
+  int slot, state;  // state 0: a row; 1: of a sequence that is refused; 2: of none
+};
+
+// By one wave. Sequences are looked at 64 at a time.
+__device__ __forceinline__ Place place_of(const DeltaAppendArgs& a, int row) {
+  const int lane = threadIdx.x & 63;
+  Place p;
+  p.state = 2;
+  p.slot = 0;
+  int seq = -1;
+  for (int j0 = 0; j0 < a.st.num_seq && seq < 0; j0 += 64) {
+    const unsigned long long got =
+        __ballot(j0 + lane < a.st.num_seq && rows_meet(a.st.row_off, a.st.total, j0 + lane, row, 1));
+    if (got) seq = j0 + __builtin_ctzll(got);
+  }
+  if (seq < 0) return p;
+  const RowsView v = rows_view(a.c, a.st, seq);
+  bool bad = !v.ok, none = false;
+  for (int j = lane; j < seq; j += 64) none = none || rows_meet(a.st.row_off, a.st.total, j, v.row0, v.rows);
+  if (a.st.parent)
+    for (int i = lane; i < v.rows; i += 64) {
+      const int up = a.st.parent[v.row0 + i];
+      bad = bad || (i == 0 ? up != -1 : (up < 0 || up >= i));
+    }
+  bad = __any(bad);
+  if (__any(none)) return p;
+  p.state = bad ? 1 : 0;
+  p.slot = v.slot;
+  if (bad) return p;
+  int at = row - v.row0;
+  for (int t = 0; t < a.c.width; ++t) {
+    p.tap[t] = at >= 0 ? v.row0 + at : -a.c.width - at;  // -1: the newest entry, width - 2
+    at = at > 0 ? (a.st.parent ? a.st.parent[v.row0 + at] : at - 1) : at - 1;
+  }
+  return p;
+}
+
+// One workgroup per Rows rows and 2048 of their channels; a thread takes 8
+// neighbouring ones, so a head is 8 or 16 neighbouring lanes of one wave, and
+// keeps their weights for all rows. The last column of workgroups makes the gates.
+template <int W, int Rows>
 __global__ __launch_bounds__(kThreads) void delta_append_kernel(DeltaAppendArgs a) {
-  __shared__ int s_seq, s_bad;
-  const int tid = threadIdx.x, row = blockIdx.x;
-  if (tid == 0) {
-    s_seq = a.st.num_seq;
-    s_bad = 0;
-  }
-  __syncthreads();
-  for (int s = tid; s < a.st.num_seq; s += kThreads)
-    if (rows_meet(a.st.row_off, a.st.total, s, row, 1)) atomicMin(&s_seq, s);
-  __syncthreads();
-  const int s = s_seq;
-  if (s >= a.st.num_seq) return;  // a row of no sequence stays as it is
-  const RowsView v = rows_view(a.c, a.st, s);
-  int bad = v.ok ? 0 : 1;
-  const int r = row - v.row0;
-  for (int j = tid; j < s; j += kThreads)
-    if (rows_meet(a.st.row_off, a.st.total, j, v.row0, v.rows)) bad |= 2;
-  if (a.st.parent) {
-    for (int i = tid; i < v.rows; i += kThreads) {
-      const int p = a.st.parent[v.row0 + i];
-      if (i == 0 ? p != -1 : (p < 0 || p >= i)) bad |= 1;
-    }
-  }
-  if (bad) atomicOr(&s_bad, bad);
-  __syncthreads();
-  bad = s_bad;
-  if (bad & 2) return;
+  __shared__ Place s_place[Rows];
+  const int tid = threadIdx.x, row0 = blockIdx.x * Rows;
   const int hk = a.c.key_heads, hv = a.c.value_heads, kd = a.c.key_dim;
+  const bool gates = blockIdx.y + 1 == gridDim.y;
   const int at = (blockIdx.y * kThreads + tid) * kPer;
-  if (blockIdx.y == 0 && tid < hv && !bad) {
-    const size_t b0 = (size_t)row * a.ba_stride + tid;
-    float b, x;
-    if (a.f32) {
-      b = static_cast<const float*>(a.ba)[b0];
-      x = static_cast<const float*>(a.ba)[b0 + hv];
-    } else {
-      b = bf16_to_f32(static_cast<const uint16_t*>(a.ba)[b0]);
-      x = bf16_to_f32(static_cast<const uint16_t*>(a.ba)[b0 + hv]);
-    }
-    x += a.dt_bias[tid];
-    // log(1 + e^x) without overflow; e^-|x| <= 1
-    const float soft = fmaxf(x, 0.0f) + log1pf(expf(-fabsf(x)));
-    a.c.gates[gate_at(a.c, a.layer, row, 0, tid)] = x != x ? x : -expf(a.a_log[tid]) * soft;
-    const float e = expf(-fabsf(b));  // not past fp32's range on either side
-    a.c.gates[gate_at(a.c, a.layer, row, 1, tid)] = b != b ? b : (b < 0 ? e : 1.0f) / (1.0f + e);
-  }
-  const int qk = 2 * hk * kd;
-  const bool on = at < a.c.channels, mine = on && !bad;
-  float y[kPer];
-  uint4 x0 = make_uint4(0, 0, 0, 0);
-  if (mine) {
-    x0 = load_bf16x8(a.qkv, a.f32, (size_t)row * a.qkv_stride + at);
+  const bool on = !gates && at < a.c.channels;
+  float w[kPer * W], bias[kPer];
+  if (on) {
+    const float4* p = reinterpret_cast<const float4*>(a.conv_weight + (size_t)at * W);
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) y[i] = a.conv_bias ? a.conv_bias[at + i] : 0.0f;
-    const int w = a.c.width;
-    int p = r;  // the tap's row in its tree; below 0: the window's entries, the newest at -1
-    for (int t = 0; t < w; ++t) {
-      uint4 x = x0;
-      if (t > 0) {
-        p = p > 0 ? (a.st.parent ? a.st.parent[v.row0 + p] : p - 1) : p - 1;
-        x = p >= 0 ? load_bf16x8(a.qkv, a.f32, (size_t)(v.row0 + p) * a.qkv_stride + at)
-                   : *reinterpret_cast<const uint4*>(a.c.conv + conv_at(a.c, a.layer, v.slot, w - 1 + p) + at);
-      }
-      const uint32_t u[4] = {x.x, x.y, x.z, x.w};
-      const float* cw = a.conv_weight + (size_t)at * w + (w - 1 - t);
-#pragma unroll
-      for (int i = 0; i < kPer; ++i)
-        y[i] += cw[i * w] * ((i & 1) ? __uint_as_float(u[i >> 1] & 0xFFFF0000u) : __uint_as_float(u[i >> 1] << 16));
+    for (int i = 0; i < kPer * W / 4; ++i) {
+      const float4 x = p[i];
+      w[4 * i] = x.x;
+      w[4 * i + 1] = x.y;
+      w[4 * i + 2] = x.z;
+      w[4 * i + 3] = x.w;
     }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) bias[i] = a.conv_bias ? a.conv_bias[at + i] : 0.0f;
   } else {
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) y[i] = 0.0f;
-  }
-  float sum = 0.0f;
+    for (int i = 0; i < kPer * W; ++i) w[i] = 0.0f;
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    y[i] = y[i] / (1.0f + __expf(-y[i]));
-    sum += y[i] * y[i];
+    for (int i = 0; i < kPer; ++i) bias[i] = 0.0f;
   }
-  if (at < qk) {  // whole heads: channels and kd are multiples of 64
-    for (int m = 1; m < kd / kPer; m <<= 1) sum += __shfl_xor(sum, m);
-    const float f = 1.0f / sqrtf(sum + kHeadEps);
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) y[i] *= f;
+  for (int r = tid >> 6; r < Rows; r += kWaves)
+    if (row0 + r < a.st.total) {
+      const Place p = place_of(a, row0 + r);
+      if ((tid & 63) == 0) s_place[r] = p;
+    }
+  __syncthreads();
+  if (gates) {
+    for (int e = tid; e < Rows * hv; e += kThreads) {
+      const int r = e / hv, h = e - r * hv, row = row0 + r;
+      if (row >= a.st.total || s_place[r].state != 0) continue;
+      const size_t b0 = (size_t)row * a.ba_stride + h;
+      float b, x;
+      if (a.f32) {
+        b = static_cast<const float*>(a.ba)[b0];
+        x = static_cast<const float*>(a.ba)[b0 + hv];
+      } else {
+        b = bf16_to_f32(static_cast<const uint16_t*>(a.ba)[b0]);
+        x = bf16_to_f32(static_cast<const uint16_t*>(a.ba)[b0 + hv]);
+      }
+      x += a.dt_bias[h];
+      // log(1 + e^x) without overflow; e^-|x| <= 1
+      const float soft = fmaxf(x, 0.0f) + log1pf(expf(-fabsf(x)));
+      a.c.gates[gate_at(a.c, a.layer, row, 0, h)] = x != x ? x : -expf(a.a_log[h]) * soft;
+      const float e1 = expf(-fabsf(b));  // not past fp32's range on either side
+      a.c.gates[gate_at(a.c, a.layer, row, 1, h)] = b != b ? b : (b < 0 ? e1 : 1.0f) / (1.0f + e1);
+    }
+    return;
   }
-  if (!on) return;
-  uint32_t o[4];
+#pragma unroll 2
+  for (int r = 0; r < Rows; ++r) {
+    const int row = row0 + r;
+    if (row >= a.st.total) return;
+    const Place p = s_place[r];
+    if (p.state == 2) continue;  // a row of no sequence stays as it is
+    const bool mine = on && p.state == 0;
+    uint4 x[W];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) o[i] = f32_to_bf16_rne(y[2 * i]) | ((uint32_t)f32_to_bf16_rne(y[2 * i + 1]) << 16);
-  if (bad) o[0] = o[1] = o[2] = o[3] = 0x7FC07FC0u;  // reported through the queries: NaN
-  const uint4 out = make_uint4(o[0], o[1], o[2], o[3]);
-  if (at < hk * kd) *reinterpret_cast<uint4*>(a.q + (size_t)row * hk * kd + at) = out;
-  if (bad) return;
-  if (at >= hk * kd) *reinterpret_cast<uint4*>(a.c.kv + kv_at(a.c, a.layer, row) + at - hk * kd) = out;
-  *reinterpret_cast<uint4*>(a.c.raw + raw_at(a.c, a.layer, row) + at) = x0;
+    for (int t = 0; t < W; ++t) x[t] = make_uint4(0, 0, 0, 0);
+    if (mine) {
+#pragma unroll
+      for (int t = 0; t < W; ++t)
+        x[t] = p.tap[t] >= 0 ? load_bf16x8(a.qkv, a.f32, (size_t)p.tap[t] * a.qkv_stride + at)
+                             : *reinterpret_cast<const uint4*>(a.c.conv + conv_at(a.c, a.layer, p.slot, -1 - p.tap[t]) + at);
+    }
+    float y[kPer], sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) y[i] = bias[i];
+#pragma unroll
+    for (int t = 0; t < W; ++t) {
+      const uint32_t u[4] = {x[t].x, x[t].y, x[t].z, x[t].w};
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        y[i] += w[i * W + W - 1 - t] * ((i & 1) ? __uint_as_float(u[i >> 1] & 0xFFFF0000u) : __uint_as_float(u[i >> 1] << 16));
+    }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      y[i] = y[i] / (1.0f + __expf(-y[i]));
+      sum += y[i] * y[i];
+    }
+    if (at < 2 * hk * kd) {  // whole heads: channels and kd are multiples of 64
+      for (int m = 1; m < kd / kPer; m <<= 1) sum += __shfl_xor(sum, m);
+      const float f = 1.0f / sqrtf(sum + kHeadEps);
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) y[i] *= f;
+    }
+    if (!on) continue;
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = f32_to_bf16_rne(y[2 * i]) | ((uint32_t)f32_to_bf16_rne(y[2 * i + 1]) << 16);
+    if (!mine) o[0] = o[1] = o[2] = o[3] = 0x7FC07FC0u;  // reported through the queries: NaN
+    const uint4 out = make_uint4(o[0], o[1], o[2], o[3]);
+    if (at < hk * kd) *reinterpret_cast<uint4*>(a.q + (size_t)row * hk * kd + at) = out;
+    if (!mine) continue;
+    if (at >= hk * kd) *reinterpret_cast<uint4*>(a.c.kv + kv_at(a.c, a.layer, row) + at - hk * kd) = out;
+    *reinterpret_cast<uint4*>(a.c.raw + raw_at(a.c, a.layer, row) + at) = x[0];
+  }
+}
+
+template <int W>
+void launch(const DeltaAppendArgs& a, hipStream_t s) {
+  const int parts = (a.c.channels + kThreads * kPer - 1) / (kThreads * kPer) + 1;
+  if (a.st.total <= 64)
+    delta_append_kernel<W, 1><<<dim3(a.st.total, parts), kThreads, 0, s>>>(a);
+  else
+    delta_append_kernel<W, 4><<<dim3((a.st.total + 3) / 4, parts), kThreads, 0, s>>>(a);
 }
 
 }  // namespace
 
 hipError_t launch_delta_append(const DeltaAppendArgs& a, hipStream_t s) {
-  const int parts = (a.c.channels + kThreads * kPer - 1) / (kThreads * kPer);
-  delta_append_kernel<<<dim3(a.st.total, parts), kThreads, 0, s>>>(a);
+  if (a.c.width == 2)
+    launch<2>(a, s);
+  else if (a.c.width == 3)
+    launch<3>(a, s);
+  else
+    launch<4>(a, s);
   return hipGetLastError();
 }
 

@@ -1,0 +1,68 @@
+// Matrix-core helpers of the recurrent layers (gfx950): states and deltas (fp32)
+// times keys and queries (bf16) in three bf16 pieces.
+#pragma once
+
+#include "delta_internal.h"
+#include "w12_device.h"
+
+namespace w12 {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+// Result layout of every product here, lane l of a wave: column l % 16, row
+// 4 (l / 16) + r in value r. An operand's depth is taken in the order (l / 16,
+// r) too, so a result serves as the next product's operand as it stands.
+__device__ __forceinline__ f32x4 mfma_bf16(const uint4& a, const uint4& b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+// 16 deep in fp32.
+__device__ __forceinline__ f32x4 mfma_f32(const f32x4& a, const f32x4& b, f32x4 c) {
+#pragma unroll
+  for (int r = 0; r < 4; ++r) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[r], b[r], c, 0, 0, 0);
+  return c;
+}
+
+// 8 fp32 values as three bf16 operands whose sum they are: each piece is the
+// value's (then the rest's) top 16 bits, and the rests are exact.
+__device__ __forceinline__ void split3(const f32x4& x, const f32x4& y, uint4& hi, uint4& mid, uint4& lo) {
+  uint32_t h[4], m[4], l[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float a = i < 2 ? x[2 * i] : y[2 * i - 4], b = i < 2 ? x[2 * i + 1] : y[2 * i - 3];
+    const uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b);
+    h[i] = __builtin_amdgcn_perm(ub, ua, 0x07060302u);
+    const float ra = a - __uint_as_float(ua & 0xFFFF0000u), rb = b - __uint_as_float(ub & 0xFFFF0000u);
+    const uint32_t va = __float_as_uint(ra), vb = __float_as_uint(rb);
+    m[i] = __builtin_amdgcn_perm(vb, va, 0x07060302u);
+    const float sa = ra - __uint_as_float(va & 0xFFFF0000u), sb = rb - __uint_as_float(vb & 0xFFFF0000u);
+    l[i] = __builtin_amdgcn_perm(__float_as_uint(sb), __float_as_uint(sa), 0x07060302u);
+  }
+  hi = make_uint4(h[0], h[1], h[2], h[3]);
+  mid = make_uint4(m[0], m[1], m[2], m[3]);
+  lo = make_uint4(l[0], l[1], l[2], l[3]);
+}
+
+// 8 bf16 of a row (two 8-byte pieces, 16 values apart): depths 4 (l / 16) + r of two neighbouring tiles of 16.
+__device__ __forceinline__ uint4 fragment(const uint16_t* p) {
+  const uint2 a = *reinterpret_cast<const uint2*>(p), b = *reinterpret_cast<const uint2*>(p + 16);
+  return make_uint4(a.x, a.y, b.x, b.y);
+}
+
+// Two rows' 8 values each, as pairs for an array with rows innermost, `stride` values a column.
+__device__ __forceinline__ void store_turned(uint16_t* to, int stride, const uint4& a, const uint4& b) {
+  const uint32_t u[2][4] = {{a.x, a.y, a.z, a.w}, {b.x, b.y, b.z, b.w}};
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    *reinterpret_cast<uint32_t*>(to + i * stride) =
+        __builtin_amdgcn_perm(u[1][i >> 1], u[0][i >> 1], (i & 1) ? 0x07060302u : 0x05040100u);
+}
+
+// The thread's place, derived anew in each phase of a kernel: kept from one
+// phase to the next, addresses made of it take more registers than the states.
+__device__ __forceinline__ int thread_now() {
+  int t = threadIdx.x;
+  asm volatile("" : "+v"(t));
+  return t;
+}
+
+}  // namespace w12

@@ -24,8 +24,7 @@
 // enters a bf16 product as three bf16 pieces, each the top of what the one
 // before left, which hold all its 24 bits; products of two fp32 factors (L and
 // D (q . k) with deltas) run on the fp32 matrix core. Sums of g are held in 64 bits.
-#include "delta_internal.h"
-#include "w12_device.h"
+#include "delta_mfma.h"
 
 namespace w12 {
 namespace {
@@ -33,56 +32,10 @@ namespace {
 constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
 
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-
-__device__ __forceinline__ f32x4 mfma_bf16(const uint4& a, const uint4& b, f32x4 c) {
-  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
-}
-// 16 deep in fp32: both operands hold depth 4 (l / 16) + r in value r.
-__device__ __forceinline__ f32x4 mfma_f32(const f32x4& a, const f32x4& b, f32x4 c) {
-#pragma unroll
-  for (int r = 0; r < 4; ++r) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[r], b[r], c, 0, 0, 0);
-  return c;
-}
-
-// 8 fp32 values as three bf16 operands whose sum they are: each piece is the
-// value's (then the rest's) top 16 bits, and the rests are exact.
-__device__ __forceinline__ void split3(const f32x4& x, const f32x4& y, uint4& hi, uint4& mid, uint4& lo) {
-  uint32_t h[4], m[4], l[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float a = i < 2 ? x[2 * i] : y[2 * i - 4], b = i < 2 ? x[2 * i + 1] : y[2 * i - 3];
-    const uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b);
-    h[i] = __builtin_amdgcn_perm(ub, ua, 0x07060302u);
-    const float ra = a - __uint_as_float(ua & 0xFFFF0000u), rb = b - __uint_as_float(ub & 0xFFFF0000u);
-    const uint32_t va = __float_as_uint(ra), vb = __float_as_uint(rb);
-    m[i] = __builtin_amdgcn_perm(vb, va, 0x07060302u);
-    const float sa = ra - __uint_as_float(va & 0xFFFF0000u), sb = rb - __uint_as_float(vb & 0xFFFF0000u);
-    l[i] = __builtin_amdgcn_perm(__float_as_uint(sb), __float_as_uint(sa), 0x07060302u);
-  }
-  hi = make_uint4(h[0], h[1], h[2], h[3]);
-  mid = make_uint4(m[0], m[1], m[2], m[3]);
-  lo = make_uint4(l[0], l[1], l[2], l[3]);
-}
-
 // An infinity or NaN among 8 bf16 values.
 __device__ __forceinline__ bool odd16(uint32_t w) { return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u; }
 __device__ __forceinline__ bool odd8(const uint4& x) { return odd16(x.x) || odd16(x.y) || odd16(x.z) || odd16(x.w); }
 __device__ __forceinline__ bool odd32(float x) { return !(fabsf(x) <= 3.4e38f); }
-
-// 8 bf16 of a row (two 8-byte pieces, 16 values apart): depth 4 g + r of two neighbouring tiles of 16.
-__device__ __forceinline__ uint4 fragment(const uint16_t* p) {
-  const uint2 a = *reinterpret_cast<const uint2*>(p), b = *reinterpret_cast<const uint2*>(p + 16);
-  return make_uint4(a.x, a.y, b.x, b.y);
-}
-
-// The thread's place, derived anew in each phase of the kernel: kept from one
-// phase to the next, addresses made of it take more registers than the states.
-__device__ __forceinline__ int thread_now() {
-  int t = threadIdx.x;
-  asm volatile("" : "+v"(t));
-  return t;
-}
 
 template <int KD, int RT>
 struct Shared {
@@ -131,13 +84,7 @@ __device__ __forceinline__ void load_rows(const DeltaRuleArgs& a, Shared<KD, RT>
       }
       *reinterpret_cast<uint4*>(kdst + (r + i) * Sh::KS + c) = x[i];
     }
-    if constexpr (KT) {
-      const uint32_t u[2][4] = {{x[0].x, x[0].y, x[0].z, x[0].w}, {x[1].x, x[1].y, x[1].z, x[1].w}};
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        *reinterpret_cast<uint32_t*>(s.t + (c + i) * Sh::TS + r) =
-            __builtin_amdgcn_perm(u[1][i >> 1], u[0][i >> 1], (i & 1) ? 0x07060302u : 0x05040100u);
-    }
+    if constexpr (KT) store_turned(s.t + c * Sh::TS + r, Sh::TS, x[0], x[1]);
   }
 }
 template <int KD, int RT>
