@@ -21,47 +21,62 @@ __device__ __forceinline__ uint4 load_bf16x8(const void* p, int f32, size_t at) 
   const float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
   uint32_t w[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) w[i] = f32_to_bf16_rne(x[2 * i]) | ((uint32_t)f32_to_bf16_rne(x[2 * i + 1]) << 16);
+  for (int i = 0; i < 4; ++i) w[i] = bf16_pair(x[2 * i], x[2 * i + 1]);
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // Where a row's inputs come from. tap[t]: the row of the step t above it, or
 // (below 0) the window's entry -1 - tap.
+template <int W>
 struct Place {
-  int tap[4];
+  int tap[W];
   int slot, state;  // state 0: a row; 1: of a sequence that is refused; 2: of none
 };
 
-// By one wave. Sequences are looked at 64 at a time.
-__device__ __forceinline__ Place place_of(const DeltaAppendArgs& a, int row) {
+// By one wave, in as few dependent loads as there are: sequences 64 at a time,
+// then the sequence's parents.
+template <int W>
+__device__ __forceinline__ Place<W> place_of(const DeltaAppendArgs& a, int row) {
   const int lane = threadIdx.x & 63;
-  Place p;
+  Place<W> p;
   p.state = 2;
   p.slot = 0;
-  int seq = -1;
+#pragma unroll
+  for (int t = 0; t < W; ++t) p.tap[t] = 0;
+  int seq = -1, row0 = 0, rows = 0, slot = 0;
+  bool none = false;
   for (int j0 = 0; j0 < a.st.num_seq && seq < 0; j0 += 64) {
-    const unsigned long long got =
-        __ballot(j0 + lane < a.st.num_seq && rows_meet(a.st.row_off, a.st.total, j0 + lane, row, 1));
-    if (got) seq = j0 + __builtin_ctzll(got);
+    const int j = min(j0 + lane, a.st.num_seq - 1);
+    const int b0 = a.st.row_off[j], b1 = a.st.row_off[j + 1], sl = a.st.slot ? a.st.slot[j] : j;
+    const bool in = j0 + lane < a.st.num_seq && b0 >= 0 && b1 <= a.st.total;
+    const unsigned long long got = __ballot(in && b0 <= row && row < b1);
+    if (!got) continue;
+    const int at = __builtin_ctzll(got);
+    seq = j0 + at;
+    row0 = __shfl(b0, at);
+    rows = __shfl(b1, at) - row0;
+    slot = __shfl(sl, at);
+    none = __any(in && lane < at && b0 < b1 && b0 < row0 + rows && b1 > row0);
+    for (int i = lane; i < j0; i += 64) none = none || rows_meet(a.st.row_off, a.st.total, i, row0, rows);
   }
-  if (seq < 0) return p;
-  const RowsView v = rows_view(a.c, a.st, seq);
-  bool bad = !v.ok, none = false;
-  for (int j = lane; j < seq; j += 64) none = none || rows_meet(a.st.row_off, a.st.total, j, v.row0, v.rows);
+  if (seq < 0 || __any(none)) return p;
+  bool bad = slot < 0 || slot >= a.c.slots;
+  int mine = lane - 1;  // the parent of the sequence's row `lane`
   if (a.st.parent)
-    for (int i = lane; i < v.rows; i += 64) {
-      const int up = a.st.parent[v.row0 + i];
+    for (int i = lane; i < rows; i += 64) {
+      const int up = a.st.parent[row0 + i];
       bad = bad || (i == 0 ? up != -1 : (up < 0 || up >= i));
+      if (i == lane) mine = up;
     }
-  bad = __any(bad);
-  if (__any(none)) return p;
-  p.state = bad ? 1 : 0;
-  p.slot = v.slot;
-  if (bad) return p;
-  int at = row - v.row0;
-  for (int t = 0; t < a.c.width; ++t) {
-    p.tap[t] = at >= 0 ? v.row0 + at : -a.c.width - at;  // -1: the newest entry, width - 2
-    at = at > 0 ? (a.st.parent ? a.st.parent[v.row0 + at] : at - 1) : at - 1;
+  p.state = __any(bad) ? 1 : 0;
+  if (p.state) return p;
+  p.slot = slot;
+  int at = row - row0;
+#pragma unroll
+  for (int t = 0; t < W; ++t) {
+    p.tap[t] = at >= 0 ? row0 + at : -W - at;  // -1: the newest entry, W - 2
+    const int near = __shfl(mine, at & 63);
+    at = at <= 0 || !a.st.parent ? at - 1 : at < 64 ? near : a.st.parent[row0 + at];
   }
   return p;
 }
@@ -71,13 +86,17 @@ __device__ __forceinline__ Place place_of(const DeltaAppendArgs& a, int row) {
 // keeps their weights for all rows. The last column of workgroups makes the gates.
 template <int W, int Rows>
 __global__ __launch_bounds__(kThreads) void delta_append_kernel(DeltaAppendArgs a) {
-  __shared__ Place s_place[Rows];
+  __shared__ Place<W> s_place[Rows];
   const int tid = threadIdx.x, row0 = blockIdx.x * Rows;
   const int hk = a.c.key_heads, hv = a.c.value_heads, kd = a.c.key_dim;
   const bool gates = blockIdx.y + 1 == gridDim.y;
   const int at = (blockIdx.y * kThreads + tid) * kPer;
   const bool on = !gates && at < a.c.channels;
   float w[kPer * W], bias[kPer];
+  uint4 own[Rows];  // the rows' own inputs: known before their places are
+#pragma unroll
+  for (int r = 0; r < Rows; ++r)
+    own[r] = on ? load_bf16x8(a.qkv, a.f32, (size_t)min(row0 + r, a.st.total - 1) * a.qkv_stride + at) : make_uint4(0, 0, 0, 0);
   if (on) {
     const float4* p = reinterpret_cast<const float4*>(a.conv_weight + (size_t)at * W);
 #pragma unroll
@@ -98,7 +117,7 @@ __global__ __launch_bounds__(kThreads) void delta_append_kernel(DeltaAppendArgs 
   }
   for (int r = tid >> 6; r < Rows; r += kWaves)
     if (row0 + r < a.st.total) {
-      const Place p = place_of(a, row0 + r);
+      const Place<W> p = place_of<W>(a, row0 + r);
       if ((tid & 63) == 0) s_place[r] = p;
     }
   __syncthreads();
@@ -124,22 +143,29 @@ __global__ __launch_bounds__(kThreads) void delta_append_kernel(DeltaAppendArgs 
     }
     return;
   }
-#pragma unroll 2
+  uint4 x[W];
+#pragma unroll
+  for (int t = 0; t < W; ++t) x[t] = make_uint4(0, 0, 0, 0);
+#pragma unroll
   for (int r = 0; r < Rows; ++r) {
     const int row = row0 + r;
     if (row >= a.st.total) return;
-    const Place p = s_place[r];
+    const Place<W> p = s_place[r];
     if (p.state == 2) continue;  // a row of no sequence stays as it is
     const bool mine = on && p.state == 0;
-    uint4 x[W];
+    bool follows = r > 0 && s_place[max(r - 1, 0)].state == 0 && p.slot == s_place[max(r - 1, 0)].slot;
 #pragma unroll
-    for (int t = 0; t < W; ++t) x[t] = make_uint4(0, 0, 0, 0);
-    if (mine) {
+    for (int t = 1; t < W; ++t) follows = follows && p.tap[t] == s_place[max(r - 1, 0)].tap[t - 1];
+    if (follows) {  // the row before is its parent, and has its other inputs
 #pragma unroll
-      for (int t = 0; t < W; ++t)
+      for (int t = W - 1; t > 0; --t) x[t] = x[t - 1];
+    } else if (mine) {
+#pragma unroll
+      for (int t = 1; t < W; ++t)
         x[t] = p.tap[t] >= 0 ? load_bf16x8(a.qkv, a.f32, (size_t)p.tap[t] * a.qkv_stride + at)
                              : *reinterpret_cast<const uint4*>(a.c.conv + conv_at(a.c, a.layer, p.slot, -1 - p.tap[t]) + at);
     }
+    x[0] = own[r];
     float y[kPer], sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) y[i] = bias[i];
@@ -152,7 +178,7 @@ __global__ __launch_bounds__(kThreads) void delta_append_kernel(DeltaAppendArgs 
     }
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      y[i] = y[i] / (1.0f + __expf(-y[i]));
+      y[i] = silu(y[i]);
       sum += y[i] * y[i];
     }
     if (at < 2 * hk * kd) {  // whole heads: channels and kd are multiples of 64
@@ -164,7 +190,7 @@ __global__ __launch_bounds__(kThreads) void delta_append_kernel(DeltaAppendArgs 
     if (!on) continue;
     uint32_t o[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] = f32_to_bf16_rne(y[2 * i]) | ((uint32_t)f32_to_bf16_rne(y[2 * i + 1]) << 16);
+    for (int i = 0; i < 4; ++i) o[i] = bf16_pair(y[2 * i], y[2 * i + 1]);
     if (!mine) o[0] = o[1] = o[2] = o[3] = 0x7FC07FC0u;  // reported through the queries: NaN
     const uint4 out = make_uint4(o[0], o[1], o[2], o[3]);
     if (at < hk * kd) *reinterpret_cast<uint4*>(a.q + (size_t)row * hk * kd + at) = out;

@@ -83,6 +83,15 @@ hipError_t launch_norm(const NormArgs& a, hipStream_t s);
 #ifdef __HIPCC__
 __device__ __forceinline__ float bf16_to_f32(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
 
+// Two values as bf16, rounded to nearest even (one instruction).
+__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
+  typedef __bf16 bf16_2 __attribute__((ext_vector_type(2)));
+  const bf16_2 p = {(__bf16)a, (__bf16)b};
+  return __builtin_bit_cast(uint32_t, p);
+}
+// z / (1 + e^-z): the reciprocal is off by one step, and 0 where e^-z overflows.
+__device__ __forceinline__ float silu(float z) { return z * __builtin_amdgcn_rcpf(1.0f + __expf(-z)); }
+
 __device__ __forceinline__ size_t state_at(const DeltaArgs& c, int layer, int slot, int head) {
   return (((size_t)layer * c.slots + slot) * c.value_heads + head) * ((size_t)c.key_dim * c.value_dim);
 }

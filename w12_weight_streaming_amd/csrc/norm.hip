@@ -62,19 +62,19 @@ __device__ __forceinline__ void store8(void* p, int f32, size_t at, int n, float
     return;
   }
   uint16_t* h = static_cast<uint16_t*>(p) + at;
-  uint16_t b[8];
+  uint32_t b[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    b[i] = f32_to_bf16_rne(x[i]);
-    x[i] = bf16_to_f32(b[i]);
+  for (int i = 0; i < 4; ++i) {
+    b[i] = bf16_pair(x[2 * i], x[2 * i + 1]);
+    x[2 * i] = __uint_as_float(b[i] << 16);
+    x[2 * i + 1] = __uint_as_float(b[i] & 0xFFFF0000u);
   }
   if constexpr (Vec) {
-    *reinterpret_cast<uint4*>(h) = make_uint4(b[0] | ((uint32_t)b[1] << 16), b[2] | ((uint32_t)b[3] << 16),
-                                              b[4] | ((uint32_t)b[5] << 16), b[6] | ((uint32_t)b[7] << 16));
+    *reinterpret_cast<uint4*>(h) = make_uint4(b[0], b[1], b[2], b[3]);
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (i < n) h[i] = b[i];
+      if (i < n) h[i] = (uint16_t)(b[i >> 1] >> (i & 1) * 16);
   }
 }
 
@@ -128,7 +128,7 @@ __device__ __forceinline__ void norm_group(const NormArgs& a, int64_t row, int g
     if (n[k] <= 0) continue;
     if (a.gate)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) t[k][i] *= z[k][i] / (1.0f + __expf(-z[k][i]));
+      for (int i = 0; i < 8; ++i) t[k][i] *= silu(z[k][i]);
     if (a.h) {
       if (a.y) {
 #pragma unroll
