@@ -77,6 +77,7 @@ struct NormArgs {
 
 hipError_t launch_delta_append(const DeltaAppendArgs& a, hipStream_t s);
 hipError_t launch_delta_rule(const DeltaRuleArgs& a, hipStream_t s);
+hipError_t launch_delta_chain(const DeltaRuleArgs& a, hipStream_t s);  // parent null
 hipError_t launch_delta_commit(const DeltaCommitArgs& a, hipStream_t s);
 hipError_t launch_norm(const NormArgs& a, hipStream_t s);
 

@@ -7,6 +7,14 @@
 
 namespace w12 {
 
+// The thread's place, derived anew in each phase of a kernel: kept from one
+// phase to the next, addresses made of it take more registers than the states.
+__device__ __forceinline__ int thread_now() {
+  int t = threadIdx.x;
+  asm volatile("" : "+v"(t));
+  return t;
+}
+
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 // Result layout of every product here, lane l of a wave: column l % 16, row
@@ -57,12 +65,51 @@ __device__ __forceinline__ void store_turned(uint16_t* to, int stride, const uin
         __builtin_amdgcn_perm(u[1][i >> 1], u[0][i >> 1], (i & 1) ? 0x07060302u : 0x05040100u);
 }
 
-// The thread's place, derived anew in each phase of a kernel: kept from one
-// phase to the next, addresses made of it take more registers than the states.
-__device__ __forceinline__ int thread_now() {
-  int t = threadIdx.x;
-  asm volatile("" : "+v"(t));
-  return t;
+// An infinity or NaN among bf16 values, or as an fp32 value.
+__device__ __forceinline__ bool odd16(uint32_t w) { return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u; }
+__device__ __forceinline__ bool odd8(const uint4& x) { return odd16(x.x) || odd16(x.y) || odd16(x.z) || odd16(x.w); }
+__device__ __forceinline__ bool odd32(float x) { return !(fabsf(x) <= 3.4e38f); }
+
+// One tile of x . k, transposed, over KD dims: lane (l / 16, l % 16) holds row l % 16 of x, rows 4 (l / 16) + r
+// of k, so that it serves as a product's first operand. x, k: the tile's first rows, `stride` values apart.
+template <int KD>
+__device__ __forceinline__ f32x4 pair_tile(const uint16_t* x, const uint16_t* k, int stride, int lane) {
+  const int at = (lane & 15) * stride + 4 * (lane >> 4);
+  f32x4 acc = {0, 0, 0, 0};
+#pragma unroll
+  for (int t = 0; t < KD / 32; ++t) acc = mfma_bf16(fragment(k + at + 32 * t), fragment(x + at + 32 * t), acc);
+  return acc;
+}
+
+// (I + L)^-1 of a diagonal tile from -L, a column per lane of the first 16, by
+// forward substitution: L's products of keys make it as well conditioned as the
+// rule itself, where powers of L would cancel. Few: the wave has few registers
+// to spare (all rows of L at once take 160), and rows past n hold nothing.
+template <bool Few>
+__device__ __forceinline__ void invert(const f32x4* low, f32x4* inv, int n) {
+  const int lane = thread_now() & 63, c = lane & 15;
+  float x[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    float y = i == c ? 1.0f : 0.0f;
+    if (!Few || i < n) {  // the same for all lanes
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        if (4 * g < i) {
+          const f32x4 l = low[g * 16 + i];
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (4 * g + r < i) y += l[r] * x[4 * g + r];
+        }
+      }
+    }
+    x[i] = y;
+  }
+  if (lane < 16) {
+    float* o = reinterpret_cast<float*>(inv);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[((c >> 2) * 16 + i) * 4 + (c & 3)] = x[i];
+  }
 }
 
 }  // namespace w12

@@ -1,0 +1,167 @@
+// What the delta rule's kernels share (gfx950): the state in registers, the
+// look at a sequence, a sequence of one row.
+#pragma once
+
+#include "delta_mfma.h"
+
+namespace w12 {
+
+// The wave's NC * 16 columns of a head's state from value dim vw, NC neighbouring ones a lane, in
+// the layout of the products: a uniform part of each address, and the lane's in 32 bits.
+template <int VD, int NC>
+__device__ __forceinline__ uint32_t state_place(int vw) {
+  const int lane = thread_now() & 63;
+  return (uint32_t)(4 * (lane >> 4) * VD + vw + (lane & 15) * NC);
+}
+template <int KT, int VD, int NC>
+__device__ __forceinline__ void load_state(const float* state, int vw, f32x4 (&S)[KT][NC]) {
+  const uint32_t at = state_place<VD, NC>(vw);
+#pragma unroll
+  for (int t = 0; t < KT; ++t)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const float* p = state + (16 * t + r) * VD + at;
+      if constexpr (NC == 2) {
+        const float2 x = *reinterpret_cast<const float2*>(p);
+        S[t][0][r] = x.x;
+        S[t][1][r] = x.y;
+      } else {
+        S[t][0][r] = *p;
+      }
+    }
+}
+template <int KT, int VD, int NC>
+__device__ __forceinline__ void store_state(float* state, int vw, const f32x4 (&S)[KT][NC]) {
+  const uint32_t at = state_place<VD, NC>(vw);
+#pragma unroll
+  for (int t = 0; t < KT; ++t)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      float* p = state + (16 * t + r) * VD + at;
+      if constexpr (NC == 2)
+        *reinterpret_cast<float2*>(p) = make_float2(S[t][0][r], S[t][1][r]);
+      else
+        *p = S[t][0][r];
+    }
+}
+
+// A kept sequence's window, shared out among the workgroups of its heads.
+__device__ __forceinline__ void keep_window(const DeltaRuleArgs& a, const RowsView& v) {
+  const int share = (a.c.channels + gridDim.x - 1) / gridDim.x;
+  advance_window(a.c, a.layer, v.slot, v.rows, blockIdx.x * share, min(a.c.channels, (int)(blockIdx.x + 1) * share),
+                 [&](int j) { return v.row0 + j; });
+}
+
+// By one wave: 1 if the sequence is refused, 2 if it has no rows.
+__device__ __forceinline__ int refused(const DeltaRuleArgs& a, const RowsView& v, int seq, bool chain) {
+  const int lane = thread_now() & 63;
+  bool bad = !v.ok, none = false;
+  for (int j = lane; j < seq; j += 64) {
+    none = none || rows_meet(a.st.row_off, a.st.total, j, v.row0, v.rows);
+    bad = bad || (a.keep && a.st.slot && a.st.slot[j] == v.slot);
+  }
+  if (!chain)
+    for (int i = lane; i < v.rows; i += 64) {
+      const int p = a.st.parent[v.row0 + i];
+      bad = bad || (i == 0 ? p != -1 : (p < 0 || p >= i));
+    }
+  return __any(none) ? 2 : __any(bad) ? 1 : 0;
+}
+
+// A refused sequence's outputs, `wide` value dims of a head from v0.
+__device__ __forceinline__ void no_numbers(const DeltaRuleArgs& a, const RowsView& v, int head, int vd, int v0, int wide) {
+  for (int e = thread_now(); e < v.rows * wide; e += blockDim.x)
+    a.out[((size_t)(v.row0 + e / wide) * a.c.value_heads + head) * vd + v0 + e % wide] = 0x7FC0;
+}
+
+// A sequence's rows one after another (plain decoding: one), each wave by itself
+// and without LDS: the products with its columns in fp32, summed over the four
+// lanes of a column. Rows follow each other (a tree has one row here).
+template <int KD, int VD, int NC>
+__device__ __forceinline__ void rows_in_turn(const DeltaRuleArgs& a, const RowsView& v, int seq, int head, int key, int vw,
+                                             float* state, f32x4 (&S)[KD / 16][NC]) {
+  constexpr int KT = KD / 16;
+  const int lane = thread_now() & 63, g = lane >> 4, v0 = vw + (lane & 15) * NC;
+  const int bad = refused(a, v, seq, !a.st.parent);
+  for (int i = 0; i < v.rows; ++i) {
+    const int row = v.row0 + i;
+    const uint16_t* kp = a.c.kv + kv_at(a.c, a.layer, row) + (key * KD + 4 * g);
+    const uint16_t* qp = a.q + ((size_t)row * a.c.key_heads + key) * KD + 4 * g;
+    uint2 k[KT], q[KT];
+#pragma unroll
+    for (int t = 0; t < KT; ++t) {
+      k[t] = *reinterpret_cast<const uint2*>(kp + 16 * t);
+      q[t] = *reinterpret_cast<const uint2*>(qp + 16 * t);
+    }
+    const uint16_t* vp = a.c.kv + kv_at(a.c, a.layer, row) + (a.c.key_heads * KD + head * VD) + v0;
+    const uint32_t val = NC == 2 ? *reinterpret_cast<const uint32_t*>(vp) : *vp;
+    const float gate = a.c.gates[gate_at(a.c, a.layer, row, 0, head)], beta = a.c.gates[gate_at(a.c, a.layer, row, 1, head)];
+    uint16_t* out = a.out + ((size_t)row * a.c.value_heads + head) * VD + v0;
+    if (bad) {
+      if (bad == 1 && g == 0)
+#pragma unroll
+        for (int c = 0; c < NC; ++c) out[c] = 0x7FC0;
+      continue;
+    }
+    const auto at = [](const uint2& x, int r) {
+      const uint32_t w = r < 2 ? x.x : x.y;
+      return r & 1 ? __uint_as_float(w & 0xFFFF0000u) : __uint_as_float(w << 16);
+    };
+    float x[NC], o[NC], kq = 0;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) x[c] = o[c] = 0;
+#pragma unroll
+    for (int t = 0; t < KT; ++t)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const float kk = at(k[t], r), qq = at(q[t], r);
+        kq += kk * qq;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+          x[c] += S[t][c][r] * kk;
+          o[c] += S[t][c][r] * qq;
+        }
+      }
+#pragma unroll
+    for (int m = 16; m < 64; m <<= 1) {
+      kq += __shfl_xor(kq, m);
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        x[c] += __shfl_xor(x[c], m);
+        o[c] += __shfl_xor(o[c], m);
+      }
+    }
+    const float f = expf(gate);
+    float d[NC];
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      d[c] = beta * (__uint_as_float(c ? val & 0xFFFF0000u : val << 16) - f * x[c]);
+      o[c] = a.scale * (f * o[c] + kq * d[c]);
+    }
+    if (g == 0) {
+      const uint32_t w = bf16_pair(o[0], o[NC - 1]);
+      if constexpr (NC == 2)
+        *reinterpret_cast<uint32_t*>(out) = w;
+      else
+        *out = (uint16_t)w;
+      if (!a.keep) {
+        float* p = a.c.delta + delta_at(a.c, a.layer, row, head) + v0;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) p[c] = d[c];
+      }
+    }
+    if (a.keep || i + 1 < v.rows) {
+#pragma unroll
+      for (int t = 0; t < KT; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+          for (int c = 0; c < NC; ++c) S[t][c][r] = f * S[t][c][r] + at(k[t], r) * d[c];
+    }
+  }
+  if (!a.keep || bad) return;
+  store_state<KT, VD, NC>(state, vw, S);
+  keep_window(a, v);
+}
+
+}  // namespace w12
