@@ -19,7 +19,7 @@ constexpr int R = 32;
 
 template <int KD>
 struct Block {
-  static constexpr int KS = KD + 16, TS = R + 16;  // 8 rows of 8-byte reads meet no bank twice
+  static constexpr int KS = KD + 8, TS = R + 8;  // rows 4 banks (of 64) further each: 8-byte reads meet none twice
   alignas(16) uint16_t q[R * KS];
   alignas(16) uint16_t k[R * KS];
   alignas(16) uint16_t t[KD * TS];  // k with rows innermost
@@ -44,23 +44,19 @@ struct Rows {
 
 template <int KD>
 __device__ __forceinline__ void fetch(const DeltaRuleArgs& a, const RowsView& v, int b, int head, int key, int tid, Rows& x) {
-  const int n = min(R, v.rows - b * R), row0 = v.row0 + b * R;
-  const int c = (tid / (R / 2)) * 8, r = (tid % (R / 2)) * 2;
-  const uint16_t* kp = a.c.kv + kv_at(a.c, a.layer, row0) + key * KD;
-  const uint16_t* qp = a.q + ((size_t)row0 * a.c.key_heads + key) * KD;
-  if (c < KD) {
+  const int last = v.rows - 1, first = b * R;  // rows past the end stand for the last one: no branch, which would wait for the loads
+  const int c = min(tid / (R / 2), KD / 8 - 1) * 8, r = (tid % (R / 2)) * 2;
+  const uint16_t* kp = a.c.kv + kv_at(a.c, a.layer, v.row0) + (key * KD + c);
+  const uint16_t* qp = a.q + ((size_t)v.row0 * a.c.key_heads + key) * KD + c;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint32_t at = min(r + i, n - 1);
-      x.k[i] = *reinterpret_cast<const uint4*>(kp + at * a.c.kv_width + c);
-      x.q[i] = *reinterpret_cast<const uint4*>(qp + at * (a.c.key_heads * KD) + c);
-    }
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t at = min(first + r + i, last);
+    x.k[i] = *reinterpret_cast<const uint4*>(kp + at * a.c.kv_width);
+    x.q[i] = *reinterpret_cast<const uint4*>(qp + at * (a.c.key_heads * KD));
   }
-  x.gate = x.beta = 0.0f;
-  if (tid < n) {
-    x.gate = a.c.gates[gate_at(a.c, a.layer, row0 + tid, 0, head)];
-    x.beta = a.c.gates[gate_at(a.c, a.layer, row0 + tid, 1, head)];
-  }
+  const float* gp = a.c.gates + gate_at(a.c, a.layer, v.row0, 0, head) + (uint32_t)min(first + (tid & (R - 1)), last) * (2 * a.c.value_heads);
+  x.gate = gp[0];
+  x.beta = gp[a.c.value_heads];
 }
 
 template <int KD>
@@ -83,11 +79,10 @@ __device__ __forceinline__ void stage(Shared<KD>& s, const RowsView& v, int b, i
     store_turned(o.t + c * B::TS + r, B::TS, x.k[0], x.k[1]);
   }
   if (tid < 64) {  // one wave; rows past n decay by nothing
-    if (!(x.gate <= 3.4e38f) || odd32(x.beta)) {
-      atomicOr(&s.odd[b], 1u << tid);
-      x.gate = x.beta = 0.0f;
-    }
-    double sum = log_decay(x.gate);
+    const bool no = !(x.gate <= 3.4e38f) || odd32(x.beta);
+    if (no && tid < n) atomicOr(&s.odd[b], 1u << tid);
+    const float gate = no || tid >= n ? 0.0f : x.gate, beta = no || tid >= n ? 0.0f : x.beta;
+    double sum = log_decay(gate);
 #pragma unroll
     for (int step = 1; step < R; step <<= 1) {
       const double up = __shfl_up(sum, step);
@@ -96,7 +91,7 @@ __device__ __forceinline__ void stage(Shared<KD>& s, const RowsView& v, int b, i
     const double end = __shfl(sum, R - 1);
     if (tid < R) {
       o.sum[tid] = sum;
-      o.beta[tid] = x.beta;
+      o.beta[tid] = beta;
       o.grow[tid] = expf((float)sum);
       o.part[tid] = expf((float)(end - sum));
     }
@@ -134,150 +129,174 @@ __global__ __launch_bounds__(kThreads, 2) void delta_chain_kernel(DeltaRuleArgs 
   const int blocks = (v.rows + R - 1) / R;
   float* state = a.c.state + state_at(a.c, a.layer, v.slot, head);
   const uint16_t* values = a.c.kv + kv_at(a.c, a.layer, v.row0) + (a.c.key_heads * KD + head * VD);
-  Rows x;
-  f32x4 S[KT][1];
-  uint16_t val[2][4];  // this block's values
-  const auto fetch_values = [&](int b) {
-    const int lane = thread_now() & 63;
-#pragma unroll
-    for (int m = 0; m < 2; ++m)
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-        val[m][r] = values[(uint32_t)min(b * R + 16 * m + 4 * (lane >> 4) + r, v.rows - 1) * a.c.kv_width + vw + (lane & 15)];
-  };
-  if (maker) {
-    fetch<KD>(a, v, 0, head, key, thread_now() - 64 * kWaves, x);
-  } else {
-    load_state<KT, VD, 1>(state, vw, S);
-    fetch_values(0);
-    if (wave == 0) {
-      const int bad = refused(a, v, seq, true);
-      if ((thread_now() & 63) == 0) s.bad = bad;
-    }
-  }
   if (tid < kStepRows / R) s.odd[tid] = s.odd_q[tid] = 0;
-  __syncthreads();
-  if (s.bad) {
-    if (!(s.bad & 2)) no_numbers(a, v, head, VD, v_slab, 16 * kWaves);
-    return;
+  if (wave == 0) {
+    const int bad = refused(a, v, seq, true);
+    if ((thread_now() & 63) == 0) s.bad = bad;
   }
-  f32x4 rhs[2], acc[2];
-  bool before = false;  // an earlier block holds a row that is no number
-  for (int b = -1; b < blocks; ++b) {
-    B& o = s.block[b & 1];
-    if (maker) {
-      if (b + 1 < blocks) {
-        const int me = thread_now() - 64 * kWaves;
-        stage<KD>(s, v, b + 1, me, x);
-        if (b + 2 < blocks) fetch<KD>(a, v, b + 2, head, key, me, x);
-      }
-    } else if (b >= 0) {  // products with the old state
-      const int lane = thread_now() & 63, col = lane & 15, g = lane >> 4;
-      const int n = min(R, v.rows - b * R);
-      f32x4 w[2];
-#pragma unroll
-      for (int m = 0; m < 2; ++m) w[m] = acc[m] = f32x4{0, 0, 0, 0};
-#pragma unroll
-      for (int t = 0; t < KT; t += 2) {
-        uint4 piece[3];
-        split3(S[t][0], S[t + 1][0], piece[0], piece[1], piece[2]);
-#pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          const uint4 fk = fragment(o.k + (16 * m + col) * B::KS + 16 * t + 4 * g);
-          const uint4 fq = fragment(o.q + (16 * m + col) * B::KS + 16 * t + 4 * g);
-#pragma unroll
-          for (int p = 2; p >= 0; --p) {
-            w[m] = mfma_bf16(fk, piece[p], w[m]);
-            acc[m] = mfma_bf16(fq, piece[p], acc[m]);
-          }
-        }
-      }
-      uint32_t odd = 0;
-#pragma unroll
-      for (int m = 0; m < 2; ++m)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int i = 16 * m + 4 * g + r;
-          uint32_t y = val[m][r];
-          if (odd16(y) && i < n) odd |= 1u << i;
-          if (odd16(y) || i >= n) y = 0;
-          const float grow = o.grow[i];
-          rhs[m][r] = o.beta[i] * (__uint_as_float(y << 16) - grow * w[m][r]);
-          acc[m][r] *= grow;
-        }
-      if (odd) atomicOr(&s.odd[b], odd);
-      if (b + 1 < blocks) fetch_values(b + 1);
-    }
+  bool before = false;  // a block holds a row that is no number
+  // Each turn of either loop has two barriers: the makers' block b + 1 is staged,
+  // then made; the others' block b meets the old state, then makes the new one.
+  if (maker) {
+    Rows x;
+    fetch<KD>(a, v, 0, head, key, thread_now() - 64 * kWaves, x);
     __syncthreads();
-    if (maker) {
-      if (b + 1 < blocks) {
-        B& p = s.block[(b + 1) & 1];
+    if (s.bad) {
+      if (!(s.bad & 2)) no_numbers(a, v, head, VD, v_slab, 16 * kWaves);
+      return;
+    }
+    for (int b = 0; b <= blocks; ++b) {
+      if (b < blocks) {
+        const int me = thread_now() - 64 * kWaves;
+        stage<KD>(s, v, b, me, x);
+        fetch<KD>(a, v, min(b + 1, blocks - 1), head, key, me, x);
+      }
+      __syncthreads();
+      if (b < blocks) {
+        B& o = s.block[b & 1];
         const int u = wave - kWaves;
         if (u < 2) {
-          tile<KD>(p, true, u);
+          tile<KD>(o, true, u);
           wave_lds_sync();
-          invert<false>(p.low[u], p.inv[u], R);
+          invert(o.low[u], o.inv[u], min(R, v.rows - b * R) - 16 * u);
         } else {
-          tile<KD>(p, u == 2, 2);
-          tile<KD>(p, false, u - 2);
-          if (u == 3) tile<KD>(p, false, 2);
+          tile<KD>(o, u == 2, 2);
+          tile<KD>(o, false, u - 2);
+          if (u == 3) tile<KD>(o, false, 2);
         }
       }
-    } else if (b >= 0) {  // the triangular system, the outputs, the state behind the block
-      const int lane = thread_now() & 63, col = lane & 15, g = lane >> 4, v0 = vw + col;
-      const int n = min(R, v.rows - b * R), row0 = v.row0 + b * R;
-      const f32x4 zero = {0, 0, 0, 0};
-      const f32x4 d0 = mfma_f32(o.inv[0][lane], rhs[0], zero);
-      const f32x4 d1 = mfma_f32(o.inv[1][lane], mfma_f32(o.low[2][lane], d0, rhs[1]), zero);
-      const uint32_t odd = s.odd[b], odd_q = s.odd_q[b];
-      if (a.keep || b + 1 < blocks) {
-        uint4 piece[3];
-        f32x4 y[2];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          y[0][r] = o.part[4 * g + r] * d0[r];
-          y[1][r] = o.part[16 + 4 * g + r] * d1[r];
-        }
-        split3(y[0], y[1], piece[0], piece[1], piece[2]);
-        const float keep = o.grow[R - 1];  // rows past n decay by nothing
-#pragma unroll
-        for (int t = 0; t < KT; ++t) {
-          const uint4 f = fragment(o.t + (16 * t + col) * B::TS + 4 * g);
-#pragma unroll
-          for (int r = 0; r < 4; ++r) S[t][0][r] *= keep;
-#pragma unroll
-          for (int p = 2; p >= 0; --p) S[t][0] = mfma_bf16(f, piece[p], S[t][0]);
-        }
-      }
-      acc[0] = mfma_f32(o.see[0][lane], d0, acc[0]);
-      acc[1] = mfma_f32(o.see[1][lane], d1, mfma_f32(o.see[2][lane], d0, acc[1]));
-      uint16_t* outs = a.out + ((size_t)row0 * hv + head) * VD;
-      float* deltas = a.c.delta + delta_at(a.c, a.layer, row0, head);
+      __syncthreads();
+    }
+  } else {
+    f32x4 S[KT][1];
+    load_state<KT, VD, 1>(state, vw, S);
+    const uint16_t* values = a.c.kv + kv_at(a.c, a.layer, v.row0) + (a.c.key_heads * KD + head * VD);
+    uint16_t val[2][4];  // a block's values
+    const auto fetch_values = [&](int b) {
+      const int lane = thread_now() & 63;
 #pragma unroll
       for (int m = 0; m < 2; ++m)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int i = 16 * m + 4 * g + r;
-          if (i < n) {
-            const bool no = before || (odd & ((2u << i) - 1));
-            const uint32_t at = (uint32_t)i * hv * VD + v0;
-            outs[at] = no || ((odd_q >> i) & 1) ? 0x7FC0 : (uint16_t)bf16_pair(a.scale * acc[m][r], 0.0f);
-            if (!a.keep) deltas[at] = no ? __builtin_nanf("") : m ? d1[r] : d0[r];
-          }
-        }
-      before = before || odd;
+        for (int r = 0; r < 4; ++r)
+          val[m][r] = values[(uint32_t)min(b * R + 16 * m + 4 * (lane >> 4) + r, v.rows - 1) * a.c.kv_width + vw + (lane & 15)];
+    };
+    fetch_values(0);
+    __syncthreads();
+    if (s.bad) {
+      if (!(s.bad & 2)) no_numbers(a, v, head, VD, v_slab, 16 * kWaves);
+      return;
     }
     __syncthreads();
-  }
-  if (!a.keep) return;
-  if (!maker) {
-    if (before) {
+    __syncthreads();
+    for (int b = 0; b < blocks; ++b) {
+      B& o = s.block[b & 1];
+      const int n = min(R, v.rows - b * R);
+      f32x4 rhs[2], acc[2];
+      {  // products with the old state
+        const int lane = thread_now() & 63, col = lane & 15, g = lane >> 4;
+        f32x4 w[2];
 #pragma unroll
-      for (int t = 0; t < KT; ++t) S[t][0] = f32x4{__builtin_nanf(""), __builtin_nanf(""), __builtin_nanf(""), __builtin_nanf("")};
+        for (int m = 0; m < 2; ++m) w[m] = acc[m] = f32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int t = 0; t < KT; t += 2) {
+          uint4 piece[3];
+          split3(S[t][0], S[t + 1][0], piece[0], piece[1], piece[2]);
+#pragma unroll
+          for (int m = 0; m < 2; ++m) {
+            const uint4 fk = fragment(o.k + (16 * m + col) * B::KS + 16 * t + 4 * g);
+            const uint4 fq = fragment(o.q + (16 * m + col) * B::KS + 16 * t + 4 * g);
+#pragma unroll
+            for (int p = 2; p >= 0; --p) {
+              w[m] = mfma_bf16(fk, piece[p], w[m]);
+              acc[m] = mfma_bf16(fq, piece[p], acc[m]);
+            }
+          }
+        }
+        uint32_t odd = 0;
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int i = 16 * m + 4 * g + r;
+            uint32_t y = val[m][r];
+            const bool no = odd16(y);
+            if (no && i < n) odd |= 1u << i;
+            y = no || i >= n ? 0 : y << 16;
+            const float grow = o.grow[i];
+            rhs[m][r] = o.beta[i] * (__uint_as_float(y) - grow * w[m][r]);
+            acc[m][r] *= grow;
+          }
+        if (odd) atomicOr(&s.odd[b], odd);
+        fetch_values(min(b + 1, blocks - 1));
+      }
+      __syncthreads();
+      {  // the triangular system, the state behind the block, the outputs
+        const int lane = thread_now() & 63, col = lane & 15, g = lane >> 4, v0 = vw + col;
+        const f32x4 zero = {0, 0, 0, 0};
+        const f32x4 d0 = mfma_f32(o.inv[0][lane], rhs[0], zero);
+        const f32x4 d1 = mfma_f32(o.inv[1][lane], mfma_f32(o.low[2][lane], d0, rhs[1]), zero);
+        if (a.keep || b + 1 < blocks) {
+          uint4 piece[3];
+          f32x4 y[2];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            y[0][r] = o.part[4 * g + r] * d0[r];
+            y[1][r] = o.part[16 + 4 * g + r] * d1[r];
+          }
+          split3(y[0], y[1], piece[0], piece[1], piece[2]);
+          const float keep = o.grow[R - 1];  // rows past n decay by nothing
+#pragma unroll
+          for (int t = 0; t < KT; ++t) {
+            const uint4 f = fragment(o.t + (16 * t + col) * B::TS + 4 * g);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) S[t][0][r] *= keep;
+#pragma unroll
+            for (int p = 2; p >= 0; --p) S[t][0] = mfma_bf16(f, piece[p], S[t][0]);
+          }
+        }
+        acc[0] = mfma_f32(o.see[0][lane], d0, acc[0]);
+        acc[1] = mfma_f32(o.see[1][lane], d1, mfma_f32(o.see[2][lane], d0, acc[1]));
+        const uint32_t odd = s.odd[b], odd_q = s.odd_q[b];
+        const int row0 = v.row0 + b * R;
+        uint16_t* outs = a.out + ((size_t)row0 * hv + head) * VD;
+        float* deltas = a.c.delta + delta_at(a.c, a.layer, row0, head);
+        const uint32_t step = hv * VD, at0 = 4 * g * step + v0;
+        if (n == R && !before && !(odd | odd_q)) {
+#pragma unroll
+          for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const uint32_t at = at0 + (16 * m + r) * step;
+              outs[at] = (uint16_t)bf16_pair(a.scale * acc[m][r], 0.0f);
+              if (!a.keep) deltas[at] = m ? d1[r] : d0[r];
+            }
+        } else {
+#pragma unroll
+          for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const int i = 16 * m + 4 * g + r;
+              if (i < n) {
+                const bool no = before || (odd & ((2u << i) - 1));
+                const uint32_t at = at0 + (16 * m + r) * step;
+                outs[at] = no || ((odd_q >> i) & 1) ? 0x7FC0 : (uint16_t)bf16_pair(a.scale * acc[m][r], 0.0f);
+                if (!a.keep) deltas[at] = no ? __builtin_nanf("") : m ? d1[r] : d0[r];
+              }
+            }
+        }
+        before = before || odd;
+      }
+      __syncthreads();
     }
-    store_state<KT, VD, 1>(state, vw, S);
+    if (a.keep) {
+      if (before) {
+#pragma unroll
+        for (int t = 0; t < KT; ++t) S[t][0] = f32x4{__builtin_nanf(""), __builtin_nanf(""), __builtin_nanf(""), __builtin_nanf("")};
+      }
+      store_state<KT, VD, 1>(state, vw, S);
+    }
   }
-  keep_window(a, v);
+  if (a.keep) keep_window(a, v);
 }
 
 }  // namespace

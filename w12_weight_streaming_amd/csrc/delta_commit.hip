@@ -14,7 +14,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kTurn = 32;             // rows a turn
-constexpr int kStride = kTurn + 16;   // of a key dim's rows in LDS: no bank twice
+constexpr int kStride = kTurn + 8;    // of a key dim's rows in LDS: 8-byte reads meet no bank twice
 
 // A wave owns NC * 16 of the head's value dims, the lane NC neighbouring ones.
 template <int KD, int NC>

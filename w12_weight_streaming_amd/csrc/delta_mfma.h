@@ -83,27 +83,37 @@ __device__ __forceinline__ f32x4 pair_tile(const uint16_t* x, const uint16_t* k,
 
 // (I + L)^-1 of a diagonal tile from -L, a column per lane of the first 16, by
 // forward substitution: L's products of keys make it as well conditioned as the
-// rule itself, where powers of L would cancel. Few: the wave has few registers
-// to spare (all rows of L at once take 160), and rows past n hold nothing.
-template <bool Few>
-__device__ __forceinline__ void invert(const f32x4* low, f32x4* inv, int n) {
-  const int lane = thread_now() & 63, c = lane & 15;
-  float x[16];
+// rule itself, where powers of L would cancel. Rows past n hold nothing, and
+// eight of them cost half a tile's time; rows of L are read eight and four at a
+// time (all at once take 160 registers).
+template <int First, int Last>
+__device__ __forceinline__ void substitute(const f32x4* low, int c, float (&x)[16]) {
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
+  for (int i = First; i < Last; ++i) {
     float y = i == c ? 1.0f : 0.0f;
-    if (!Few || i < n) {  // the same for all lanes
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        if (4 * g < i) {
-          const f32x4 l = low[g * 16 + i];
+    for (int g = 0; g < 4; ++g) {
+      if (4 * g < i) {
+        const f32x4 l = low[g * 16 + i];
 #pragma unroll
-          for (int r = 0; r < 4; ++r)
-            if (4 * g + r < i) y += l[r] * x[4 * g + r];
-        }
+        for (int r = 0; r < 4; ++r)
+          if (4 * g + r < i) y += l[r] * x[4 * g + r];
       }
     }
     x[i] = y;
+  }
+  __builtin_amdgcn_sched_barrier(0);
+}
+__device__ __forceinline__ void invert(const f32x4* low, f32x4* inv, int n) {
+  const int lane = thread_now() & 63, c = lane & 15;
+  float x[16];
+  substitute<0, 8>(low, c, x);
+  if (n > 8) {  // the same for all lanes
+    substitute<8, 12>(low, c, x);
+    substitute<12, 16>(low, c, x);
+  } else {
+#pragma unroll
+    for (int i = 8; i < 16; ++i) x[i] = i == c ? 1.0f : 0.0f;
   }
   if (lane < 16) {
     float* o = reinterpret_cast<float*>(inv);

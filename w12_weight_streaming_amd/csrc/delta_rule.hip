@@ -29,14 +29,12 @@
 namespace w12 {
 namespace {
 
-constexpr int kWaves = 4;
-constexpr int kThreads = 64 * kWaves;
 
 template <int KD, int RT>
 struct Shared {
   static constexpr int R = 16 * RT;
-  static constexpr int KS = KD + 16;                // row of q and k: 8 rows of 8-byte reads meet no bank twice
-  static constexpr int TS = 16;                     // the same for a key dim's rows
+  static constexpr int KS = KD + 8;                 // row of q and k: each 4 banks (of 64) further, so 8-byte reads meet none twice
+  static constexpr int TS = 24;                     // the same for a key dim's rows
   alignas(16) uint16_t q[R * KS];
   alignas(16) uint16_t k[R * KS];
   // chains (RT 1): k with rows innermost; trees: the rows of an earlier block
@@ -59,31 +57,37 @@ struct Shared {
   int bad;
 };
 
-// Rows of keys or queries into LDS, rows past `n` zero; all loads first. A row with an infinity or NaN is
-// marked, and zeros stand in for it: its outputs are set apart from the products.
-template <int KD, int R, int KS>
-__device__ __forceinline__ void load_rows(const uint16_t* from, int step, int n, uint16_t* to, unsigned long long* odd) {
-  constexpr int kChunks = KD / 8, kTurns = (R * kChunks + kThreads - 1) / kThreads;
-  const int tid = thread_now();
+// Rows of keys or queries in the registers of a workgroup, then into LDS, rows past `n` zero. A row with an
+// infinity or NaN is marked, and zeros stand in for it: its outputs are set apart from the products.
+template <int KD, int R, int kThreads>
+struct Staged {
+  static constexpr int kChunks = KD / 8, kTurns = (R * kChunks + kThreads - 1) / kThreads;
   uint4 x[kTurns];
+  __device__ __forceinline__ void load(const uint16_t* from, int step, int n) {
+    const int tid = thread_now();
 #pragma unroll
-  for (int i = 0; i < kTurns; ++i) {
-    const int e = tid + i * kThreads, r = e / kChunks;
-    x[i] = *reinterpret_cast<const uint4*>(from + ((uint32_t)min(r, n - 1) * step + (e % kChunks) * 8));
+    for (int i = 0; i < kTurns; ++i) {
+      const int e = tid + i * kThreads;
+      x[i] = *reinterpret_cast<const uint4*>(from + ((uint32_t)min(e / kChunks, n - 1) * step + (e % kChunks) * 8));
+    }
   }
+  __device__ __forceinline__ void store(int n, uint16_t* to, int stride, unsigned long long* odd) {
+    const int tid = thread_now();
 #pragma unroll
-  for (int i = 0; i < kTurns; ++i) {
-    const int e = tid + i * kThreads, r = e / kChunks;
-    if (R * kChunks % kThreads != 0 && e >= R * kChunks) break;
-    const bool no = odd8(x[i]);
-    if (no && r < n) atomicOr(odd, 1ull << r);
-    if (no || r >= n) x[i] = make_uint4(0, 0, 0, 0);
-    *reinterpret_cast<uint4*>(to + r * KS + (e % kChunks) * 8) = x[i];
+    for (int i = 0; i < kTurns; ++i) {
+      const int e = tid + i * kThreads, r = e / kChunks;
+      if (R * kChunks % kThreads != 0 && e >= R * kChunks) break;
+      const bool no = odd8(x[i]);
+      if (no && r < n) atomicOr(odd, 1ull << r);
+      if (no || r >= n) x[i] = make_uint4(0, 0, 0, 0);
+      *reinterpret_cast<uint4*>(to + r * stride + (e % kChunks) * 8) = x[i];
+    }
   }
-}
+};
 
-template <int KD, int VD, int RT, int NC>
-__global__ __launch_bounds__(kThreads, RT == 1 ? (NC == 1 ? 4 : 3) : RT == 2 ? 2 : 1) void delta_rule_kernel(DeltaRuleArgs a) {
+template <int KD, int VD, int RT, int kWaves>
+__global__ __launch_bounds__(64 * kWaves, RT == 1 ? 4 : RT == 2 ? 2 : 1) void delta_rule_kernel(DeltaRuleArgs a) {
+  constexpr int NC = 1, kThreads = 64 * kWaves;
   using Sh = Shared<KD, RT>;
   constexpr int R = Sh::R, KS = Sh::KS, TS = Sh::TS, KT = KD / 16;
   __shared__ Sh s;
@@ -103,6 +107,24 @@ __global__ __launch_bounds__(kThreads, RT == 1 ? (NC == 1 ? 4 : 3) : RT == 2 ? 2
   }
   const bool chain = RT == 1 && !a.st.parent;
   const int blocks = (v.rows + R - 1) / R;
+  // a block's keys, queries and values (in the layout of the products)
+  Staged<KD, R, kThreads> keys, queries;
+  uint32_t values[RT][4];
+  const auto fetch = [&](int b) {
+    const int row0 = v.row0 + b * R, n = min(R, v.rows - b * R);
+    const uint16_t* kv = a.c.kv + kv_at(a.c, a.layer, row0);
+    keys.load(kv + key * KD, a.c.kv_width, n);
+    queries.load(a.q + ((size_t)row0 * a.c.key_heads + key) * KD, a.c.key_heads * KD, n);
+    const int lane = thread_now() & 63, g = lane >> 4, v0 = a.c.key_heads * KD + head * VD + vw + (lane & 15) * NC;
+#pragma unroll
+    for (int m = 0; m < RT; ++m)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const uint16_t* p = kv + ((uint32_t)min(16 * m + 4 * g + r, n - 1) * a.c.kv_width + v0);
+        values[m][r] = NC == 2 ? *reinterpret_cast<const uint32_t*>(p) : *p;
+      }
+  };
+  fetch(0);
   // parts that one wave plays go round the waves with the workgroup, so that no SIMD has them all
   const int role = (wave + blockIdx.x) & (kWaves - 1);
   for (int i = tid; i < kStepRows / R; i += kThreads) s.odd[i] = 0;
@@ -166,22 +188,19 @@ __global__ __launch_bounds__(kThreads, RT == 1 ? (NC == 1 ? 4 : 3) : RT == 2 ? 2
       }
       __syncthreads();
     }
-    const uint16_t* keys = a.c.kv + kv_at(a.c, a.layer, row0) + key * KD;
-    load_rows<KD, R, KS>(keys, a.c.kv_width, n, s.k, &s.odd[b]);
-    load_rows<KD, R, KS>(a.q + ((size_t)row0 * a.c.key_heads + key) * KD, a.c.key_heads * KD, n, s.q, &s.odd_q);
-    // values, in the layout of the products
+    if (b > 0) fetch(b);
+    keys.store(n, s.k, KS, &s.odd[b]);
+    queries.store(n, s.q, KS, &s.odd_q);
     f32x4 rhs[RT][NC];
     {
-      const int lane = thread_now() & 63, g = lane >> 4, v0 = vw + (lane & 15) * NC;
+      const int lane = thread_now() & 63, g = lane >> 4;
       unsigned long long odd = 0;
-      const uint16_t* values = a.c.kv + kv_at(a.c, a.layer, row0) + (a.c.key_heads * KD + head * VD);
 #pragma unroll
       for (int m = 0; m < RT; ++m)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const int i = 16 * m + 4 * g + r;
-          const uint16_t* p = values + ((uint32_t)min(i, n - 1) * a.c.kv_width + v0);
-          uint32_t x = NC == 2 ? *reinterpret_cast<const uint32_t*>(p) : *p;
+          uint32_t x = values[m][r];
           if (odd16(x) && i < n) odd |= 1ull << i;
           if (odd16(x) || i >= n) x = 0;
           rhs[m][0][r] = __uint_as_float(x << 16);
@@ -192,7 +211,7 @@ __global__ __launch_bounds__(kThreads, RT == 1 ? (NC == 1 ? 4 : 3) : RT == 2 ? 2
     if (tid < R) s.behind[tid] = 0, s.next[tid] = base + tid < v.rows ? s.leave[base + tid] : -1;
     __syncthreads();
     if (s.bad) {
-      if (!(s.bad & 2)) no_numbers(a, v, head, VD, vw - wave * (16 * NC), 64 * NC);
+      if (!(s.bad & 2)) no_numbers(a, v, head, VD, vw - wave * 16, 16 * kWaves);
       return;
     }
     if (b > 0 && !chain) {  // sums from the state, now that those of the rows above the block are
@@ -226,7 +245,7 @@ __global__ __launch_bounds__(kThreads, RT == 1 ? (NC == 1 ? 4 : 3) : RT == 2 ? 2
     if (role < RT) {
       tile(true, role, role);
       wave_lds_sync();
-      invert<RT == 1>(s.low[role * RT + role], s.inv[role], n);
+      invert(s.low[role * RT + role], s.inv[role], n - 16 * role);
     }
     {
       int u = RT;
@@ -234,8 +253,8 @@ __global__ __launch_bounds__(kThreads, RT == 1 ? (NC == 1 ? 4 : 3) : RT == 2 ? 2
       for (int bi = 0; bi < RT; ++bi)
 #pragma unroll
         for (int bj = 0; bj <= bi; ++bj) {
-          if (bj < bi && (u++ & 3) == role) tile(true, bi, bj);
-          if ((u++ & 3) == role) tile(false, bi, bj);
+          if (bj < bi && (u++ & (kWaves - 1)) == role) tile(true, bi, bj);
+          if ((u++ & (kWaves - 1)) == role) tile(false, bi, bj);
         }
     }
 
@@ -285,7 +304,8 @@ __global__ __launch_bounds__(kThreads, RT == 1 ? (NC == 1 ? 4 : 3) : RT == 2 ? 2
       for (int e = b - 1; e >= 0; --e) {
         __syncthreads();
         const int lane = thread_now() & 63, col = lane & 15, g = lane >> 4, v0 = vw + col * NC;
-        load_rows<KD, R, KS>(a.c.kv + kv_at(a.c, a.layer, v.row0 + e * R) + key * KD, a.c.kv_width, R, s.t, &s.odd[e]);
+        keys.load(a.c.kv + kv_at(a.c, a.layer, v.row0 + e * R) + key * KD, a.c.kv_width, R);
+        keys.store(R, s.t, KS, &s.odd[e]);
         if (tid < R) {
           const int p = s.next[tid];
           unsigned long long m = 0;
@@ -423,8 +443,10 @@ __global__ __launch_bounds__(kThreads, RT == 1 ? (NC == 1 ? 4 : 3) : RT == 2 ? 2
 }
 
 // Plain decoding: as many rows as sequences, chains.
+constexpr int kDecodeThreads = 256;
 template <int KD, int VD, int NC>
-__global__ __launch_bounds__(kThreads, 4) void delta_decode_kernel(DeltaRuleArgs a) {
+__global__ __launch_bounds__(kDecodeThreads, 4) void delta_decode_kernel(DeltaRuleArgs a) {
+  constexpr int kWaves = kDecodeThreads / 64;
   constexpr int KT = KD / 16, slabs = VD / (kWaves * 16 * NC);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int head = blockIdx.x / slabs, key = head / (a.c.value_heads / a.c.key_heads), seq = blockIdx.y;
@@ -444,19 +466,19 @@ hipError_t launch(const DeltaRuleArgs& a, hipStream_t s) {
   if (rows == 1 && !a.st.parent) {
     if constexpr (VD == 128) {
       if (a.c.value_heads * a.st.num_seq >= 512) {
-        delta_decode_kernel<KD, VD, 2><<<dim3(a.c.value_heads, a.st.num_seq), kThreads, 0, s>>>(a);
+        delta_decode_kernel<KD, VD, 2><<<dim3(a.c.value_heads, a.st.num_seq), kDecodeThreads, 0, s>>>(a);
         return hipGetLastError();
       }
     }
-    delta_decode_kernel<KD, VD, 1><<<grid, kThreads, 0, s>>>(a);
+    delta_decode_kernel<KD, VD, 1><<<grid, kDecodeThreads, 0, s>>>(a);
   } else if (rows <= 16) {
-    delta_rule_kernel<KD, VD, 1, 1><<<grid, kThreads, 0, s>>>(a);
+    delta_rule_kernel<KD, VD, 1, VD / 16><<<dim3(a.c.value_heads, a.st.num_seq), VD * 4, 0, s>>>(a);
   } else if (!a.st.parent) {
     return launch_delta_chain(a, s);
   } else if (rows <= 32) {
-    delta_rule_kernel<KD, VD, 2, 1><<<grid, kThreads, 0, s>>>(a);
+    delta_rule_kernel<KD, VD, 2, 4><<<grid, 256, 0, s>>>(a);
   } else {
-    delta_rule_kernel<KD, VD, 4, 1><<<grid, kThreads, 0, s>>>(a);
+    delta_rule_kernel<KD, VD, 4, 4><<<grid, 256, 0, s>>>(a);
   }
   return hipGetLastError();
 }
