@@ -65,14 +65,14 @@ __device__ __forceinline__ void stage(Shared<KD>& s, int b, int n, int tid, Rows
     for (int i = 0; i < 2; ++i)
       if (r + i >= n) x.k[i] = x.q[i] = make_uint4(0, 0, 0, 0);
   }
-  if (odd8(x.k[0]) || odd8(x.k[1]) || odd8(x.q[0]) || odd8(x.q[1])) {
+  if (is_odd(odd_sum(x.k[0]) | odd_sum(x.k[1]) | odd_sum(x.q[0]) | odd_sum(x.q[1]))) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      if (odd8(x.k[i])) {
+      if (is_odd(odd_sum(x.k[i]))) {
         atomicOr(&s.odd[b], 1u << (r + i));
         x.k[i] = make_uint4(0, 0, 0, 0);
       }
-      if (odd8(x.q[i])) {
+      if (is_odd(odd_sum(x.q[i]))) {
         atomicOr(&s.odd_q[b], 1u << (r + i));
         x.q[i] = make_uint4(0, 0, 0, 0);
       }
@@ -239,21 +239,34 @@ __global__ __launch_bounds__(64 * (kMakers + kTakers)) __attribute__((amdgpu_wav
               acc[m] = mfma_bf16(fq[m][t], piece[p], acc[m]);
             }
         }
-        uint32_t odd = 0;
+        uint32_t sums = 0;
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) sums |= odd_sum(val[m][r]);
+        if (is_odd(sums)) {
+          uint32_t odd = 0;
+#pragma unroll
+          for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              if (is_odd(odd_sum(val[m][r]))) {
+                const int i = 16 * m + 4 * g + r;
+                if (i < n) odd |= 1u << i;
+                val[m][r] = 0;
+              }
+          if (odd) atomicOr(&s.odd[b], odd);
+        }
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
-          const int i = 16 * m + 4 * g;
-          const f32x4 grow = *reinterpret_cast<const f32x4*>(s.grow + b * R + i), beta = *reinterpret_cast<const f32x4*>(s.beta + b * R + i);
+          const int i = b * R + 16 * m + 4 * g;
+          const f32x4 grow = *reinterpret_cast<const f32x4*>(s.grow + i), beta = *reinterpret_cast<const f32x4*>(s.beta + i);
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const bool no = odd16(val[m][r]);
-            if (no && i + r < n) odd |= 1u << (i + r);
-            const float y = no ? 0.0f : __uint_as_float(val[m][r] << 16);  // rows past the end have no strength
-            rhs[m][r] = beta[r] * (y - grow[r] * w[m][r]);
+          for (int r = 0; r < 4; ++r) {  // rows past the end have no strength
+            rhs[m][r] = beta[r] * (__uint_as_float(val[m][r] << 16) - grow[r] * w[m][r]);
             acc[m][r] *= grow[r];
           }
         }
-        if (odd) atomicOr(&s.odd[b], odd);
         fetch_values((b + 1) * R);
       }
       __syncthreads();

@@ -65,9 +65,11 @@ __device__ __forceinline__ void store_turned(uint16_t* to, int stride, const uin
         __builtin_amdgcn_perm(u[1][i >> 1], u[0][i >> 1], (i & 1) ? 0x07060302u : 0x05040100u);
 }
 
-// An infinity or NaN among bf16 values, or as an fp32 value.
-__device__ __forceinline__ bool odd16(uint32_t w) { return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u; }
-__device__ __forceinline__ bool odd8(const uint4& x) { return odd16(x.x) || odd16(x.y) || odd16(x.z) || odd16(x.w); }
+// Infinities and NaN among bf16 values: their exponent's ones carry into the
+// sign's place, and several words' sums can be looked at together.
+__device__ __forceinline__ uint32_t odd_sum(uint32_t w) { return (w & 0x7F807F80u) + 0x00800080u; }
+__device__ __forceinline__ uint32_t odd_sum(const uint4& x) { return odd_sum(x.x) | odd_sum(x.y) | odd_sum(x.z) | odd_sum(x.w); }
+__device__ __forceinline__ bool is_odd(uint32_t sums) { return sums & 0x80008000u; }
 __device__ __forceinline__ bool odd32(float x) { return !(fabsf(x) <= 3.4e38f); }
 
 // One tile of x . k, transposed, over KD dims: lane (l / 16, l % 16) holds row l % 16 of x, rows 4 (l / 16) + r

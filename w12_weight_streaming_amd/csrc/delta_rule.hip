@@ -77,7 +77,7 @@ struct Staged {
     for (int i = 0; i < kTurns; ++i) {
       const int e = tid + i * kThreads, r = e / kChunks;
       if (R * kChunks % kThreads != 0 && e >= R * kChunks) break;
-      const bool no = odd8(x[i]);
+      const bool no = is_odd(odd_sum(x[i]));
       if (no && r < n) atomicOr(odd, 1ull << r);
       if (no || r >= n) x[i] = make_uint4(0, 0, 0, 0);
       *reinterpret_cast<uint4*>(to + r * stride + (e % kChunks) * 8) = x[i];
@@ -121,7 +121,7 @@ __global__ __launch_bounds__(64 * kWaves, RT == 1 ? 4 : RT == 2 ? 2 : 1) void de
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const uint16_t* p = kv + ((uint32_t)min(16 * m + 4 * g + r, n - 1) * a.c.kv_width + v0);
-        values[m][r] = NC == 2 ? *reinterpret_cast<const uint32_t*>(p) : *p;
+        values[m][r] = *p;
       }
   };
   fetch(0);
@@ -200,11 +200,10 @@ __global__ __launch_bounds__(64 * kWaves, RT == 1 ? 4 : RT == 2 ? 2 : 1) void de
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const int i = 16 * m + 4 * g + r;
-          uint32_t x = values[m][r];
-          if (odd16(x) && i < n) odd |= 1ull << i;
-          if (odd16(x) || i >= n) x = 0;
-          rhs[m][0][r] = __uint_as_float(x << 16);
-          if constexpr (NC == 2) rhs[m][1][r] = __uint_as_float(x & 0xFFFF0000u);
+          const uint32_t x = values[m][r];
+          const bool no = is_odd(odd_sum(x));
+          if (no && i < n) odd |= 1ull << i;
+          rhs[m][0][r] = no || i >= n ? 0.0f : __uint_as_float(x << 16);
         }
       if (odd) atomicOr(&s.odd[b], odd);
     }
