@@ -147,7 +147,7 @@ __global__ __launch_bounds__(64 * (kMakers + kTakers)) __attribute__((amdgpu_wav
   const int blocks = (v.rows + R - 1) / R;
   if (tid < kStepRows / R) s.odd[tid] = s.odd_q[tid] = 0;
   if (wave == 0) {
-    const int bad = refused(a, v, seq, true);
+    const int bad = refused(a, v, seq, look(a, v));
     if ((thread_now() & 63) == 0) s.bad = bad;
   }
   bool before = false;  // a block holds a row that is no number

@@ -52,18 +52,34 @@ __device__ __forceinline__ void keep_window(const DeltaRuleArgs& a, const RowsVi
                  [&](int j) { return v.row0 + j; });
 }
 
+// What a wave looks at to tell whether its sequence is one, the first 64 of
+// each: read before the state, whose loads a later one would have to wait for.
+struct Look {
+  int first, end, slot, parent;
+};
+__device__ __forceinline__ Look look(const DeltaRuleArgs& a, const RowsView& v) {
+  const int lane = thread_now() & 63, j = min(lane, a.st.num_seq - 1);
+  Look l;
+  l.first = a.st.row_off[j];
+  l.end = a.st.row_off[j + 1];
+  l.slot = a.st.slot ? a.st.slot[j] : j;
+  l.parent = a.st.parent ? a.st.parent[v.row0 + min(lane, v.rows - 1)] : lane - 1;
+  return l;
+}
 // By one wave: 1 if the sequence is refused, 2 if it has no rows.
-__device__ __forceinline__ int refused(const DeltaRuleArgs& a, const RowsView& v, int seq, bool chain) {
-  const int lane = thread_now() & 63;
-  bool bad = !v.ok, none = false;
-  for (int j = lane; j < seq; j += 64) {
+__device__ __forceinline__ int refused(const DeltaRuleArgs& a, const RowsView& v, int seq, const Look& l) {
+  const int lane = thread_now() & 63, last = v.row0 + v.rows;
+  bool none = lane < seq && l.first >= 0 && l.end <= a.st.total && l.first < l.end && l.first < last && l.end > v.row0;
+  bool bad = !v.ok || (a.keep && lane < seq && l.slot == v.slot) ||
+             (lane < v.rows && (lane == 0 ? l.parent != -1 : (l.parent < 0 || l.parent >= lane)));
+  for (int j = lane + 64; j < seq; j += 64) {
     none = none || rows_meet(a.st.row_off, a.st.total, j, v.row0, v.rows);
-    bad = bad || (a.keep && a.st.slot && a.st.slot[j] == v.slot);
+    bad = bad || (a.keep && (a.st.slot ? a.st.slot[j] : j) == v.slot);
   }
-  if (!chain)
-    for (int i = lane; i < v.rows; i += 64) {
+  if (a.st.parent)
+    for (int i = lane + 64; i < v.rows; i += 64) {
       const int p = a.st.parent[v.row0 + i];
-      bad = bad || (i == 0 ? p != -1 : (p < 0 || p >= i));
+      bad = bad || p < 0 || p >= i;
     }
   return __any(none) ? 2 : __any(bad) ? 1 : 0;
 }
@@ -79,10 +95,10 @@ __device__ __forceinline__ void no_numbers(const DeltaRuleArgs& a, const RowsVie
 // lanes of a column. Rows follow each other (a tree has one row here).
 template <int KD, int VD, int NC>
 __device__ __forceinline__ void rows_in_turn(const DeltaRuleArgs& a, const RowsView& v, int seq, int head, int key, int vw,
-                                             float* state, f32x4 (&S)[KD / 16][NC]) {
+                                             float* state, const Look& seen, f32x4 (&S)[KD / 16][NC]) {
   constexpr int KT = KD / 16;
   const int lane = thread_now() & 63, g = lane >> 4, v0 = vw + (lane & 15) * NC;
-  const int bad = refused(a, v, seq, !a.st.parent);
+  const int bad = refused(a, v, seq, seen);
   for (int i = 0; i < v.rows; ++i) {
     const int row = v.row0 + i;
     const uint16_t* kp = a.c.kv + kv_at(a.c, a.layer, row) + (key * KD + 4 * g);

@@ -100,9 +100,11 @@ __global__ __launch_bounds__(64 * kWaves, RT == 1 ? 4 : RT == 2 ? 2 : 1) void de
   if (v.rows == 0) return;
   float* state = a.c.state + state_at(a.c, a.layer, v.slot, head);
   f32x4 S[KT][NC];
-  load_state<KT, VD, NC>(state, vw, S);
+  // loads come back in order: what is needed before the state is read before it
+  const Look seen = look(a, v);
   if (v.rows == 1) {
-    rows_in_turn<KD, VD, NC>(a, v, seq, head, key, vw, state, S);
+    load_state<KT, VD, NC>(state, vw, S);
+    rows_in_turn<KD, VD, NC>(a, v, seq, head, key, vw, state, seen, S);
     return;
   }
   const bool chain = RT == 1 && !a.st.parent;
@@ -124,14 +126,23 @@ __global__ __launch_bounds__(64 * kWaves, RT == 1 ? 4 : RT == 2 ? 2 : 1) void de
         values[m][r] = *p;
       }
   };
-  fetch(0);
   // parts that one wave plays go round the waves with the workgroup, so that no SIMD has them all
   const int role = (wave + blockIdx.x) & (kWaves - 1);
+  float gate0, beta0;  // of the first row whose path this lane follows
+  int parent0;
+  {
+    const int i = min(role * 64 + (thread_now() & 63), v.rows - 1);
+    gate0 = a.c.gates[gate_at(a.c, a.layer, v.row0 + i, 0, head)];
+    beta0 = a.c.gates[gate_at(a.c, a.layer, v.row0 + i, 1, head)];
+    parent0 = a.st.parent ? a.st.parent[v.row0 + i] : i - 1;
+  }
+  fetch(0);
+  load_state<KT, VD, NC>(state, vw, S);
   for (int i = tid; i < kStepRows / R; i += kThreads) s.odd[i] = 0;
   if (tid == 0) s.odd_q = 0, s.bad = 0;
   __syncthreads();
   if (role == kWaves - 1) {
-    const int bad = refused(a, v, seq, !a.st.parent);
+    const int bad = refused(a, v, seq, seen);
     if ((thread_now() & 63) == 0) s.bad = bad;
   }
   // paths within each block, by doubling; a lane is a row, the waves take 64 rows in turn
@@ -140,13 +151,14 @@ __global__ __launch_bounds__(64 * kWaves, RT == 1 ? 4 : RT == 2 ? 2 : 1) void de
     float gate = 0, beta = 0;
     int cur = -1, leave = -1;
     if (i < v.rows) {
-      gate = a.c.gates[gate_at(a.c, a.layer, v.row0 + i, 0, head)];
-      beta = a.c.gates[gate_at(a.c, a.layer, v.row0 + i, 1, head)];
+      const bool again = i0 >= kThreads;
+      gate = again ? a.c.gates[gate_at(a.c, a.layer, v.row0 + i, 0, head)] : gate0;
+      beta = again ? a.c.gates[gate_at(a.c, a.layer, v.row0 + i, 1, head)] : beta0;
       if (!(gate <= 3.4e38f) || odd32(beta)) {
         atomicOr(&s.odd[i / R], 1ull << row);
         gate = beta = 0;
       }
-      int p = chain ? (row > 0 ? i - 1 : -1) : a.st.parent[v.row0 + i];
+      int p = chain ? (row > 0 ? i - 1 : -1) : again ? a.st.parent[v.row0 + i] : parent0;
       if (p >= i || p < -1) p = -1;  // no tree: reported, once every row has been looked at
       cur = p - (i - row);
       leave = p;
@@ -381,11 +393,7 @@ __global__ __launch_bounds__(64 * kWaves, RT == 1 ? 4 : RT == 2 ? 2 : 1) void de
           const bool no = before || (s.in[base + i] & odd) || (!chain && s.behind[i]);
           const bool no_q = no || ((odd_q >> i) & 1);
           const uint32_t at = (uint32_t)i * hv * VD + v0;
-          const uint32_t o = no_q ? 0x7FC07FC0u : bf16_pair(a.scale * acc[m][0][r], a.scale * acc[m][NC - 1][r]);
-          if constexpr (NC == 2)
-            *reinterpret_cast<uint32_t*>(outs + at) = o;
-          else
-            outs[at] = (uint16_t)o;
+          outs[at] = no_q ? 0x7FC0 : (uint16_t)bf16_pair(a.scale * acc[m][0][r], 0.0f);
           if (!a.keep) {
 #pragma unroll
             for (int c = 0; c < NC; ++c) deltas[at + c] = no ? __builtin_nanf("") : rhs[m][c][r];
@@ -454,8 +462,9 @@ __global__ __launch_bounds__(kDecodeThreads, 4) void delta_decode_kernel(DeltaRu
   if (v.rows == 0) return;
   float* state = a.c.state + state_at(a.c, a.layer, v.slot, head);
   f32x4 S[KT][NC];
+  const Look seen = look(a, v);
   load_state<KT, VD, NC>(state, vw, S);
-  rows_in_turn<KD, VD, NC>(a, v, seq, head, key, vw, state, S);
+  rows_in_turn<KD, VD, NC>(a, v, seq, head, key, vw, state, seen, S);
 }
 
 template <int KD, int VD>
