@@ -112,18 +112,19 @@ __device__ __forceinline__ size_t delta_at(const DeltaArgs& c, int layer, int ro
   return (((size_t)layer * c.step_rows + row) * c.value_heads + head) * (size_t)c.value_dim;
 }
 
-// Sequence s of a step: ok is false where its offsets or its slot are outside their arrays.
+// Sequence s (the same for all lanes) of a step: ok is false where its offsets
+// or its slot are outside their arrays. In scalar registers, so that addresses are too.
 struct RowsView {
   int row0, rows, slot;
   bool ok;
 };
 __device__ __forceinline__ RowsView rows_view(const DeltaArgs& c, const StepArgs& st, int s) {
   RowsView v;
-  const int b0 = st.row_off[s], b1 = st.row_off[s + 1];
+  const int b0 = __builtin_amdgcn_readfirstlane(st.row_off[s]), b1 = __builtin_amdgcn_readfirstlane(st.row_off[s + 1]);
   v.ok = b0 >= 0 && b0 <= b1 && b1 <= st.total;
   v.row0 = v.ok ? b0 : 0;
   v.rows = v.ok ? b1 - b0 : 0;
-  v.slot = st.slot ? st.slot[s] : s;
+  v.slot = st.slot ? __builtin_amdgcn_readfirstlane(st.slot[s]) : s;
   if (v.slot < 0 || v.slot >= c.slots) {
     v.ok = false;
     v.slot = 0;

@@ -68,7 +68,7 @@ struct Staged {
 #pragma unroll
     for (int i = 0; i < kTurns; ++i) {
       const int e = tid + i * kThreads;
-      x[i] = *reinterpret_cast<const uint4*>(from + ((uint32_t)min(e / kChunks, n - 1) * step + (e % kChunks) * 8));
+      x[i] = *reinterpret_cast<const uint4*>(from + (__umul24(min(e / kChunks, n - 1), step) + (e % kChunks) * 8));
     }
   }
   __device__ __forceinline__ void store(int n, uint16_t* to, int stride, unsigned long long* odd) {
@@ -122,7 +122,7 @@ __global__ __launch_bounds__(64 * kWaves, RT == 1 ? 4 : RT == 2 ? 2 : 1) void de
     for (int m = 0; m < RT; ++m)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const uint16_t* p = kv + ((uint32_t)min(16 * m + 4 * g + r, n - 1) * a.c.kv_width + v0);
+        const uint16_t* p = kv + (__umul24(min(16 * m + 4 * g + r, n - 1), a.c.kv_width) + v0);
         values[m][r] = *p;
       }
   };
@@ -253,20 +253,18 @@ __global__ __launch_bounds__(64 * kWaves, RT == 1 ? 4 : RT == 2 ? 2 : 1) void de
       }
       (of_low ? s.low : s.see)[bi * RT + bj][lane] = x;
     };
-    if (role < RT) {
-      tile(true, role, role);
-      wave_lds_sync();
-      invert(s.low[role * RT + role], s.inv[role], n - 16 * role);
-    }
-    {
-      int u = RT;
-#pragma unroll
-      for (int bi = 0; bi < RT; ++bi)
-#pragma unroll
-        for (int bj = 0; bj <= bi; ++bj) {
-          if (bj < bi && (u++ & (kWaves - 1)) == role) tile(true, bi, bj);
-          if ((u++ & (kWaves - 1)) == role) tile(false, bi, bj);
-        }
+    // (a loop, as the code runs once and its instructions have to be fetched)
+#pragma unroll 1
+    for (int turn = 0, item = role; turn * kWaves < RT + RT * RT; ++turn) {
+      if (item < RT) {
+        tile(true, item, item);
+        wave_lds_sync();
+        invert(s.low[item * RT + item], s.inv[item], n - 16 * item);
+      } else if (item < RT + RT * RT) {
+        const int i = (item - RT) / RT, j = (item - RT) % RT;
+        tile(j > i, max(i, j), min(i, j));
+      }
+      item = (turn + 1) * kWaves + (turn & 1 ? role : kWaves - 1 - role);
     }
 
     // the rows' products with the old state
@@ -384,20 +382,24 @@ __global__ __launch_bounds__(64 * kWaves, RT == 1 ? 4 : RT == 2 ? 2 : 1) void de
     const unsigned long long odd = s.odd[b], odd_q = s.odd_q;
     uint16_t* outs = a.out + ((size_t)row0 * hv + head) * VD;
     float* deltas = a.c.delta + delta_at(a.c, a.layer, row0, head);
+    const uint32_t step = hv * VD, at0 = 4 * g * step + v0;
+    const bool plain = b == 0 && !odd && !odd_q;  // no row to set apart
 #pragma unroll
     for (int m = 0; m < RT; ++m)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const int i = 16 * m + 4 * g + r;
-        if (i < n) {
+        const uint32_t at = at0 + (16 * m + r) * step;
+        uint16_t o = (uint16_t)bf16_pair(a.scale * acc[m][0][r], 0.0f);
+        float d = rhs[m][0][r];
+        if (!plain) {
           const bool no = before || (s.in[base + i] & odd) || (!chain && s.behind[i]);
-          const bool no_q = no || ((odd_q >> i) & 1);
-          const uint32_t at = (uint32_t)i * hv * VD + v0;
-          outs[at] = no_q ? 0x7FC0 : (uint16_t)bf16_pair(a.scale * acc[m][0][r], 0.0f);
-          if (!a.keep) {
-#pragma unroll
-            for (int c = 0; c < NC; ++c) deltas[at + c] = no ? __builtin_nanf("") : rhs[m][c][r];
-          }
+          if (no || ((odd_q >> i) & 1)) o = 0x7FC0;
+          if (no) d = __builtin_nanf("");
+        }
+        if (i < n) {
+          outs[at] = o;
+          if (!a.keep) deltas[at] = d;
         }
       }
 
