@@ -711,24 +711,35 @@ class DeltaCache:
     key_heads: int
 
     def __post_init__(self):
-        at = _get(self.state, _F32, "state", 5, None)
-        index = self.state.get_device()
-        ats = (at, _get(self.conv, _BF16, "conv", 4, index), _get(self.raw, _BF16, "raw", 3, index),
-               _get(self.kv, _BF16, "kv", 3, index), _get(self.gates, _F32, "gates", 4, index),
-               _get(self.delta, _F32, "delta", 4, index))
-        layers, slots, hv, kd, vd = self.state.shape
-        rows = self.raw.shape[1]
-        kv_width = self.key_heads * kd + hv * vd
-        channels = kv_width + self.key_heads * kd
-        width = self.conv.shape[2] + 1
-        if (self.conv.shape != (layers, slots, width - 1, channels) or self.raw.shape != (layers, rows, channels)
-                or self.kv.shape != (layers, rows, kv_width) or self.gates.shape != (layers, rows, 2, hv)
-                or self.delta.shape != (layers, rows, hv, vd)):
+        state, conv, raw, kv, gates, delta, hk = (self.state, self.conv, self.raw, self.kv, self.gates, self.delta,
+                                                  self.key_heads)
+        try:  # all at once: programs describe their state again where they switch between steps' arrays
+            index = state.get_device()
+            layers, slots, hv, kd, vd = state.shape
+            rows, width = raw.shape[1], conv.shape[2]
+            kv_width = hk * kd + hv * vd
+            channels = kv_width + hk * kd
+            good = (index >= 0 and state.dtype is _F32 and gates.dtype is _F32 and delta.dtype is _F32
+                    and conv.dtype is _BF16 and raw.dtype is _BF16 and kv.dtype is _BF16
+                    and conv.shape == (layers, slots, width, channels) and raw.shape == (layers, rows, channels)
+                    and kv.shape == (layers, rows, kv_width) and gates.shape == (layers, rows, 2, hv)
+                    and delta.shape == (layers, rows, hv, vd)
+                    and state.is_contiguous() and conv.is_contiguous() and raw.is_contiguous() and kv.is_contiguous()
+                    and gates.is_contiguous() and delta.is_contiguous() and conv.get_device() == index
+                    and raw.get_device() == index and kv.get_device() == index and gates.get_device() == index
+                    and delta.get_device() == index)
+        except (AttributeError, TypeError, ValueError, IndexError):
+            good = False
+        if not good:
+            _get(state, _F32, "state", 5, None)
+            for t, dtype, name, ndim in ((conv, _BF16, "conv", 4), (raw, _BF16, "raw", 3), (kv, _BF16, "kv", 3),
+                                         (gates, _F32, "gates", 4), (delta, _F32, "delta", 4)):
+                _get(t, dtype, name, ndim, state.get_device())
             raise ValueError("the recurrent state's arrays differ in shape")
-        desc = W12DeltaCache(layers, slots, rows, self.key_heads, hv, kd, vd, width, *ats)
-        for name, value in (("index", index), ("value_heads", hv), ("key_dim", kd), ("value_dim", vd),
-                            ("channels", channels), ("conv_width", width), ("_desc", desc), ("_ref", ctypes.byref(desc))):
-            object.__setattr__(self, name, value)
+        desc = W12DeltaCache(layers, slots, rows, hk, hv, kd, vd, width + 1, state.data_ptr(), conv.data_ptr(),
+                             raw.data_ptr(), kv.data_ptr(), gates.data_ptr(), delta.data_ptr())
+        self.__dict__.update(index=index, value_heads=hv, key_dim=kd, value_dim=vd, channels=channels,
+                             conv_width=width + 1, step_rows=rows, _desc=desc, _ref=ctypes.byref(desc))
 
     @property
     def device(self):
@@ -755,19 +766,26 @@ def delta_cache(layers: int, slots: int, key_heads: int, value_heads: int, key_d
                       torch.zeros(layers, step_rows, value_heads, value_dim, **f), key_heads)
 
 
-def _rows_of(t, name: str, columns: int, index: int | None) -> tuple[int, int, int]:
+def _rows_of(t, name: str, columns: int, index: int) -> tuple[int, int, int]:
     """Address, row stride and type of a [rows, columns] fp32 or bf16 tensor
-    whose rows lie apart (columns of a wider product)."""
-    if not isinstance(t, torch.Tensor) or t.dtype not in (_F32, _BF16):
-        raise TypeError(f"{name} must be a float32 or bfloat16 tensor")
-    if t.dim() != 2 or t.shape[1] != columns:
-        raise ValueError(f"{name} must be [rows, {columns}] (got {tuple(t.shape)})")
-    if t.get_device() < 0 or (index is not None and t.get_device() != index):
-        raise ValueError(f"{name} must be on {'a GPU' if index is None else f'cuda:{index}'} (got {t.device})")
+    on GPU `index` whose rows lie apart (columns of a wider product)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    dtype, shape = t.dtype, t.shape
+    if dtype is not _F32 and dtype is not _BF16:
+        raise TypeError(f"{name} must be a float32 or bfloat16 tensor (got {dtype})")
+    if len(shape) != 2 or shape[1] != columns:
+        raise ValueError(f"{name} must be [rows, {columns}] (got {tuple(shape)})")
+    if index < 0 or t.get_device() != index:
+        raise ValueError(f"{name} must be on {'a GPU' if index < 0 else f'cuda:{index}'} (got {t.device})")
     step, unit = t.stride()
-    if (unit != 1 and columns > 1) or (t.shape[0] > 1 and step < columns):
-        raise ValueError(f"{name}'s rows must be contiguous and apart (strides {t.stride()})")
-    return t.data_ptr(), max(step, columns) if t.shape[0] > 1 else -(-columns // 8) * 8, W12_Y_F32 if t.dtype is _F32 else W12_Y_BF16
+    if shape[0] == 1:
+        step = -(-columns // 8) * 8  # one row: any stride
+    elif step < columns:
+        raise ValueError(f"{name}'s rows must lie apart (strides {t.stride()})")
+    if unit != 1 and columns > 1:
+        raise ValueError(f"{name}'s rows must be contiguous (strides {t.stride()})")
+    return t.data_ptr(), step, W12_Y_F32 if dtype is _F32 else W12_Y_BF16
 
 
 def w12_delta_append(cache: DeltaCache, layer: int, qkv: torch.Tensor, ba: torch.Tensor, row_off: torch.Tensor,
@@ -846,7 +864,7 @@ def w12_delta_commit(cache: DeltaCache, row_off: torch.Tensor, accept_len: torch
     if path is not None:
         at_path, rows = _get(path, _I32, "path", 1, index, rows), path.shape[0]
     elif rows is None:
-        rows = min(MAX_ROWS, cache._desc.step_rows)
+        rows = min(MAX_ROWS, cache.step_rows)
     kept = torch.empty(max(seqs, 0), dtype=_I32, device=cache.device)
     _run(index, "w12_delta_commit", cache._ref, seqs, 0 if slot is None else _get(slot, _I32, "slot", 1, index, seqs),
          at_off, rows, _get(accept_len, _I32, "accept_len", 1, index, seqs), at_path, kept.data_ptr())
