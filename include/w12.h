@@ -533,7 +533,8 @@ typedef struct w12_delta_cache {
  *        product as they lie;
  *   conv_weight [channels][conv_width] fp32, the row's own tap last;
  *   conv_bias [channels] fp32 or NULL; a_log, dt_bias [value_heads] fp32;
- *   q    [total_rows][key_heads][key_dim] bf16 out, apart from qkv and ba.
+ *   q    [total_rows][key_heads][key_dim] bf16 out, apart from qkv, ba and
+ *        the cache's arrays.
  * Writes raw, kv and gates of its rows; state and conv are read at most.
  * Device-detected, reported as NaN queries with nothing staged: an invalid
  * tree, a slot outside [0, slots).
@@ -553,9 +554,12 @@ w12_status w12_delta_append(const w12_delta_cache *cache, int32_t layer, int32_t
  * the matrix products whole: in fp32, or in three bf16 pieces that hold its 24 bits)
  * and decays summed in 64 bits. A row sees its ancestors and itself: an
  * infinity or NaN in a row's q, k, v or gates reaches only its own outputs
- * and those behind it (whole heads of them), never other rows'.
+ * and deltas and those behind it, and the state behind them, of the heads it
+ * belongs to (whole heads of them), never other rows'. Deltas and products
+ * beyond 2^100 may come out as infinities or NaN in the whole sequence.
  *   q    [total_rows][key_heads][key_dim] bf16 (w12_delta_append's output);
- *   out  [total_rows][value_heads * value_dim] bf16, apart from q;
+ *   out  [total_rows][value_heads * value_dim] bf16, apart from q and the
+ *        cache's arrays;
  *   keep 0: writes the rows' delta; state and conv stay, and w12_delta_commit
  *        keeps the accepted rows. Not 0 (parent NULL only: prompts, plain
  *        decoding): every row is kept, state and conv become those behind the
@@ -576,8 +580,8 @@ w12_status w12_delta_rule(const w12_delta_cache *cache, int32_t layer, int32_t n
  * along the path, and the window.
  *   kept [num_seq] out: rows kept; accept_len -1 (a refused tree) keeps none.
  * Device-detected, reported as kept -1 with nothing written: a slot outside
- * [0, slots) or of an earlier sequence, an accept_len or path outside the
- * sequence's rows or not ascending from row 0.
+ * [0, slots) or of an earlier sequence, a range of rows that is none, an
+ * accept_len or path outside the sequence's rows or not ascending from row 0.
  */
 w12_status w12_delta_commit(const w12_delta_cache *cache, int32_t num_seq, const int32_t *slot, const int32_t *row_off,
                             int32_t total_rows, const int32_t *accept_len, const int32_t *path, int32_t *kept,

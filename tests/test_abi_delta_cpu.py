@@ -64,7 +64,8 @@ def test_append_arguments(w12):
                dict(x=NULL), dict(x=ODD), dict(xs=C - 4), dict(xs=C + 2), dict(xs=C + 4, kind=1), dict(xs=1 << 33), dict(xs=-C),
                dict(ba=NULL), dict(ba=ODD), dict(ba=P(0x1001), kind=1), dict(bs=15), dict(bs=1 << 33), dict(kind=2), dict(w=NULL),
                dict(w=P(0x1008)), dict(bias=P(0x1004)), dict(a=NULL), dict(a=ODD), dict(dt=NULL), dict(dt=ODD), dict(q=NULL),
-               dict(q=P((1 << 40) + 2)), dict(q=FAKE), dict(q=P(0x1000 + 16)), dict(x=FAR, q=P(0x1010))):  # the last over ba
+               dict(q=P((1 << 40) + 2)), dict(q=FAKE), dict(q=P(0x1000 + 16)), dict(x=FAR, q=P(0x1010)),  # the last over ba
+               dict(x=FAR, ba=FAR, q=P(0x1000 + 4096))):  # over the state
         assert go(**kw) == w12.W12_EINVAL, kw
 
 
@@ -75,7 +76,8 @@ def test_rule_arguments(w12):
         return L.w12_delta_rule(d, layer, seqs, NULL, off, rows, parent, q, scale, keep, out, NULL)
     for kw in (dict(layer=2), dict(seqs=0), dict(seqs=513), dict(off=NULL), dict(rows=0), dict(rows=97), dict(q=NULL), dict(q=ODD),
                dict(scale=float("nan")), dict(scale=float("inf")), dict(out=NULL), dict(out=P((1 << 40) + 8)), dict(out=FAKE),
-               dict(out=P(0x1000 + 4 * 4 * 64 * 2 - 16)), dict(keep=1, parent=FAKE)):
+               dict(out=P(0x1000 + 4 * 4 * 64 * 2 - 16)), dict(q=FAR, out=P(0x1000)), dict(q=FAR, out=P(0x1000 + (1 << 20))),
+               dict(keep=1, parent=FAKE)):
         assert go(**kw) == w12.W12_EINVAL, kw
 
 
@@ -85,7 +87,7 @@ def test_commit_arguments(w12):
     def go(seqs=2, off=FAKE, rows=4, acc=FAKE, path=NULL, kept=FAR):
         return L.w12_delta_commit(d, seqs, NULL, off, rows, acc, path, kept, NULL)
     for kw in (dict(seqs=0), dict(seqs=513), dict(off=NULL), dict(rows=0), dict(rows=97), dict(acc=NULL), dict(kept=NULL),
-               dict(kept=P(0x1004)), dict(acc=FAR, path=FAKE, kept=P(0x100C))):
+               dict(kept=P(0x1004)), dict(acc=FAR, path=FAKE, kept=P(0x100C)), dict(acc=FAR, kept=P(0x1000 + (1 << 20)))):
         assert go(**kw) == w12.W12_EINVAL, kw
 
 
@@ -102,7 +104,8 @@ def test_norm_arguments(w12):
                dict(scale=float("inf")), dict(h=P(0x2002)), dict(h=far, ht=3), dict(post=ODD), dict(weight=ODD), dict(eps=0.0),
                dict(eps=-1.0), dict(eps=float("nan")), dict(eps=float("inf")), dict(out=NULL), dict(out=P((1 << 40) + 1)),
                dict(out=FAKE), dict(out=P(0x1000 + 3 * 512 + 508)), dict(gate=FAR), dict(h=FAR), dict(h=FAKE),
-               dict(h=far, gate=P((1 << 40) + (1 << 30) + 256))):
+               dict(h=far, gate=P((1 << 40) + (1 << 30) + 256)), dict(post=FAR), dict(weight=P((1 << 40) + 1020)),
+               dict(h=far, weight=far), dict(h=far, post=P((1 << 40) + (1 << 30) + 2044))):
         assert go(**kw) == w12.W12_EINVAL, kw
 
 

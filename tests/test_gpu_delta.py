@@ -142,6 +142,26 @@ def test_rule_trees(w12, rows, tree):
     check_rule(Step(w12, rows, tree=tree, seed=rows[0]))
 
 
+RAGGED = [[70] + [2] * 9, [1] * 5 + [100] + [3] * 20, [60, 10, 20], [1, 40, 1, 90, 1], [2] * 80, [1] * 70 + [33], [0, 2, 1, 1], [0, 0, 4, 0]]
+
+
+@pytest.mark.parametrize("rows", RAGGED, ids=str)
+@pytest.mark.parametrize("tree", [None, "random", "line"])
+def test_rule_ragged(w12, rows, tree):
+    """Few long sequences among short ones, more than 64 of them, empty ones."""
+    check_rule(Step(w12, rows, 1, 2, tree=tree, seed=len(rows)), heads=(1,))
+    if tree is None:
+        check_rule(Step(w12, rows, 1, 2, seed=len(rows)), keep=True, heads=(0,))
+
+
+@pytest.mark.parametrize("rows", [[1] * 33, [0, 2] + [1] * 31, [20] * 9, [33, 3, 40, 17, 16, 31, 20, 18, 50]], ids=str)
+@pytest.mark.parametrize("kd,vd", [(128, 128), (64, 128), (128, 64)])
+def test_rule_many_heads(w12, rows, kd, vd):
+    """Enough sequences and heads for the forms that a full card takes."""
+    for keep in (False, True):
+        check_rule(Step(w12, rows, 4, 16, kd, vd, seed=kd + vd), keep=keep, heads=(0, 7, 15))
+
+
 @pytest.mark.parametrize("hk,hv", [(1, 1), (1, 3), (3, 3), (2, 6), (4, 4)])
 @pytest.mark.parametrize("kd,vd", [(64, 64), (64, 128), (128, 64), (128, 128)])
 @pytest.mark.parametrize("tree", [None, "random"])
@@ -178,7 +198,8 @@ def test_rule_decay_of_minus_infinity(w12):
     assert torch.equal(out[7:], late.rule()[7:])
 
 
-@pytest.mark.parametrize("rows,tree", [([12], "star"), ([40, 6], "random"), ([20], None), ([90], "random"), ([90], None)], ids=str)
+@pytest.mark.parametrize("rows,tree", [([12], "star"), ([40, 6], "random"), ([20], None), ([90], "random"), ([90], None),
+                                       ([50] + [2] * 9, "random"), ([50] + [2] * 9, None), ([8, 1, 1], None)], ids=str)
 @pytest.mark.parametrize("where", ["k", "v", "g", "beta", "q"])
 @pytest.mark.parametrize("value", [float("nan"), float("inf")])
 def test_rule_rows_that_are_no_numbers(w12, rows, tree, where, value):
@@ -211,6 +232,21 @@ def test_rule_rows_that_are_no_numbers(w12, rows, tree, where, value):
     assert bad.any()
 
 
+@pytest.mark.parametrize("rows", [[8, 1, 1], [40], [30] + [1] * 5], ids=str)
+def test_rule_kept_rows_that_are_no_numbers(w12, rows):
+    """They stay with their sequence's state, and their head."""
+    import torch
+    clean, st = Step(w12, rows, 2, 2, seed=43), Step(w12, rows, 2, 2, seed=43)
+    st.c.kv[0, 4, 2 * 128 + 5] = float("nan")  # a value of head 0
+    a, b = clean.rule(keep=True).view(-1, 2, 128), st.rule(keep=True).view(-1, 2, 128)
+    assert torch.equal(a[:4], b[:4]) and torch.equal(a[:, 1], b[:, 1]) and torch.isnan(b[4:rows[0], 0, 5]).all()
+    assert torch.equal(a[rows[0]:], b[rows[0]:])
+    s0 = int(st.slot[0])
+    assert torch.isnan(st.c.state[0, s0, 0, :, 5]).all() and torch.equal(st.c.state[0, s0, 1], clean.c.state[0, s0, 1])
+    rest = [i for i in range(st.slots) if i != s0]
+    assert torch.equal(st.c.state[0, rest], clean.c.state[0, rest]) and torch.equal(st.c.conv, clean.c.conv)
+
+
 def test_rule_refuses_on_the_device(w12):
     """Trees and slots that are none: NaN for that sequence, nothing else written."""
     import torch
@@ -228,6 +264,24 @@ def test_rule_refuses_on_the_device(w12):
         rest = torch.tensor([i for i in range(35) if not 9 <= i < 29], device=DEV)
         assert torch.isnan(b[9:29]).all() and torch.equal(a[rest], b[rest]), kind
         assert torch.equal(before[0, 9:29], st.c.delta[0, 9:29]) and torch.equal(before[0, 35:], st.c.delta[0, 35:])
+
+
+def test_rule_refuses_far_sequences(w12):
+    """Sequences past the 64th, and rows past the 64th of a tree."""
+    import torch
+    make = lambda: Step(w12, [1] * 70 + [100], 1, 2, tree="random", seed=44)  # noqa: E731
+    clean, st, bad = make(), make(), make()
+    a = clean.rule()
+    bad.parent[70 + 90] = 90
+    b = bad.rule()
+    assert torch.isnan(b[70:]).all() and torch.equal(a[:70], b[:70])
+    st.slot[68] = -1
+    b = st.rule()
+    assert torch.isnan(b[68]).all() and torch.equal(a[:68], b[:68]) and torch.equal(a[69:], b[69:])
+    keep = Step(w12, [1] * 70, 1, 2, seed=45)
+    keep.slot[69] = keep.slot[66]
+    b = keep.rule(keep=True)
+    assert torch.isnan(b[69]).all() and torch.isfinite(b[:69]).all()
 
 
 def test_rule_keeps_a_slot_once(w12):
@@ -372,8 +426,8 @@ def check_append(st, x, layer=0, **kw):
     return q
 
 
-@pytest.mark.parametrize("rows", [[1], [1, 1, 2], [3, 7], [33, 0, 1], [130]], ids=str)
-@pytest.mark.parametrize("tree", [None, "random", "star"])
+@pytest.mark.parametrize("rows", [[1], [1, 1, 2], [3, 7], [33, 0, 1], [130], [1] * 70 + [5, 0, 2], [66, 1, 70, 3]], ids=str)
+@pytest.mark.parametrize("tree", [None, "random", "star", "line"])
 @pytest.mark.parametrize("kind", ["f32", "bf16"])
 def test_append(w12, rows, tree, kind):
     st = Step(w12, rows, tree=tree, seed=21)
@@ -572,6 +626,41 @@ def test_commit_values_that_are_no_numbers(w12):
     for x in (st, clean):
         w12.w12_delta_commit(x.c, i32(x.off), i32([4]), path=i32(path), slot=i32(x.slot))
     assert torch.equal(st.c.state, clean.c.state) and torch.equal(st.c.conv, clean.c.conv)
+
+
+def test_commit_a_batch(w12):
+    """More than 64 sequences, one of them refused, one empty."""
+    st = Step(w12, [3] * 70 + [0, 2], 1, 1, 64, 64, tree="line", seed=46)
+    st.slot[69] = st.slots + 3
+    check_commit(st, [[0, 1]] * 35 + [[0]] * 35 + [[], [0, 1]], refused=(69,))
+
+
+def test_commit_and_append_in_graphs(w12):
+    """A captured step, replayed: every replay goes on from the state the one before left."""
+    import torch
+    eager, st = Step(w12, [9, 4], 2, 4, tree="random", seed=47), Step(w12, [9, 4], 2, 4, tree="random", seed=47)
+    x = Inputs(st, "bf16")
+    path = np.full(13, -1)
+    path[0], path[9:11] = 0, [0, 1]
+    fixed = [(i32(e.off), i32(e.slot), i32(e.parent), i32([0, 1]), i32(path)) for e in (eager, st)]
+
+    def step(e, off, slot, parent, acc, p, q, out):
+        w12.w12_delta_append(e.c, 0, x.qkv, x.ba, off, x.weight, x.a_log, x.dt, conv_bias=x.bias, slot=slot, parent=parent, out=q)
+        w12.w12_delta_rule(e.c, 0, q, off, slot=slot, parent=parent, out=out)
+        return w12.w12_delta_commit(e.c, off, acc, path=p, slot=slot)
+
+    bufs = [(torch.zeros(13, 2, 128, dtype=torch.bfloat16, device=DEV), torch.zeros(13, 512, dtype=torch.bfloat16, device=DEV)) for _ in range(2)]
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        kept = step(st, *fixed[1], *bufs[1])
+    for i in range(4):
+        want = step(eager, *fixed[0], *bufs[0])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert want.tolist() == kept.tolist() == [1, 2]
+        assert torch.equal(bufs[0][1], bufs[1][1]) and torch.equal(eager.c.state, st.c.state) and torch.equal(eager.c.conv, st.c.conv), i
+        eager.c.state.square().sum().item()
 
 
 # ---------------------------------------------------------------------------------------------- together

@@ -61,6 +61,15 @@ size_t span(int64_t rows, int64_t values, int64_t stride, int type) {
   return ((size_t)(rows - 1) * (size_t)stride + (size_t)values) * bytes_of(type);
 }
 
+// `bytes` at p meet none of the cache's arrays.
+bool apart_of(const w12::DeltaArgs& a, const void* p, size_t bytes) {
+  const size_t steps = (size_t)a.layers * a.step_rows, slots = (size_t)a.layers * a.slots;
+  return apart(p, bytes, a.state, slots * a.value_heads * a.key_dim * a.value_dim * 4) &&
+         apart(p, bytes, a.conv, slots * (a.width - 1) * a.channels * 2) && apart(p, bytes, a.raw, steps * a.channels * 2) &&
+         apart(p, bytes, a.kv, steps * a.kv_width * 2) && apart(p, bytes, a.gates, steps * 2 * a.value_heads * 4) &&
+         apart(p, bytes, a.delta, steps * a.value_heads * a.value_dim * 4);
+}
+
 }  // namespace
 
 extern "C" {
@@ -84,7 +93,7 @@ w12_status w12_delta_append(const w12_delta_cache* cache, int32_t layer, int32_t
     return W12_EINVAL;
   const size_t qb = (size_t)total_rows * a.c.key_heads * a.c.key_dim * 2;
   if (!apart(q, qb, qkv, span(total_rows, a.c.channels, qkv_stride, type)) ||
-      !apart(q, qb, ba, span(total_rows, 2 * a.c.value_heads, ba_stride, type)))
+      !apart(q, qb, ba, span(total_rows, 2 * a.c.value_heads, ba_stride, type)) || !apart_of(a.c, q, qb))
     return W12_EINVAL;
   a.st = {row_off, slot, parent, num_seq, total_rows};
   a.layer = layer;
@@ -110,9 +119,8 @@ w12_status w12_delta_rule(const w12_delta_cache* cache, int32_t layer, int32_t n
   if (!aligned(q, 16) || !aligned(out, 16)) return W12_EINVAL;
   w12::DeltaRuleArgs a{};
   a.c = args_of(cache);
-  if (!apart(q, (size_t)total_rows * a.c.key_heads * a.c.key_dim * 2, out,
-             (size_t)total_rows * a.c.value_heads * a.c.value_dim * 2))
-    return W12_EINVAL;
+  const size_t ob = (size_t)total_rows * a.c.value_heads * a.c.value_dim * 2;
+  if (!apart(q, (size_t)total_rows * a.c.key_heads * a.c.key_dim * 2, out, ob) || !apart_of(a.c, out, ob)) return W12_EINVAL;
   a.st = {row_off, slot, parent, num_seq, total_rows};
   a.layer = layer;
   a.q = q;
@@ -131,6 +139,7 @@ w12_status w12_delta_commit(const w12_delta_cache* cache, int32_t num_seq, const
     return W12_EINVAL;
   w12::DeltaCommitArgs a{};
   a.c = args_of(cache);
+  if (!apart_of(a.c, kept, (size_t)num_seq * 4)) return W12_EINVAL;
   a.st = {row_off, slot, nullptr, num_seq, total_rows};
   a.accept_len = accept_len;
   a.path = path;
@@ -155,6 +164,8 @@ w12_status w12_norm(int64_t rows, int32_t groups, int32_t width, const void* y, 
   if ((h && !apart(out, ob, h, hb)) || (y && !apart(out, ob, y, yb)) || (gate && !apart(out, ob, gate, gb)))
     return W12_EINVAL;
   if (h && ((y && !apart(h, hb, y, yb)) || (gate && !apart(h, hb, gate, gb)))) return W12_EINVAL;
+  for (const float* w : {post_weight, weight})
+    if (w && (!apart(out, ob, w, (size_t)width * 4) || (h && !apart(h, hb, w, (size_t)width * 4)))) return W12_EINVAL;
   w12::NormArgs a{};
   a.rows = rows;
   a.groups = groups;
