@@ -501,6 +501,83 @@ def run_step(args, w12, synth, torch, dev):
     print(json.dumps(line), flush=True)
 
 
+def run_recurrent(args, w12, synth, torch, dev):
+    """What the recurrent layers of a verify step do beside their products: per
+    layer the residual and norm before the block, the 32-node tree's inputs,
+    the gated delta rule, its heads' norm and gate, the residual and norm
+    behind; then the accepted path committed in all layers. 16 key and 48 value
+    heads of 128 x 128 (the 6144 of the layer shapes), every layer its own
+    state and rows; the projections' outputs are synthetic."""
+    import numpy as np
+
+    layers, hk, hv, dim = min(args.layers, 48), 16, 48, 128
+    cache = w12.delta_cache(layers, 1, hk, hv, dim, dim, 4, M_ROWS, device=dev)
+    cache.state.normal_(generator=torch.Generator(device=dev).manual_seed(8))
+    wide, inner = cache.channels + hv * dim + 2 * hv, hv * dim
+    proj = [synth.activations_bf16(M_ROWS, wide, seed=5_000_000 + li, device=dev) for li in range(layers)]
+    y = [synth.activations_bf16(M_ROWS, HIDDEN, seed=6_000_000 + li, device=dev) for li in range(layers)]
+    h = synth.activations_bf16(M_ROWS, HIDDEN, seed=7_000_000, device=dev).float()
+    gen = torch.Generator(device=dev).manual_seed(9)
+    conv = torch.randn(cache.channels, 4, generator=gen, device=dev) / 2
+    a_log, dt = torch.rand(hv, generator=gen, device=dev) * 2.7, torch.randn(hv, generator=gen, device=dev) - 3
+    w_head, w_norm = torch.ones(dim, device=dev), torch.ones(HIDDEN, device=dev)
+    i32 = lambda a: torch.tensor(np.asarray(a), dtype=torch.int32, device=dev)
+    rng = np.random.RandomState(10)
+    parent = np.array([-1] + [int(rng.randint(max(0, i - 4), i)) for i in range(1, M_ROWS)], np.int32)
+    path, node = [], M_ROWS - 1
+    while node >= 0:
+        path.append(node)
+        node = int(parent[node])
+    t_off, t_par, t_acc = i32([0, M_ROWS]), i32(parent), i32([len(path) - 1])
+    t_path = i32(path[::-1] + [-1] * (M_ROWS - len(path)))
+    q = torch.empty(M_ROWS, hk, dim, dtype=torch.bfloat16, device=dev)
+    out, x = (torch.empty(M_ROWS, n, dtype=torch.bfloat16, device=dev) for n in (inner, HIDDEN))
+    gated = torch.empty_like(out)
+
+    def launch(name, li=0):
+        if name == "APPEND":
+            w12.w12_delta_append(cache, li, proj[li][:, :cache.channels], proj[li][:, cache.channels + inner:], t_off, conv,
+                                 a_log, dt, parent=t_par, out=q)
+        elif name == "RULE":
+            w12.w12_delta_rule(cache, li, q, t_off, parent=t_par, out=out)
+        elif name == "GATED_NORM":
+            w12.w12_norm(out, post_weight=w_head, gate=proj[li][:, cache.channels:cache.channels + inner], groups=hv, out=gated)
+        elif name == "NORM":
+            w12.w12_norm(y[li], weight=w_norm, h=h, scale=0.1, out=x)
+        else:
+            w12.w12_delta_commit(cache, t_off, t_acc, path=t_path)
+
+    order = ["NORM", "APPEND", "RULE", "GATED_NORM", "NORM"]
+
+    def step():
+        for li in range(layers):
+            for name in order:
+                launch(name, li)
+        launch("COMMIT")
+
+    for _ in range(args.warmup):
+        step()
+    torch.cuda.synchronize()
+    us = time_events(lambda i: step(), args.steps)
+    assert bool(torch.isfinite(x.float()).all()) and bool(torch.isfinite(cache.state).all())
+    per = {}
+    for name in order[:4] + ["COMMIT"]:
+        n = layers if name != "COMMIT" else 1
+        launch(name)
+        per[name] = time_events(lambda i: [launch(name, li) for li in range(n)], max(2, args.steps)) / n
+    line = {
+        "metric": f"recurrent layers of a verify step beside their products: ms at M={M_ROWS} rows",
+        "value": round(us / 1000.0, 4), "unit": "ms", "n_gpus": 1, "steps": args.steps, "warmup": args.warmup,
+        "ms_per_step": round(us / 1000.0, 4), "higher_is_better": False, "scaling": "weak", "vs_baseline": None,
+        "dtype": "bf16", "data": "synthetic",
+        "config": {"workload": f"{layers} recurrent layers of {hk} key and {hv} value heads of {dim} x {dim}: norms, inputs, "
+                               "gated delta rule over one 32-node tree, heads' norm and gate, commit; no products",
+                   "rows": M_ROWS, "layers": layers, "accepted": len(path), "cache_bytes": cache.nbytes()},
+        "call_us": {k: round(v, 2) for k, v in per.items()},
+    }
+    print(json.dumps(line), flush=True)
+
+
 def main():
     ap = argparse.ArgumentParser(description=__doc__.split("\n")[0])
     ap.add_argument("--gpus", type=int, default=1)
@@ -515,7 +592,7 @@ def main():
     ap.add_argument("--graph", action="store_true", help="replay the step as a HIP graph")
     ap.add_argument("--copy-gib", type=float, default=1.0,
                     help="size of the calibration copy launched after timing (0 = none)")
-    ap.add_argument("--workload", choices=("pass", "block", "batched", "sweep", "qpass", "tree", "cert", "step"),
+    ap.add_argument("--workload", choices=("pass", "block", "batched", "sweep", "qpass", "tree", "cert", "step", "recurrent"),
                     default="pass",
                     help="pass: 64 layers + LM head argmax + tree acceptance at M=32 (the headline line); "
                          "block: the same with one layer; "
@@ -525,7 +602,8 @@ def main():
                          "qpass: one block + head through the Q pass (8-bit view only) next to the exact pass; "
                          "tree: best-first draft trees, 24 requests sharing 192 rows and one 32-row tree; "
                          "cert: the certified INT8 LM head next to the W12 head at M=32; "
-                         "step: the pass with its KV cache of --context tokens, sampled acceptance and commit")
+                         "step: the pass with its KV cache of --context tokens, sampled acceptance and commit; "
+                         "recurrent: what 48 recurrent layers do in a verify step beside their products")
     ap.add_argument("--context", type=int, default=8192,
                     help="committed tokens of the step workload (default 8192, at most 65536)")
     args = ap.parse_args()
@@ -548,7 +626,8 @@ def main():
     torch.cuda.set_device(dev)
     w12.lib()
     fn = {"pass": run_pass, "block": run_block, "batched": run_batched, "sweep": run_sweep,
-          "qpass": run_qpass, "tree": run_tree, "cert": run_cert, "step": run_step}[args.workload]
+          "qpass": run_qpass, "tree": run_tree, "cert": run_cert, "step": run_step,
+          "recurrent": run_recurrent}[args.workload]
     return fn(args, w12, synth, torch, dev)
 
 
