@@ -29,27 +29,8 @@ __global__ __launch_bounds__(kThreads, 3) void delta_commit_kernel(DeltaCommitAr
   const RowsView v = rows_view(a.c, a.st, seq);
   const int acc = a.accept_len[seq];
   float* state = a.c.state + state_at(a.c, layer, v.slot, head);
-  const auto place = [&]() {
-    const int lane = thread_now() & 63;
-    return (uint32_t)(4 * (lane >> 4) * VD + (wave * 16 + (lane & 15)) * NC);
-  };
   f32x4 S[KT][NC];
-  {
-    const uint32_t at = place();
-#pragma unroll
-    for (int t = 0; t < KT; ++t)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const float* p = state + (16 * t + r) * VD + at;
-        if constexpr (NC == 2) {
-          const float2 x = *reinterpret_cast<const float2*>(p);
-          S[t][0][r] = x.x;
-          S[t][1][r] = x.y;
-        } else {
-          S[t][0][r] = *p;
-        }
-      }
-  }
+  load_state<KT, VD, NC>(state, wave * 16 * NC, S);
   const int n = v.ok ? acc + 1 : 0;
   int bad = (!v.ok || acc < -1 || acc >= v.rows) ? 1 : 0;
   for (int j = tid; j < seq; j += kThreads) {
@@ -134,17 +115,7 @@ __global__ __launch_bounds__(kThreads, 3) void delta_commit_kernel(DeltaCommitAr
       }
     }
   }
-  const uint32_t at = place();
-#pragma unroll
-  for (int t = 0; t < KT; ++t)
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      float* p = state + (16 * t + r) * VD + at;
-      if constexpr (NC == 2)
-        *reinterpret_cast<float2*>(p) = make_float2(S[t][0][r], S[t][1][r]);
-      else
-        *p = S[t][0][r];
-    }
+  store_state<KT, VD, NC>(state, wave * 16 * NC, S);
 }
 
 }  // namespace

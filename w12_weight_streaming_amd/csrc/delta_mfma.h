@@ -17,6 +17,63 @@ __device__ __forceinline__ int thread_now() {
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
+// Reads and writes of states, which no call comes back to before others have
+// gone through the caches: past them, if the lane has two neighbouring dims (a
+// wave's 128 bytes a row are whole lines; of 64 bytes the caches join the halves).
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+template <int NC>
+__device__ __forceinline__ void read_dims(const float* p, float (&x)[NC]) {
+  if constexpr (NC == 2) {
+    const f32x2 y = __builtin_nontemporal_load(reinterpret_cast<const f32x2*>(p));
+    x[0] = y[0];
+    x[1] = y[1];
+  } else {
+    x[0] = *p;
+  }
+}
+template <int NC>
+__device__ __forceinline__ void write_dims(float* p, const float (&x)[NC]) {
+  if constexpr (NC == 2)
+    __builtin_nontemporal_store(f32x2{x[0], x[1]}, reinterpret_cast<f32x2*>(p));
+  else
+    *p = x[0];
+}
+
+// The NC * 16 columns of a head's state that a wave holds, from value dim vw,
+// NC neighbouring ones a lane, in the layout of the products: a uniform part of
+// each address, and the lane's in 32 bits.
+template <int VD, int NC>
+__device__ __forceinline__ uint32_t state_place(int vw) {
+  const int lane = thread_now() & 63;
+  return (uint32_t)(4 * (lane >> 4) * VD + vw + (lane & 15) * NC);
+}
+template <int KT, int VD, int NC>
+__device__ __forceinline__ void load_state(const float* state, int vw, f32x4 (&S)[KT][NC]) {
+  const uint32_t at = state_place<VD, NC>(vw);
+#pragma unroll
+  for (int t = 0; t < KT; ++t)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      float x[NC];
+      read_dims<NC>(state + (16 * t + r) * VD + at, x);
+#pragma unroll
+      for (int c = 0; c < NC; ++c) S[t][c][r] = x[c];
+    }
+}
+template <int KT, int VD, int NC>
+__device__ __forceinline__ void store_state(float* state, int vw, const f32x4 (&S)[KT][NC]) {
+  const uint32_t at = state_place<VD, NC>(vw);
+#pragma unroll
+  for (int t = 0; t < KT; ++t)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      float x[NC];
+#pragma unroll
+      for (int c = 0; c < NC; ++c) x[c] = S[t][c][r];
+      write_dims<NC>(state + (16 * t + r) * VD + at, x);
+    }
+}
+
 // Result layout of every product here, lane l of a wave: column l % 16, row
 // 4 (l / 16) + r in value r. An operand's depth is taken in the order (l / 16,
 // r) too, so a result serves as the next product's operand as it stands.

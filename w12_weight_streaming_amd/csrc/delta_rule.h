@@ -6,45 +6,6 @@
 
 namespace w12 {
 
-// The wave's NC * 16 columns of a head's state from value dim vw, NC neighbouring ones a lane, in
-// the layout of the products: a uniform part of each address, and the lane's in 32 bits.
-template <int VD, int NC>
-__device__ __forceinline__ uint32_t state_place(int vw) {
-  const int lane = thread_now() & 63;
-  return (uint32_t)(4 * (lane >> 4) * VD + vw + (lane & 15) * NC);
-}
-template <int KT, int VD, int NC>
-__device__ __forceinline__ void load_state(const float* state, int vw, f32x4 (&S)[KT][NC]) {
-  const uint32_t at = state_place<VD, NC>(vw);
-#pragma unroll
-  for (int t = 0; t < KT; ++t)
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const float* p = state + (16 * t + r) * VD + at;
-      if constexpr (NC == 2) {
-        const float2 x = *reinterpret_cast<const float2*>(p);
-        S[t][0][r] = x.x;
-        S[t][1][r] = x.y;
-      } else {
-        S[t][0][r] = *p;
-      }
-    }
-}
-template <int KT, int VD, int NC>
-__device__ __forceinline__ void store_state(float* state, int vw, const f32x4 (&S)[KT][NC]) {
-  const uint32_t at = state_place<VD, NC>(vw);
-#pragma unroll
-  for (int t = 0; t < KT; ++t)
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      float* p = state + (16 * t + r) * VD + at;
-      if constexpr (NC == 2)
-        *reinterpret_cast<float2*>(p) = make_float2(S[t][0][r], S[t][1][r]);
-      else
-        *p = S[t][0][r];
-    }
-}
-
 // A kept sequence's window, shared out among the workgroups of its heads.
 __device__ __forceinline__ void keep_window(const DeltaRuleArgs& a, const RowsView& v) {
   const int share = (a.c.channels + gridDim.x - 1) / gridDim.x;

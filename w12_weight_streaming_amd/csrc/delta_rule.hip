@@ -14,7 +14,7 @@
 // rows of a tree have no such state in common, and add what the rows of
 // earlier blocks on their path contribute, from the deltas those left.
 //
-// Value dims are independent of each other: a wave owns NC times 16 of them
+// Value dims are independent of each other: a wave owns 16 of them
 // and holds its columns of S0 in registers, in the layout of the products, so
 // states, deltas and results pass from one product into the next without
 // leaving the registers.
@@ -87,24 +87,24 @@ struct Staged {
 
 template <int KD, int VD, int RT, int kWaves>
 __global__ __launch_bounds__(64 * kWaves, RT == 1 ? 4 : RT == 2 ? 2 : 1) void delta_rule_kernel(DeltaRuleArgs a) {
-  constexpr int NC = 1, kThreads = 64 * kWaves;
+  constexpr int kThreads = 64 * kWaves;
   using Sh = Shared<KD, RT>;
   constexpr int R = Sh::R, KS = Sh::KS, TS = Sh::TS, KT = KD / 16;
   __shared__ Sh s;
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int hv = a.c.value_heads;
-  constexpr int slabs = VD / (kWaves * 16 * NC);
+  constexpr int slabs = VD / (kWaves * 16);
   const int head = blockIdx.x / slabs, key = head / (hv / a.c.key_heads), seq = blockIdx.y;
-  const int vw = (blockIdx.x - head * slabs) * (kWaves * 16 * NC) + wave * (16 * NC);  // the wave's first value dim
+  const int vw = (blockIdx.x - head * slabs) * (kWaves * 16) + wave * 16;  // the wave's first value dim
   const RowsView v = rows_view(a.c, a.st, seq);
   if (v.rows == 0) return;
   float* state = a.c.state + state_at(a.c, a.layer, v.slot, head);
-  f32x4 S[KT][NC];
+  f32x4 S[KT][1];
   // loads come back in order: what is needed before the state is read before it
   const Look seen = look(a, v);
   if (v.rows == 1) {
-    load_state<KT, VD, NC>(state, vw, S);
-    rows_in_turn<KD, VD, NC>(a, v, seq, head, key, vw, state, seen, S);
+    load_state<KT, VD, 1>(state, vw, S);
+    rows_in_turn<KD, VD, 1>(a, v, seq, head, key, vw, state, seen, S);
     return;
   }
   const bool chain = RT == 1 && !a.st.parent;
@@ -117,7 +117,7 @@ __global__ __launch_bounds__(64 * kWaves, RT == 1 ? 4 : RT == 2 ? 2 : 1) void de
     const uint16_t* kv = a.c.kv + kv_at(a.c, a.layer, row0);
     keys.load(kv + key * KD, a.c.kv_width, n);
     queries.load(a.q + ((size_t)row0 * a.c.key_heads + key) * KD, a.c.key_heads * KD, n);
-    const int lane = thread_now() & 63, g = lane >> 4, v0 = a.c.key_heads * KD + head * VD + vw + (lane & 15) * NC;
+    const int lane = thread_now() & 63, g = lane >> 4, v0 = a.c.key_heads * KD + head * VD + vw + (lane & 15);
 #pragma unroll
     for (int m = 0; m < RT; ++m)
 #pragma unroll
@@ -137,7 +137,7 @@ __global__ __launch_bounds__(64 * kWaves, RT == 1 ? 4 : RT == 2 ? 2 : 1) void de
     parent0 = a.st.parent ? a.st.parent[v.row0 + i] : i - 1;
   }
   fetch(0);
-  load_state<KT, VD, NC>(state, vw, S);
+  load_state<KT, VD, 1>(state, vw, S);
   for (int i = tid; i < kStepRows / R; i += kThreads) s.odd[i] = 0;
   if (tid == 0) s.odd_q = 0, s.bad = 0;
   __syncthreads();
@@ -203,7 +203,7 @@ __global__ __launch_bounds__(64 * kWaves, RT == 1 ? 4 : RT == 2 ? 2 : 1) void de
     if (b > 0) fetch(b);
     keys.store(n, s.k, KS, &s.odd[b]);
     queries.store(n, s.q, KS, &s.odd_q);
-    f32x4 rhs[RT][NC];
+    f32x4 rhs[RT];
     {
       const int lane = thread_now() & 63, g = lane >> 4;
       unsigned long long odd = 0;
@@ -215,7 +215,7 @@ __global__ __launch_bounds__(64 * kWaves, RT == 1 ? 4 : RT == 2 ? 2 : 1) void de
           const uint32_t x = values[m][r];
           const bool no = is_odd(odd_sum(x));
           if (no && i < n) odd |= 1ull << i;
-          rhs[m][0][r] = no || i >= n ? 0.0f : __uint_as_float(x << 16);
+          rhs[m][r] = no || i >= n ? 0.0f : __uint_as_float(x << 16);
         }
       if (odd) atomicOr(&s.odd[b], odd);
     }
@@ -268,30 +268,26 @@ __global__ __launch_bounds__(64 * kWaves, RT == 1 ? 4 : RT == 2 ? 2 : 1) void de
     }
 
     // the rows' products with the old state
-    f32x4 acc[RT][NC];
+    f32x4 acc[RT];
     {
       const int lane = thread_now() & 63, col = lane & 15, g = lane >> 4;
-      f32x4 w[RT][NC];
+      f32x4 w[RT];
 #pragma unroll
       for (int m = 0; m < RT; ++m)
-#pragma unroll
-        for (int c = 0; c < NC; ++c) w[m][c] = acc[m][c] = f32x4{0, 0, 0, 0};
+        w[m] = acc[m] = f32x4{0, 0, 0, 0};
 #pragma unroll
       for (int t = 0; t < KT; t += 2) {
-        uint4 piece[NC][3];
-#pragma unroll
-        for (int c = 0; c < NC; ++c) split3(S[t][c], S[t + 1][c], piece[c][0], piece[c][1], piece[c][2]);
+        uint4 piece[3];
+        split3(S[t][0], S[t + 1][0], piece[0], piece[1], piece[2]);
 #pragma unroll
         for (int m = 0; m < RT; ++m) {
           const uint4 fk = fragment(s.k + (16 * m + col) * KS + 16 * t + 4 * g);
           const uint4 fq = fragment(s.q + (16 * m + col) * KS + 16 * t + 4 * g);
 #pragma unroll
-          for (int p = 2; p >= 0; --p)
-#pragma unroll
-            for (int c = 0; c < NC; ++c) {
-              w[m][c] = mfma_bf16(fk, piece[c][p], w[m][c]);
-              acc[m][c] = mfma_bf16(fq, piece[c][p], acc[m][c]);
-            }
+          for (int p = 2; p >= 0; --p) {
+            w[m] = mfma_bf16(fk, piece[p], w[m]);
+            acc[m] = mfma_bf16(fq, piece[p], acc[m]);
+          }
         }
       }
 #pragma unroll
@@ -300,11 +296,8 @@ __global__ __launch_bounds__(64 * kWaves, RT == 1 ? 4 : RT == 2 ? 2 : 1) void de
         for (int r = 0; r < 4; ++r) {
           const int i = base + 16 * m + 4 * g + r;
           const float grow = s.grow[i], beta = s.beta[i];
-#pragma unroll
-          for (int c = 0; c < NC; ++c) {
-            rhs[m][c][r] = i < v.rows ? beta * (rhs[m][c][r] - grow * w[m][c][r]) : 0.0f;
-            acc[m][c][r] *= grow;
-          }
+          rhs[m][r] = i < v.rows ? beta * (rhs[m][r] - grow * w[m][r]) : 0.0f;
+          acc[m][r] *= grow;
         }
     }
 
@@ -312,7 +305,7 @@ __global__ __launch_bounds__(64 * kWaves, RT == 1 ? 4 : RT == 2 ? 2 : 1) void de
     if (!chain) {
       for (int e = b - 1; e >= 0; --e) {
         __syncthreads();
-        const int lane = thread_now() & 63, col = lane & 15, g = lane >> 4, v0 = vw + col * NC;
+        const int lane = thread_now() & 63, col = lane & 15, g = lane >> 4, v0 = vw + col;
         keys.load(a.c.kv + kv_at(a.c, a.layer, v.row0 + e * R) + key * KD, a.c.kv_width, R);
         keys.store(R, s.t, KS, &s.odd[e]);
         if (tid < R) {
@@ -345,40 +338,35 @@ __global__ __launch_bounds__(64 * kWaves, RT == 1 ? 4 : RT == 2 ? 2 : 1) void de
         const float* deltas = a.c.delta + delta_at(a.c, a.layer, v.row0 + e * R, head);  // as this lane wrote them
 #pragma unroll
         for (int mj = 0; mj < RT; ++mj) {
-          f32x4 d[NC];
+          f32x4 d;
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             const int j = 16 * mj + 4 * g + r;
             const float* p = deltas + ((uint32_t)j * hv * VD + v0);
-#pragma unroll
-            for (int c = 0; c < NC; ++c) d[c][r] = (odd >> j) & 1 ? 0.0f : p[c];
+            d[r] = (odd >> j) & 1 ? 0.0f : *p;
           }
 #pragma unroll
-          for (int m = 0; m < RT; ++m)
-#pragma unroll
-            for (int c = 0; c < NC; ++c) {
-              rhs[m][c] = mfma_f32(s.far_low[m * RT + mj][lane], d[c], rhs[m][c]);
-              acc[m][c] = mfma_f32(s.far_see[m * RT + mj][lane], d[c], acc[m][c]);
-            }
+          for (int m = 0; m < RT; ++m) {
+            rhs[m] = mfma_f32(s.far_low[m * RT + mj][lane], d, rhs[m]);
+            acc[m] = mfma_f32(s.far_see[m * RT + mj][lane], d, acc[m]);
+          }
         }
       }
     }
     __syncthreads();
 
     // the triangular system, and the outputs
-    const int lane = thread_now() & 63, col = lane & 15, g = lane >> 4, v0 = vw + col * NC;
+    const int lane = thread_now() & 63, col = lane & 15, g = lane >> 4, v0 = vw + col;
 #pragma unroll
-    for (int m = 0; m < RT; ++m)
+    for (int m = 0; m < RT; ++m) {
+      f32x4 d = mfma_f32(s.inv[m][lane], rhs[m], f32x4{0, 0, 0, 0});
+      rhs[m] = d;
 #pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        f32x4 d = mfma_f32(s.inv[m][lane], rhs[m][c], f32x4{0, 0, 0, 0});
-        rhs[m][c] = d;
-#pragma unroll
-        for (int i = 0; i < RT; ++i) {
-          if (i > m) rhs[i][c] = mfma_f32(s.low[i * RT + m][lane], d, rhs[i][c]);
-          if (i >= m) acc[i][c] = mfma_f32(s.see[i * RT + m][lane], d, acc[i][c]);
-        }
+      for (int i = 0; i < RT; ++i) {
+        if (i > m) rhs[i] = mfma_f32(s.low[i * RT + m][lane], d, rhs[i]);
+        if (i >= m) acc[i] = mfma_f32(s.see[i * RT + m][lane], d, acc[i]);
       }
+    }
     const unsigned long long odd = s.odd[b], odd_q = s.odd_q;
     uint16_t* outs = a.out + ((size_t)row0 * hv + head) * VD;
     float* deltas = a.c.delta + delta_at(a.c, a.layer, row0, head);
@@ -390,8 +378,8 @@ __global__ __launch_bounds__(64 * kWaves, RT == 1 ? 4 : RT == 2 ? 2 : 1) void de
       for (int r = 0; r < 4; ++r) {
         const int i = 16 * m + 4 * g + r;
         const uint32_t at = at0 + (16 * m + r) * step;
-        uint16_t o = (uint16_t)bf16_pair(a.scale * acc[m][0][r], 0.0f);
-        float d = rhs[m][0][r];
+        uint16_t o = (uint16_t)bf16_pair(a.scale * acc[m][r], 0.0f);
+        float d = rhs[m][r];
         if (!plain) {
           const bool no = before || (s.in[base + i] & odd) || (!chain && s.behind[i]);
           if (no || ((odd_q >> i) & 1)) o = 0x7FC0;
@@ -416,25 +404,18 @@ __global__ __launch_bounds__(64 * kWaves, RT == 1 ? 4 : RT == 2 ? 2 : 1) void de
         if (tid < R) s.part[tid] = tid < n ? expf((float)(s.sum[base + n - 1] - s.sum[base + tid])) : 0.0f;
         __syncthreads();
         const float keep = s.grow[base + n - 1];
-        uint4 piece[NC][3];
+        uint4 piece[3];
+        f32x4 y;
 #pragma unroll
-        for (int c = 0; c < NC; ++c) {
-          f32x4 x;
-#pragma unroll
-          for (int r = 0; r < 4; ++r) x[r] = s.part[4 * g + r] * rhs[0][c][r];
-          split3(x, f32x4{0, 0, 0, 0}, piece[c][0], piece[c][1], piece[c][2]);
-        }
+        for (int r = 0; r < 4; ++r) y[r] = s.part[4 * g + r] * rhs[0][r];
+        split3(y, f32x4{0, 0, 0, 0}, piece[0], piece[1], piece[2]);
 #pragma unroll
         for (int t = 0; t < KT; ++t) {
           const uint2 x = *reinterpret_cast<const uint2*>(s.t + (16 * t + col) * TS + 4 * g);
           const uint4 f = make_uint4(x.x, x.y, 0, 0);
+          S[t][0] *= keep;
 #pragma unroll
-          for (int c = 0; c < NC; ++c) {
-#pragma unroll
-            for (int r = 0; r < 4; ++r) S[t][c][r] *= keep;
-#pragma unroll
-            for (int p = 2; p >= 0; --p) S[t][c] = mfma_bf16(f, piece[c][p], S[t][c]);
-          }
+          for (int p = 2; p >= 0; --p) S[t][0] = mfma_bf16(f, piece[p], S[t][0]);
         }
       }
     }
@@ -443,10 +424,9 @@ __global__ __launch_bounds__(64 * kWaves, RT == 1 ? 4 : RT == 2 ? 2 : 1) void de
     if (before) {
 #pragma unroll
       for (int t = 0; t < KT; ++t)
-#pragma unroll
-        for (int c = 0; c < NC; ++c) S[t][c] = f32x4{__builtin_nanf(""), __builtin_nanf(""), __builtin_nanf(""), __builtin_nanf("")};
+        S[t][0] = f32x4{__builtin_nanf(""), __builtin_nanf(""), __builtin_nanf(""), __builtin_nanf("")};
     }
-    store_state<KT, VD, NC>(state, vw, S);
+    store_state<KT, VD, 1>(state, vw, S);
     keep_window(a, v);
   }
 }
