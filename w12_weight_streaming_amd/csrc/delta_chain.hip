@@ -49,8 +49,8 @@ __device__ __forceinline__ void fetch(const uint16_t* kv, int kv_step, const uin
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int at = min(r + i, last);
-    x.k[i] = *reinterpret_cast<const uint4*>(kv + (__umul24(at, kv_step) + c));
-    x.q[i] = *reinterpret_cast<const uint4*>(q + (__umul24(at, q_step) + c));
+    x.k[i] = *reinterpret_cast<const uint4*>(behind(kv, 2 * (__umul24(at, kv_step) + c)));
+    x.q[i] = *reinterpret_cast<const uint4*>(behind(q, 2 * (__umul24(at, q_step) + c)));
   }
 }
 
@@ -178,7 +178,7 @@ __global__ __launch_bounds__(64 * (kMakers + kTakers)) __attribute__((amdgpu_wav
         if (mw < 2) {
           tile<KD>(s, o, b * R, true, mw);
           wave_lds_sync();
-          invert(o.low[mw], o.inv[mw], v.rows - b * R - 16 * mw);
+          invert<true>(o.low[mw], o.inv[mw], 16);
         } else {
           tile<KD>(s, o, b * R, mw == 2, 2);
           tile<KD>(s, o, b * R, false, mw - 2);
@@ -199,7 +199,7 @@ __global__ __launch_bounds__(64 * (kMakers + kTakers)) __attribute__((amdgpu_wav
       for (int m = 0; m < 2; ++m)
 #pragma unroll
         for (int r = 0; r < 4; ++r)
-          val[m][r] = values[__umul24(min(first + 16 * m + 4 * (lane >> 4) + r, v.rows - 1), a.c.kv_width) + (lane & 15)];
+          val[m][r] = *behind(values, 2 * (__umul24(min(first + 16 * m + 4 * (lane >> 4) + r, v.rows - 1), a.c.kv_width) + (lane & 15)));
     };
     fetch_values(0);
     __syncthreads();
@@ -271,12 +271,12 @@ __global__ __launch_bounds__(64 * (kMakers + kTakers)) __attribute__((amdgpu_wav
       }
       __syncthreads();
       // the triangular system, the state behind the block, the outputs
-      const f32x4 zero = {0, 0, 0, 0};
       const f32x4 inv0 = o.inv[0][lane], inv1 = o.inv[1][lane], low2 = o.low[2][lane];
       const f32x4 see0 = o.see[0][lane], see1 = o.see[1][lane], see2 = o.see[2][lane];
       uint4 ft[KT];
 #pragma unroll
       for (int t = 0; t < KT; ++t) ft[t] = fragment(o.t + (16 * t + col) * B::TS + 4 * g);
+      const f32x4 zero = {0, 0, 0, 0};
       const f32x4 d0 = mfma_f32(inv0, rhs[0], zero);
       const f32x4 d1 = mfma_f32(inv1, mfma_f32(low2, d0, rhs[1]), zero);
       acc[0] = mfma_f32(see0, d0, acc[0]);
@@ -305,8 +305,8 @@ __global__ __launch_bounds__(64 * (kMakers + kTakers)) __attribute__((amdgpu_wav
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             const uint32_t at = at0 + (16 * m + r) * step;
-            outs[at] = (uint16_t)bf16_pair(a.scale * acc[m][r], 0.0f);
-            if (!a.keep) deltas[at] = m ? d1[r] : d0[r];
+            *behind(outs, 2 * at) = (uint16_t)bf16_pair(a.scale * acc[m][r], 0.0f);
+            if (!a.keep) *behind(deltas, 4 * at) = m ? d1[r] : d0[r];
           }
       } else {
 #pragma unroll

@@ -2,6 +2,8 @@
 // times keys and queries (bf16) in three bf16 pieces.
 #pragma once
 
+#include <type_traits>
+
 #include "delta_internal.h"
 #include "w12_device.h"
 
@@ -16,6 +18,14 @@ __device__ __forceinline__ int thread_now() {
 }
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+// `bytes` behind a uniform address: in this form the address stays in scalar
+// registers and the lane's part in one vector register.
+template <typename T>
+__device__ __forceinline__ T* behind(T* base, uint32_t bytes) {
+  using Byte = std::conditional_t<std::is_const_v<T>, const char, char>;
+  return reinterpret_cast<T*>(reinterpret_cast<Byte*>(base) + bytes);
+}
 
 // Reads and writes of states, which no call comes back to before others have
 // gone through the caches: past them, if the lane has two neighbouring dims (a
@@ -45,7 +55,7 @@ __device__ __forceinline__ void write_dims(float* p, const float (&x)[NC]) {
 template <int VD, int NC>
 __device__ __forceinline__ uint32_t state_place(int vw) {
   const int lane = thread_now() & 63;
-  return (uint32_t)(4 * (lane >> 4) * VD + vw + (lane & 15) * NC);
+  return (uint32_t)(4 * (4 * (lane >> 4) * VD + vw + (lane & 15) * NC));  // in bytes
 }
 template <int KT, int VD, int NC>
 __device__ __forceinline__ void load_state(const float* state, int vw, f32x4 (&S)[KT][NC]) {
@@ -55,7 +65,7 @@ __device__ __forceinline__ void load_state(const float* state, int vw, f32x4 (&S
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       float x[NC];
-      read_dims<NC>(state + (16 * t + r) * VD + at, x);
+      read_dims<NC>(behind(state + (16 * t + r) * VD, at), x);
 #pragma unroll
       for (int c = 0; c < NC; ++c) S[t][c][r] = x[c];
     }
@@ -70,7 +80,7 @@ __device__ __forceinline__ void store_state(float* state, int vw, const f32x4 (&
       float x[NC];
 #pragma unroll
       for (int c = 0; c < NC; ++c) x[c] = S[t][c][r];
-      write_dims<NC>(state + (16 * t + r) * VD + at, x);
+      write_dims<NC>(behind(state + (16 * t + r) * VD, at), x);
     }
 }
 
@@ -142,9 +152,10 @@ __device__ __forceinline__ f32x4 pair_tile(const uint16_t* x, const uint16_t* k,
 
 // (I + L)^-1 of a diagonal tile from -L, a column per lane of the first 16, by
 // forward substitution: L's products of keys make it as well conditioned as the
-// rule itself, where powers of L would cancel. Rows past n hold nothing, and
-// eight of them cost half a tile's time; rows of L are read eight and four at a
-// time (all at once take 160 registers).
+// rule itself, where powers of L would cancel. Wide: all rows of L are read at
+// once, into 144 registers, and each value goes into all the sums that wait
+// for it (900 cycles); else rows a few at a time, each value's sum at once (2000),
+// and tiles of up to eight rows stop there.
 template <int First, int Last>
 __device__ __forceinline__ void substitute(const f32x4* low, int c, float (&x)[16]) {
 #pragma unroll
@@ -163,16 +174,33 @@ __device__ __forceinline__ void substitute(const f32x4* low, int c, float (&x)[1
   }
   __builtin_amdgcn_sched_barrier(0);
 }
+template <bool Wide>
 __device__ __forceinline__ void invert(const f32x4* low, f32x4* inv, int n) {
   const int lane = thread_now() & 63, c = lane & 15;
   float x[16];
-  substitute<0, 8>(low, c, x);
-  if (n > 8) {  // the same for all lanes
-    substitute<8, 12>(low, c, x);
-    substitute<12, 16>(low, c, x);
-  } else {
+  if constexpr (Wide) {
+    f32x4 l[16][4];
 #pragma unroll
-    for (int i = 8; i < 16; ++i) x[i] = i == c ? 1.0f : 0.0f;
+    for (int i = 1; i < 16; ++i)
+#pragma unroll
+      for (int g = 0; g < 4; ++g)
+        if (4 * g < i) l[i][g] = low[g * 16 + i];
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] = i == c ? 1.0f : 0.0f;
+#pragma unroll
+    for (int j = 0; j < 15; ++j)
+#pragma unroll
+      for (int i = j + 1; i < 16; ++i) x[i] += l[i][j >> 2][j & 3] * x[j];
+  } else {
+    substitute<0, 8>(low, c, x);
+    if (n > 8) {  // the same for all lanes
+      substitute<8, 12>(low, c, x);
+      substitute<12, 16>(low, c, x);
+    } else {
+#pragma unroll
+      for (int i = 8; i < 16; ++i) x[i] = i == c ? 1.0f : 0.0f;
+    }
   }
   if (lane < 16) {
     float* o = reinterpret_cast<float*>(inv);

@@ -68,7 +68,7 @@ struct Staged {
 #pragma unroll
     for (int i = 0; i < kTurns; ++i) {
       const int e = tid + i * kThreads;
-      x[i] = *reinterpret_cast<const uint4*>(from + (__umul24(min(e / kChunks, n - 1), step) + (e % kChunks) * 8));
+      x[i] = *reinterpret_cast<const uint4*>(behind(from, 2 * (__umul24(min(e / kChunks, n - 1), step) + (e % kChunks) * 8)));
     }
   }
   __device__ __forceinline__ void store(int n, uint16_t* to, int stride, unsigned long long* odd) {
@@ -122,7 +122,7 @@ __global__ __launch_bounds__(64 * kWaves, RT == 1 ? 4 : RT == 2 ? 2 : 1) void de
     for (int m = 0; m < RT; ++m)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const uint16_t* p = kv + (__umul24(min(16 * m + 4 * g + r, n - 1), a.c.kv_width) + v0);
+        const uint16_t* p = behind(kv, 2 * (__umul24(min(16 * m + 4 * g + r, n - 1), a.c.kv_width) + v0));
         values[m][r] = *p;
       }
   };
@@ -259,7 +259,7 @@ __global__ __launch_bounds__(64 * kWaves, RT == 1 ? 4 : RT == 2 ? 2 : 1) void de
       if (item < RT) {
         tile(true, item, item);
         wave_lds_sync();
-        invert(s.low[item * RT + item], s.inv[item], n - 16 * item);
+        invert<(RT > 1)>(s.low[item * RT + item], s.inv[item], n - 16 * item);
       } else if (item < RT + RT * RT) {
         const int i = (item - RT) / RT, j = (item - RT) % RT;
         tile(j > i, max(i, j), min(i, j));
@@ -386,8 +386,8 @@ __global__ __launch_bounds__(64 * kWaves, RT == 1 ? 4 : RT == 2 ? 2 : 1) void de
           if (no) d = __builtin_nanf("");
         }
         if (i < n) {
-          outs[at] = o;
-          if (!a.keep) deltas[at] = d;
+          *behind(outs, 2 * at) = o;
+          if (!a.keep) *behind(deltas, 4 * at) = d;
         }
       }
 
