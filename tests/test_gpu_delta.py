@@ -154,12 +154,13 @@ def test_rule_ragged(w12, rows, tree):
         check_rule(Step(w12, rows, 1, 2, seed=len(rows)), keep=True, heads=(0,))
 
 
-@pytest.mark.parametrize("rows", [[1] * 33, [0, 2] + [1] * 31, [20] * 9, [33, 3, 40, 17, 16, 31, 20, 18, 50]], ids=str)
+@pytest.mark.parametrize("rows", [[1] * 33, [0, 2] + [1] * 31, [20] * 9, [33, 3, 40, 17, 16, 31, 20, 18, 50], [20] * 20, [40, 60, 3, 70, 50, 65, 33, 66, 40]], ids=str)
 @pytest.mark.parametrize("kd,vd", [(128, 128), (64, 128), (128, 64)])
 def test_rule_many_heads(w12, rows, kd, vd):
     """Enough sequences and heads for the forms that a full card takes."""
     for keep in (False, True):
-        check_rule(Step(w12, rows, 4, 16, kd, vd, seed=kd + vd), keep=keep, heads=(0, 7, 15))
+        check_rule(Step(w12, rows, 4, 16, kd, vd, seed=kd + vd), keep=keep, heads=(0, 15))
+    check_rule(Step(w12, rows, 4, 16, kd, vd, tree="random", seed=kd + vd), heads=(7,))
 
 
 @pytest.mark.parametrize("hk,hv", [(1, 1), (1, 3), (3, 3), (2, 6), (4, 4)])

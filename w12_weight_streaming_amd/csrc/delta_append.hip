@@ -1,6 +1,11 @@
 // Inputs of a recurrent layer's rows (gfx950): the short causal convolution
 // along each row's root path, SiLU, normalised query and key heads, and the
 // decay and strength of every value head.
+//
+// Each input is read once by its own row and up to three times more, from the
+// caches, by the rows behind it; outputs are written once. Bound by latency at
+// few rows (the row's sequence, then its parents, then their inputs): 32 rows of
+// 10240 channels 5.5 us. 512 fp32 rows 15.5 us for 42 MB (2.7 TB/s).
 #include "delta_internal.h"
 #include "w12_device.h"
 
@@ -200,10 +205,13 @@ __global__ __launch_bounds__(kThreads) void delta_append_kernel(DeltaAppendArgs 
   }
 }
 
+// Rows a workgroup: one leaves more of them to hide each other's waits, four read
+// the weights and hand on chains' inputs for four: 128 rows 7.1 us against 8.3,
+// 256 rows 10.8 against 9.9, 512 fp32 rows 22 against 15.5.
 template <int W>
 void launch(const DeltaAppendArgs& a, hipStream_t s) {
   const int parts = (a.c.channels + kThreads * kPer - 1) / (kThreads * kPer) + 1;
-  if (a.st.total <= 64)
+  if (a.st.total <= 128)
     delta_append_kernel<W, 1><<<dim3(a.st.total, parts), kThreads, 0, s>>>(a);
   else
     delta_append_kernel<W, 4><<<dim3((a.st.total + 3) / 4, parts), kThreads, 0, s>>>(a);

@@ -6,7 +6,10 @@
 // one pass over the state with no product that depends on another. Bound by
 // the state's bytes, read and written once: a workgroup holds one head's state
 // in registers and adds 32 rows at a time on the matrix cores (most paths are
-// one turn), keys as they are (bf16), weighted deltas in three bf16 pieces.
+// one turn), keys as they are (bf16), weighted deltas in three bf16 pieces. 48
+// layers of 48 heads of 128 x 128, one sequence: 63 us for 303 MB (4.8 TB/s);
+// 12 layers of 24 sequences 330 us for 1.83 GB (5.5 TB/s). With the states' traffic
+// through the caches 77 and 389.
 #include "delta_mfma.h"
 
 namespace w12 {

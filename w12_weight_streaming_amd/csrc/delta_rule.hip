@@ -23,6 +23,14 @@
 // enters a bf16 product as three bf16 pieces, each the top of what the one
 // before left, which hold all its 24 bits; products of two fp32 factors (L and
 // D (q . k) with deltas) run on the fp32 matrix core. Sums of g are held in 64 bits.
+//
+// Bound by the state's bytes where there are many sequences: 24 x 8 rows, 16 key
+// and 48 value heads of 128 x 128, 24.5 us for 99 MB (4.0 TB/s), 32 x 1 41 us for 202 MB
+// read and written (4.9 TB/s); by latency where there are few: one 32-row tree
+// takes 9.0 us, about 1.5 of them until a sequence's rows and slot are there,
+// 2 for the loads behind those, 2.5 for tiles and inverses, 1 for the products.
+// A workgroup's code runs once, so its instructions are fetched as it goes:
+// loops of few instructions beat unrolled ones outside the state's registers.
 #include "delta_mfma.h"
 #include "delta_rule.h"
 
@@ -449,23 +457,35 @@ __global__ __launch_bounds__(kDecodeThreads, 4) void delta_decode_kernel(DeltaRu
   rows_in_turn<KD, VD, NC>(a, v, seq, head, key, vw, state, seen, S);
 }
 
+// Which form: by the rows a sequence has on average (their numbers are on the
+// device) and by the workgroups there are. In us, 16 key and 48 value heads of
+// 128 x 128, sequences x rows, states rotated past the caches for single rows:
+//   single rows, 32 value dims a wave (past the caches) against 16: 1 x 1 7.6 / 6.6,
+//     2 x 1 7.8 / 7.1, 3 x 1 8.1 / 9.7, 8 x 1 14.0 / 17.8, 32 x 1 42.3 / 52.0.
+//   trees, blocks of 16 / 32 / 64 rows: 24 x 8 24.0 / 38.2 / 99.9, 1 x 16 7.9 / 8.1 /
+//     13.2, 1 x 24 13.9 / 8.5 / 13.5, 6 x 32 20.0 / 17.1 / 37.7, 1 x 64 32.9 / 17.7 / 15.2,
+//     3 x 64 33.4 / 20.7 / 27.1 (a CU holds one workgroup of the last).
+//   chains, delta_chain.hip against blocks of 16: 1 x 16 9.0 / 10.0, 8 x 8 27.3 / 14.6,
+//     1 x 64 11.2 / 27.3, 4 x 32 17.5 / 17.5, 6 x 32 26.0 / 23.4, 8 x 48 38.3 / 32.9, 8 x 64
+//     37.7 / 39.6, 4 x 128 35.0 / 52.7, 16 x 32 58.2 / 40.7.
 template <int KD, int VD>
 hipError_t launch(const DeltaRuleArgs& a, hipStream_t s) {
   const int rows = (a.st.total + a.st.num_seq - 1) / a.st.num_seq;
-  const dim3 grid(a.c.value_heads * (VD / 64), a.st.num_seq);
+  const int heads = a.c.value_heads * a.st.num_seq, groups = heads * (VD / 64);  // of 64 value dims
+  const dim3 grid(a.c.value_heads * (VD / 64), a.st.num_seq), whole(a.c.value_heads, a.st.num_seq);
   if (rows == 1 && !a.st.parent) {
     if constexpr (VD == 128) {
-      if (a.c.value_heads * a.st.num_seq >= 512) {
-        delta_decode_kernel<KD, VD, 2><<<dim3(a.c.value_heads, a.st.num_seq), kDecodeThreads, 0, s>>>(a);
+      if (heads >= 128) {
+        delta_decode_kernel<KD, VD, 2><<<whole, kDecodeThreads, 0, s>>>(a);
         return hipGetLastError();
       }
     }
     delta_decode_kernel<KD, VD, 1><<<grid, kDecodeThreads, 0, s>>>(a);
-  } else if (rows <= 16) {
-    delta_rule_kernel<KD, VD, 1, VD / 16><<<dim3(a.c.value_heads, a.st.num_seq), VD * 4, 0, s>>>(a);
+  } else if (rows <= 16 || (!a.st.parent && rows < 64 && groups > 384)) {
+    delta_rule_kernel<KD, VD, 1, VD / 16><<<whole, VD * 4, 0, s>>>(a);
   } else if (!a.st.parent) {
     return launch_delta_chain(a, s);
-  } else if (rows <= 32) {
+  } else if (rows <= 32 || groups > 256) {
     delta_rule_kernel<KD, VD, 2, 4><<<grid, 256, 0, s>>>(a);
   } else {
     delta_rule_kernel<KD, VD, 4, 4><<<grid, 256, 0, s>>>(a);

