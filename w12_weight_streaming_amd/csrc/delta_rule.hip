@@ -25,7 +25,7 @@
 // D (q . k) with deltas) run on the fp32 matrix core. Sums of g are held in 64 bits.
 //
 // Bound by the state's bytes where there are many sequences: 24 x 8 rows, 16 key
-// and 48 value heads of 128 x 128, 24.5 us for 99 MB (4.0 TB/s), 32 x 1 41 us for 202 MB
+// and 48 value heads of 128 x 128, 24.5 us for 85 MB (3.5 TB/s), 32 x 1 41 us for 202 MB
 // read and written (4.9 TB/s); by latency where there are few: one 32-row tree
 // takes 9.0 us, about 1.5 of them until a sequence's rows and slot are there,
 // 2 for the loads behind those, 2.5 for tiles and inverses, 1 for the products.
