@@ -248,6 +248,47 @@ def test_rule_kept_rows_that_are_no_numbers(w12, rows):
     assert torch.equal(st.c.state[0, rest], clean.c.state[0, rest]) and torch.equal(st.c.conv, clean.c.conv)
 
 
+@pytest.mark.parametrize("rows", [[1] * 5, [9, 2], [40], [30] + [1] * 5], ids=str)
+def test_rule_queries_that_are_no_numbers_leave_the_state(w12, rows):
+    import torch
+    clean, st = Step(w12, rows, 1, 2, seed=48), Step(w12, rows, 1, 2, seed=48)
+    st.q[0, 0, 7] = float("inf")
+    a, b = clean.rule(keep=True), st.rule(keep=True)
+    assert torch.equal(a[1:], b[1:]) and not torch.isfinite(b[0]).any() and torch.equal(clean.c.state, st.c.state)
+
+
+def test_two_steps_in_flight(w12):
+    """Two descriptions over the same state and window, each with its step's arrays and its own stream."""
+    import torch
+    one, two = Step(w12, [20, 7, 1], 2, 4, seed=49, slots=8), Step(w12, [5, 40], 2, 4, seed=50, slots=8)
+    one.slot, two.slot = np.array([0, 3, 6]), np.array([5, 1])
+    c = two.c
+    two.c = w12.DeltaCache(state=one.c.state, conv=one.c.conv, raw=c.raw, kv=c.kv, gates=c.gates, delta=c.delta, key_heads=2)
+    state, conv = one.c.state.clone(), one.c.conv.clone()
+    xs = [Inputs(one, seed=1), Inputs(two, seed=2)]
+    fixed = [dict(off=i32(s.off), slot=i32(s.slot), acc=i32([n - 1 for n in s.rows])) for s in (one, two)]
+
+    def step(st, x, f):
+        q = w12.w12_delta_append(st.c, 0, x.qkv, x.ba, f["off"], x.weight, x.a_log, x.dt, slot=f["slot"])
+        out = w12.w12_delta_rule(st.c, 0, q, f["off"], slot=f["slot"])
+        w12.w12_delta_commit(st.c, f["off"], f["acc"], slot=f["slot"], rows=st.total)
+        return out
+
+    want = [step(st, x, f) for st, x, f in zip((one, two), xs, fixed)]
+    after = one.c.state.clone(), one.c.conv.clone()
+    for _ in range(3):
+        one.c.state.copy_(state)
+        one.c.conv.copy_(conv)
+        torch.cuda.synchronize()
+        streams, got = [torch.cuda.Stream() for _ in range(2)], []
+        for s, st, x, f in zip(streams, (one, two), xs, fixed):
+            with torch.cuda.stream(s):
+                got.append(step(st, x, f))
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
+        assert torch.equal(after[0], one.c.state) and torch.equal(after[1], one.c.conv)
+
+
 def test_rule_refuses_on_the_device(w12):
     """Trees and slots that are none: NaN for that sequence, nothing else written."""
     import torch

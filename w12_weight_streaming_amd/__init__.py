@@ -6,9 +6,10 @@ names as the C entry points: w12_pack, w12_decode, w12_check, w12_gemm,
 w12_head_argmax, tree_accept, and for the pass's KV cache and sampling
 requests w12_kv_append, w12_kv_attention, w12_kv_commit and
 tree_accept_sampled; for its recurrent layers w12_delta_append,
-w12_delta_rule and w12_delta_commit, and w12_norm between products. Every step of the path runs in the library's
-HIP kernels; this module only checks tensor dtypes/devices, passes device
-pointers and the current HIP stream, and keeps zero-filled workspaces.
+w12_delta_rule and w12_delta_commit, and w12_norm between products. Every
+step of the path runs in the library's HIP kernels; this module only checks
+tensor dtypes/devices, passes device pointers and the current HIP stream, and
+keeps zero-filled workspaces.
 There is no CPU fallback: without the built library every call raises.
 """
 from __future__ import annotations
@@ -464,13 +465,14 @@ def _raw_stream(index: int) -> int:
 
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
+_device_now = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)  # a tensor on a GPU has made it ready
 
 
 def _run(index: int, what: str, *args) -> None:
     """Calls an entry point with the current stream of GPU `index`, that GPU
     being the current one meanwhile."""
     fn = getattr(_lib or lib(), what)
-    if torch.cuda.current_device() == index:
+    if _device_now() == index:
         status = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(index):

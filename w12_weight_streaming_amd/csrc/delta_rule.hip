@@ -37,7 +37,6 @@
 namespace w12 {
 namespace {
 
-
 template <int KD, int RT>
 struct Shared {
   static constexpr int R = 16 * RT;
@@ -281,8 +280,7 @@ __global__ __launch_bounds__(64 * kWaves, RT == 1 ? 4 : RT == 2 ? 2 : 1) void de
       const int lane = thread_now() & 63, col = lane & 15, g = lane >> 4;
       f32x4 w[RT];
 #pragma unroll
-      for (int m = 0; m < RT; ++m)
-        w[m] = acc[m] = f32x4{0, 0, 0, 0};
+      for (int m = 0; m < RT; ++m) w[m] = acc[m] = f32x4{0, 0, 0, 0};
 #pragma unroll
       for (int t = 0; t < KT; t += 2) {
         uint4 piece[3];
@@ -431,8 +429,7 @@ __global__ __launch_bounds__(64 * kWaves, RT == 1 ? 4 : RT == 2 ? 2 : 1) void de
   if (RT == 1 && a.keep) {
     if (before) {
 #pragma unroll
-      for (int t = 0; t < KT; ++t)
-        S[t][0] = f32x4{__builtin_nanf(""), __builtin_nanf(""), __builtin_nanf(""), __builtin_nanf("")};
+      for (int t = 0; t < KT; ++t) S[t][0] = f32x4{__builtin_nanf(""), __builtin_nanf(""), __builtin_nanf(""), __builtin_nanf("")};
     }
     store_state<KT, VD, 1>(state, vw, S);
     keep_window(a, v);
