@@ -693,7 +693,7 @@ def tree_accept_sampled(node_off: torch.Tensor, parent: torch.Tensor, token: tor
 
 # ------------------------------------------------------------------ recurrent layers of the verify pass
 
-@dataclass(frozen=True, eq=False)  # the description holds the arrays' addresses
+@dataclass(frozen=True, eq=False, init=False)  # the description holds the arrays' addresses
 class DeltaCache:
     """Device-resident state of the recurrent layers: the arrays of
     include/w12.h. state is [layers, slots, value_heads, key_dim, value_dim]
@@ -712,9 +712,8 @@ class DeltaCache:
     delta: torch.Tensor
     key_heads: int
 
-    def __post_init__(self):
-        state, conv, raw, kv, gates, delta, hk = (self.state, self.conv, self.raw, self.kv, self.gates, self.delta,
-                                                  self.key_heads)
+    def __init__(self, state, conv, raw, kv, gates, delta, key_heads):
+        hk = key_heads
         try:  # all at once: programs describe their state again where they switch between steps' arrays
             index = state.get_device()
             layers, slots, hv, kd, vd = state.shape
@@ -740,8 +739,9 @@ class DeltaCache:
             raise ValueError("the recurrent state's arrays differ in shape")
         desc = W12DeltaCache(layers, slots, rows, hk, hv, kd, vd, width + 1, state.data_ptr(), conv.data_ptr(),
                              raw.data_ptr(), kv.data_ptr(), gates.data_ptr(), delta.data_ptr())
-        self.__dict__.update(index=index, value_heads=hv, key_dim=kd, value_dim=vd, channels=channels,
-                             conv_width=width + 1, step_rows=rows, _desc=desc, _ref=ctypes.byref(desc))
+        self.__dict__.update(state=state, conv=conv, raw=raw, kv=kv, gates=gates, delta=delta, key_heads=hk, index=index,
+                             value_heads=hv, key_dim=kd, value_dim=vd, channels=channels, conv_width=width + 1,
+                             step_rows=rows, _desc=desc, _ref=ctypes.byref(desc))
 
     @property
     def device(self):
@@ -901,9 +901,8 @@ def w12_norm(y: torch.Tensor | None, weight: torch.Tensor | None = None, post_we
         if h.dtype not in (_F32, _BF16):
             raise TypeError("h must be a float32 or bfloat16 tensor")
         at_h, kind_h = _get(h, h.dtype, "h", 2, index), W12_Y_F32 if h.dtype is _F32 else W12_Y_BF16
-    for t in (gate, h):
-        if t is not None and t.shape != first.shape:
-            raise ValueError("y, gate and h differ in shape")
+    if (gate is not None and gate.shape[0] != rows) or (h is not None and h is not first and h.shape != first.shape):
+        raise ValueError("y, gate and h differ in shape")
     at_p = 0 if post_weight is None else _get(post_weight, _F32, "post_weight", 1, index, width)
     at_w = 0 if weight is None else _get(weight, _F32, "weight", 1, index, width)
     if out is None:
