@@ -186,6 +186,32 @@ def test_rule_decays(w12, tree, rate):
     check_rule(Step(w12, [40, 9], 1, 2, tree=tree, seed=11, rate=rate))
 
 
+@pytest.mark.parametrize("rows,tree", [([64], None), ([200, 5], None), ([14], None), ([32], "line"), ([130], "line"), ([60], "random")], ids=str)
+def test_rule_the_same_key_again(w12, rows, tree):
+    """Every row the same key at full strength and no decay: a row reads its own
+    value back, and its delta is its value less its parent's. L is all ones on
+    the path, so a tile's inverse is exact, where powers of L reach 3432; left are the
+    roundings of a sum of at most `rows` deltas."""
+    st = Step(w12, rows, 1, 2, tree=tree, seed=51)
+    st.c.kv[0, :, :128] = 0
+    st.c.kv[0, :, 3] = 1
+    st.q.zero_()
+    st.q[:, 0, 3] = 1
+    st.c.gates[0, :, 0], st.c.gates[0, :, 1] = 0, 1
+    out, delta = f64(st.rule(scale=0.5)).reshape(-1, 2, 128), f64(st.c.delta[0])
+    v = f64(st.c.kv[0, :, 128:]).reshape(-1, 2, 128)
+    for s, n in enumerate(rows):
+        a = int(st.off[s])
+        first = f64(st.c.state[0, int(st.slot[s]), :, 3])
+        size = 4 * max(np.abs(v[a:a + n]).max(), np.abs(first).max())
+        tol = (3 * n + 100) * D.U * size
+        for i in range(n):
+            p = i - 1 if tree is None else int(st.parent[a + i])
+            before = v[a + p] if i else first
+            assert (np.abs(delta[a + i] - (v[a + i] - before)) <= tol).all(), (s, i)
+            assert (np.abs(out[a + i] - 0.5 * v[a + i]) <= D.BF16 * np.abs(0.5 * v[a + i]) + tol).all(), (s, i)
+
+
 def test_rule_decay_of_minus_infinity(w12):
     """The state is forgotten, and what follows is as from a state of zeros."""
     import torch
