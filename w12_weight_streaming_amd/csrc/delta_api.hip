@@ -1,6 +1,8 @@
 // extern "C" entry points of the recurrent layers and of the norms (declared
 // in include/w12.h). Every call checks its arguments on the host and returns
 // before anything is launched when one is wrong; nothing here allocates memory.
+#include <initializer_list>
+
 #include "../../include/w12.h"
 #include "delta_internal.h"
 
@@ -61,6 +63,20 @@ size_t span(int64_t rows, int64_t values, int64_t stride, int type) {
   return ((size_t)(rows - 1) * (size_t)stride + (size_t)values) * bytes_of(type);
 }
 
+// What a call reads or writes; p null: nothing.
+struct Range {
+  const void* p;
+  size_t bytes;
+};
+// Nothing that is written lies over what the same call reads.
+bool clear(std::initializer_list<Range> written, std::initializer_list<Range> read) {
+  for (const Range& w : written)
+    for (const Range& r : read)
+      if (w.p && r.p && !apart(w.p, w.bytes, r.p, r.bytes)) return false;
+  return true;
+}
+size_t off_bytes(int32_t num_seq) { return ((size_t)num_seq + 1) * 4; }
+
 // `bytes` at p meet none of the cache's arrays.
 bool apart_of(const w12::DeltaArgs& a, const void* p, size_t bytes) {
   const size_t steps = (size_t)a.layers * a.step_rows, slots = (size_t)a.layers * a.slots;
@@ -92,8 +108,18 @@ w12_status w12_delta_append(const w12_delta_cache* cache, int32_t layer, int32_t
       !aligned(dt_bias, 4))
     return W12_EINVAL;
   const size_t qb = (size_t)total_rows * a.c.key_heads * a.c.key_dim * 2;
-  if (!apart(q, qb, qkv, span(total_rows, a.c.channels, qkv_stride, type)) ||
-      !apart(q, qb, ba, span(total_rows, 2 * a.c.value_heads, ba_stride, type)) || !apart_of(a.c, q, qb))
+  const size_t wb = (size_t)a.c.channels * 4, hb = (size_t)a.c.value_heads * 4;
+  if (!apart_of(a.c, q, qb) ||
+      !clear({{q, qb}},
+             {{qkv, span(total_rows, a.c.channels, qkv_stride, type)},
+              {ba, span(total_rows, 2 * a.c.value_heads, ba_stride, type)},
+              {conv_weight, wb * a.c.width},
+              {conv_bias, wb},
+              {a_log, hb},
+              {dt_bias, hb},
+              {slot, (size_t)num_seq * 4},
+              {row_off, off_bytes(num_seq)},
+              {parent, (size_t)total_rows * 4}}))
     return W12_EINVAL;
   a.st = {row_off, slot, parent, num_seq, total_rows};
   a.layer = layer;
