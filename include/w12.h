@@ -535,7 +535,8 @@ typedef struct w12_delta_cache {
  *   conv_bias [channels] fp32 or NULL; a_log, dt_bias [value_heads] fp32;
  *   q    [total_rows][key_heads][key_dim] bf16 out, apart from the cache's
  *        arrays and all that the call reads.
- * Writes raw, kv and gates of its rows; state and conv are read at most.
+ * Writes raw, kv and gates of its rows, which lie apart from all that the call
+ * reads; state and conv are read at most.
  * Device-detected, reported as NaN queries with nothing staged: an invalid
  * tree, a slot outside [0, slots).
  */

@@ -60,3 +60,8 @@ def append(w12):
 def test_append_outputs_over_what_it_reads(w12):
     call, reads = append(w12)
     refused(w12, call, AT, dict(q=ROWS * HK * KD * 2), reads)
+
+
+def test_append_staged_rows_over_what_it_reads(w12):
+    call, reads = append(w12)
+    refused(w12, call, AT, {n: CACHE[n] for n in ("raw", "kv", "gates")}, reads)

@@ -109,8 +109,12 @@ w12_status w12_delta_append(const w12_delta_cache* cache, int32_t layer, int32_t
     return W12_EINVAL;
   const size_t qb = (size_t)total_rows * a.c.key_heads * a.c.key_dim * 2;
   const size_t wb = (size_t)a.c.channels * 4, hb = (size_t)a.c.value_heads * 4;
+  const size_t steps = (size_t)a.c.layers * a.c.step_rows;
   if (!apart_of(a.c, q, qb) ||
-      !clear({{q, qb}},
+      !clear({{q, qb},
+              {a.c.raw, steps * a.c.channels * 2},
+              {a.c.kv, steps * a.c.kv_width * 2},
+              {a.c.gates, steps * 2 * a.c.value_heads * 4}},
              {{qkv, span(total_rows, a.c.channels, qkv_stride, type)},
               {ba, span(total_rows, 2 * a.c.value_heads, ba_stride, type)},
               {conv_weight, wb * a.c.width},
