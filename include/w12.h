@@ -559,8 +559,8 @@ w12_status w12_delta_append(const w12_delta_cache *cache, int32_t layer, int32_t
  * belongs to (whole heads of them), never other rows'. Deltas and products
  * beyond 2^100 may come out as infinities or NaN in the whole sequence.
  *   q    [total_rows][key_heads][key_dim] bf16 (w12_delta_append's output);
- *   out  [total_rows][value_heads * value_dim] bf16, apart from q and the
- *        cache's arrays;
+ *   out  [total_rows][value_heads * value_dim] bf16, apart from the cache's
+ *        arrays and all that the call reads;
  *   keep 0: writes the rows' delta; state and conv stay, and w12_delta_commit
  *        keeps the accepted rows. Not 0 (parent NULL only: prompts, plain
  *        decoding): every row is kept, state and conv become those behind the

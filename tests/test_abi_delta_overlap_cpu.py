@@ -65,3 +65,21 @@ def test_append_outputs_over_what_it_reads(w12):
 def test_append_staged_rows_over_what_it_reads(w12):
     call, reads = append(w12)
     refused(w12, call, AT, {n: CACHE[n] for n in ("raw", "kv", "gates")}, reads)
+
+
+def rule(w12, keep):
+    L, d = w12.lib(), cache(w12)
+
+    def call(a):
+        return L.w12_delta_rule(ctypes.byref(d), 0, SEQS, a["slot"], a["row_off"], ROWS, 0 if keep else a["parent"], a["q"], 0.1, keep,
+                                a["out"], None)
+    reads = dict(STEP_READS, q=ROWS * HK * KD * 2)
+    if keep:
+        del reads["parent"]
+    return call, reads
+
+
+@pytest.mark.parametrize("keep", [0, 1])
+def test_rule_outputs_over_what_it_reads(w12, keep):
+    call, reads = rule(w12, keep)
+    refused(w12, call, AT, dict(out=ROWS * HV * VD * 2), reads)

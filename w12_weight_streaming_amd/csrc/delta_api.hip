@@ -150,7 +150,12 @@ w12_status w12_delta_rule(const w12_delta_cache* cache, int32_t layer, int32_t n
   w12::DeltaRuleArgs a{};
   a.c = args_of(cache);
   const size_t ob = (size_t)total_rows * a.c.value_heads * a.c.value_dim * 2;
-  if (!apart(q, (size_t)total_rows * a.c.key_heads * a.c.key_dim * 2, out, ob) || !apart_of(a.c, out, ob)) return W12_EINVAL;
+  if (!apart_of(a.c, out, ob) || !clear({{out, ob}},
+                                        {{q, (size_t)total_rows * a.c.key_heads * a.c.key_dim * 2},
+                                         {slot, (size_t)num_seq * 4},
+                                         {row_off, off_bytes(num_seq)},
+                                         {parent, (size_t)total_rows * 4}}))
+    return W12_EINVAL;
   a.st = {row_off, slot, parent, num_seq, total_rows};
   a.layer = layer;
   a.q = q;
