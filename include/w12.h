@@ -564,7 +564,8 @@ w12_status w12_delta_append(const w12_delta_cache *cache, int32_t layer, int32_t
  *   keep 0: writes the rows' delta; state and conv stay, and w12_delta_commit
  *        keeps the accepted rows. Not 0 (parent NULL only: prompts, plain
  *        decoding): every row is kept, state and conv become those behind the
- *        last row, and delta is not written.
+ *        last row, and delta is not written. q, slot, row_off and parent lie
+ *        apart from what is written.
  * Device-detected, reported as NaN outputs of the sequence with nothing else
  * written: what w12_delta_append lists, and with keep a slot of an earlier
  * sequence of the call. Results are bitwise reproducible.

@@ -83,3 +83,10 @@ def rule(w12, keep):
 def test_rule_outputs_over_what_it_reads(w12, keep):
     call, reads = rule(w12, keep)
     refused(w12, call, AT, dict(out=ROWS * HV * VD * 2), reads)
+
+
+@pytest.mark.parametrize("keep", [0, 1])
+def test_rule_kept_arrays_over_what_it_reads(w12, keep):
+    """The deltas, or the state and the window that a call with keep moves on."""
+    call, reads = rule(w12, keep)
+    refused(w12, call, AT, {n: CACHE[n] for n in (("state", "conv") if keep else ("delta",))}, reads)

@@ -150,7 +150,12 @@ w12_status w12_delta_rule(const w12_delta_cache* cache, int32_t layer, int32_t n
   w12::DeltaRuleArgs a{};
   a.c = args_of(cache);
   const size_t ob = (size_t)total_rows * a.c.value_heads * a.c.value_dim * 2;
-  if (!apart_of(a.c, out, ob) || !clear({{out, ob}},
+  const size_t vb = (size_t)a.c.value_heads * a.c.value_dim * 4;  // a row's deltas
+  const size_t steps = (size_t)a.c.layers * a.c.step_rows, slots = (size_t)a.c.layers * a.c.slots;
+  if (!apart_of(a.c, out, ob) || !clear({{out, ob},
+                                         {keep ? nullptr : a.c.delta, steps * vb},
+                                         {keep ? a.c.state : nullptr, slots * a.c.key_dim * vb},
+                                         {keep ? a.c.conv : nullptr, slots * (a.c.width - 1) * a.c.channels * 2}},
                                         {{q, (size_t)total_rows * a.c.key_heads * a.c.key_dim * 2},
                                          {slot, (size_t)num_seq * 4},
                                          {row_off, off_bytes(num_seq)},
