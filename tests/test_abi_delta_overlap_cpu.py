@@ -90,3 +90,16 @@ def test_rule_kept_arrays_over_what_it_reads(w12, keep):
     """The deltas, or the state and the window that a call with keep moves on."""
     call, reads = rule(w12, keep)
     refused(w12, call, AT, {n: CACHE[n] for n in (("state", "conv") if keep else ("delta",))}, reads)
+
+
+def commit(w12):
+    L, d = w12.lib(), cache(w12)
+
+    def call(a):
+        return L.w12_delta_commit(ctypes.byref(d), SEQS, a["slot"], a["row_off"], ROWS, a["accept_len"], a["path"], a["kept"], None)
+    return call, dict(slot=SEQS * 4, row_off=(SEQS + 1) * 4, accept_len=SEQS * 4, path=ROWS * 4)
+
+
+def test_commit_counts_over_what_it_reads(w12):
+    call, reads = commit(w12)
+    refused(w12, call, AT, dict(kept=SEQS * 4), reads)

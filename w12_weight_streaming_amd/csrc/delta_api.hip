@@ -174,12 +174,13 @@ w12_status w12_delta_commit(const w12_delta_cache* cache, int32_t num_seq, const
                             int32_t total_rows, const int32_t* accept_len, const int32_t* path, int32_t* kept,
                             hipStream_t stream) {
   if (!cache_ok(cache) || !step_ok(cache, num_seq, row_off, total_rows) || !accept_len || !kept) return W12_EINVAL;
-  if (!apart(kept, (size_t)num_seq * 4, accept_len, (size_t)num_seq * 4) ||
-      (path && !apart(kept, (size_t)num_seq * 4, path, (size_t)total_rows * 4)))
-    return W12_EINVAL;
   w12::DeltaCommitArgs a{};
   a.c = args_of(cache);
-  if (!apart_of(a.c, kept, (size_t)num_seq * 4)) return W12_EINVAL;
+  const size_t nb = (size_t)num_seq * 4;
+  if (!apart_of(a.c, kept, nb) ||
+      !clear({{kept, nb}},
+             {{accept_len, nb}, {path, (size_t)total_rows * 4}, {slot, nb}, {row_off, off_bytes(num_seq)}}))
+    return W12_EINVAL;
   a.st = {row_off, slot, nullptr, num_seq, total_rows};
   a.accept_len = accept_len;
   a.path = path;
