@@ -581,7 +581,8 @@ w12_status w12_delta_rule(const w12_delta_cache *cache, int32_t layer, int32_t n
  *   S <- e^G_n S + sum_j e^(G_n - G_j) k_j delta_j^T,  G_j = g_0 + ... + g_j
  * along the path, and the window.
  *   kept [num_seq] out: rows kept; accept_len -1 (a refused tree) keeps none.
- *        Apart from the cache's arrays and all that the call reads.
+ *        Apart from the cache's arrays and all that the call reads, as state
+ *        and conv are from the latter.
  * Device-detected, reported as kept -1 with nothing written: a slot outside
  * [0, slots) or of an earlier sequence, a range of rows that is none, an
  * accept_len or path outside the sequence's rows or not ascending from row 0.

@@ -103,3 +103,8 @@ def commit(w12):
 def test_commit_counts_over_what_it_reads(w12):
     call, reads = commit(w12)
     refused(w12, call, AT, dict(kept=SEQS * 4), reads)
+
+
+def test_commit_states_over_what_it_reads(w12):
+    call, reads = commit(w12)
+    refused(w12, call, AT, {n: CACHE[n] for n in ("state", "conv")}, reads)

@@ -176,9 +176,11 @@ w12_status w12_delta_commit(const w12_delta_cache* cache, int32_t num_seq, const
   if (!cache_ok(cache) || !step_ok(cache, num_seq, row_off, total_rows) || !accept_len || !kept) return W12_EINVAL;
   w12::DeltaCommitArgs a{};
   a.c = args_of(cache);
-  const size_t nb = (size_t)num_seq * 4;
+  const size_t nb = (size_t)num_seq * 4, slots = (size_t)a.c.layers * a.c.slots;
   if (!apart_of(a.c, kept, nb) ||
-      !clear({{kept, nb}},
+      !clear({{kept, nb},
+              {a.c.state, slots * a.c.value_heads * a.c.key_dim * a.c.value_dim * 4},
+              {a.c.conv, slots * (a.c.width - 1) * a.c.channels * 2}},
              {{accept_len, nb}, {path, (size_t)total_rows * 4}, {slot, nb}, {row_off, off_bytes(num_seq)}}))
     return W12_EINVAL;
   a.st = {row_off, slot, nullptr, num_seq, total_rows};
