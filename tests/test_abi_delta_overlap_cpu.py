@@ -31,7 +31,7 @@ STEP_READS = dict(slot=SEQS * 4, row_off=(SEQS + 1) * 4, parent=ROWS * 4)
 
 def meet(written, written_bytes, read, read_bytes):
     """Places of `read` whose first or last 16 bytes (4, if it has no more) lie in `written`, and inside it."""
-    step = 16 if read_bytes >= 16 else 4
+    step = 16 if min(read_bytes, written_bytes) >= 16 else 4
     return [written + written_bytes - step, written - (read_bytes - step) // 16 * 16, written + (written_bytes - step) // 32 * 16]
 
 
