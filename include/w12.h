@@ -554,10 +554,14 @@ w12_status w12_delta_append(const w12_delta_cache *cache, int32_t layer, int32_t
  * with fp32 states, deltas and accumulation (a factor that is not bf16 enters
  * the matrix products whole: in fp32, or in three bf16 pieces that hold its 24 bits)
  * and decays summed in 64 bits. A row sees its ancestors and itself: an
- * infinity or NaN in a row's q, k, v or gates reaches only its own outputs
- * and deltas and those behind it, and the state behind them, of the heads it
- * belongs to (whole heads of them), never other rows'. Deltas and products
- * beyond 2^100 may come out as infinities or NaN in the whole sequence.
+ * infinity or NaN in a row's k, v or gates (g of minus infinity apart: it
+ * forgets the state) leaves no numbers in its own outputs and deltas, those of
+ * the rows behind it on their paths, and the state behind them; in its q, none
+ * in its own outputs. No other row's change. Of k, q and
+ * the gates it reaches all of the value heads that they belong to; of v at least
+ * the value dim it stands in and at most its head (how many of the head's other
+ * dims share a workgroup goes by the form that the call takes). Deltas and
+ * products beyond 2^100 may come out as infinities or NaN in the whole sequence.
  *   q    [total_rows][key_heads][key_dim] bf16 (w12_delta_append's output);
  *   out  [total_rows][value_heads * value_dim] bf16, apart from the cache's
  *        arrays and all that the call reads;
