@@ -289,12 +289,15 @@ __global__ __launch_bounds__(64 * (kMakers + kTakers)) __attribute__((amdgpu_wav
         uint4 piece[3];
         split3(p0 * d0, p1 * d1, piece[0], piece[1], piece[2]);
         const float keep = s.grow[b * R + R - 1];  // rows past the end decay by nothing
+        f32x4 add[KT];
 #pragma unroll
-        for (int t = 0; t < KT; ++t) S[t][0] *= keep;
+        for (int t = 0; t < KT; ++t) add[t] = mfma_bf16(ft[t], piece[2], zero);
 #pragma unroll
-        for (int p = 2; p >= 0; --p)
+        for (int p = 1; p >= 0; --p)
 #pragma unroll
-          for (int t = 0; t < KT; ++t) S[t][0] = mfma_bf16(ft[t], piece[p], S[t][0]);
+          for (int t = 0; t < KT; ++t) add[t] = mfma_bf16(ft[t], piece[p], add[t]);
+#pragma unroll
+        for (int t = 0; t < KT; ++t) join_state(S[t][0], keep, add[t]);
       }
       acc[1] = mfma_f32(see1, d1, acc[1]);
       const uint32_t odd = s.odd[b], odd_q = s.odd_q[b];

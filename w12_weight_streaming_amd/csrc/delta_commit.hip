@@ -8,7 +8,7 @@
 // in registers and adds 32 rows at a time on the matrix cores (most paths are
 // one turn), keys as they are (bf16), weighted deltas in three bf16 pieces. 48
 // layers of 48 heads of 128 x 128, one sequence: 63 us for 303 MB (4.8 TB/s);
-// 12 layers of 24 sequences 330 us for 1.83 GB (5.5 TB/s). With the states' traffic
+// 12 layers of 24 sequences 332 us for 1.83 GB (5.5 TB/s). With the states' traffic
 // through the caches 77 and 389.
 #include "delta_mfma.h"
 
@@ -21,7 +21,7 @@ constexpr int kStride = kTurn + 8;    // of a key dim's rows in LDS: 8-byte read
 
 // A wave owns NC * 16 of the head's value dims, the lane NC neighbouring ones.
 template <int KD, int NC>
-__global__ __launch_bounds__(kThreads, 3) void delta_commit_kernel(DeltaCommitArgs a) {
+__global__ __launch_bounds__(kThreads, 4) void delta_commit_kernel(DeltaCommitArgs a) {
   constexpr int KT = KD / 16, VD = 64 * NC;
   __shared__ alignas(16) uint16_t s_k[KD * kStride];
   __shared__ int s_row[kStepRows];
@@ -111,10 +111,11 @@ __global__ __launch_bounds__(kThreads, 3) void delta_commit_kernel(DeltaCommitAr
       const uint4 f = fragment(s_k + (16 * t + col) * kStride + 4 * g);
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
+f32x4 add = {0, 0, 0, 0};
 #pragma unroll
-        for (int r = 0; r < 4; ++r) S[t][c][r] *= keep;
-#pragma unroll
-        for (int p = 2; p >= 0; --p) S[t][c] = mfma_bf16(f, piece[c][p], S[t][c]);
+        for (int p = 2; p >= 0; --p) add = mfma_bf16(f, piece[c][p], add);
+        join_state(S[t][c], keep, add);
+        asm volatile("" : "+v"(S[t][c]));  // keeps its place among the products: else 157 registers, 354 us below
       }
     }
   }

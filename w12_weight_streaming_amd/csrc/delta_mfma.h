@@ -117,6 +117,14 @@ __device__ __forceinline__ void split3(const f32x4& x, const f32x4& y, uint4& hi
   lo = make_uint4(l[0], l[1], l[2], l[3]);
 }
 
+// What rows add to a state, S <- keep S + add, rounded once at the state's size:
+// the pieces' products are gathered from zero, as each one that went into S by
+// itself would round it again.
+__device__ __forceinline__ void join_state(f32x4& S, float keep, const f32x4& add) {
+#pragma unroll
+  for (int r = 0; r < 4; ++r) S[r] = __builtin_fmaf(keep, S[r], add[r]);
+}
+
 // 8 bf16 of a row (two 8-byte pieces, 16 values apart): depths 4 (l / 16) + r of two neighbouring tiles of 16.
 __device__ __forceinline__ uint4 fragment(const uint16_t* p) {
   const uint2 a = *reinterpret_cast<const uint2*>(p), b = *reinterpret_cast<const uint2*>(p + 16);

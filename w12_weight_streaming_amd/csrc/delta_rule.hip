@@ -419,9 +419,10 @@ __global__ __launch_bounds__(64 * kWaves, RT == 1 ? 4 : RT == 2 ? 2 : 1) void de
         for (int t = 0; t < KT; ++t) {
           const uint2 x = *reinterpret_cast<const uint2*>(s.t + (16 * t + col) * TS + 4 * g);
           const uint4 f = make_uint4(x.x, x.y, 0, 0);
-          S[t][0] *= keep;
+          f32x4 add = {0, 0, 0, 0};
 #pragma unroll
-          for (int p = 2; p >= 0; --p) S[t][0] = mfma_bf16(f, piece[p], S[t][0]);
+          for (int p = 2; p >= 0; --p) add = mfma_bf16(f, piece[p], add);
+          join_state(S[t][0], keep, add);
         }
       }
     }
