@@ -182,10 +182,9 @@ __global__ __launch_bounds__(64 * (kMakers + kTakers)) __attribute__((amdgpu_wav
           tile<KD>(s, o, b * R, true, mw);
           wave_lds_sync();
           invert<true>(o.low[mw], o.inv[mw], 16);
-        } else {
+        } else {  // the lower tile of L and of D (q . k), then the diagonal ones of the latter
           tile<KD>(s, o, b * R, mw == 2, 2);
           tile<KD>(s, o, b * R, false, mw - 2);
-          if (mw == 3) tile<KD>(s, o, b * R, false, 2);
         }
       }
       __syncthreads();
