@@ -2,20 +2,22 @@
 //
 // t = y, normed, gated; h += scale t; out = norm of h (or t). Every tensor is
 // read and written once: a row stays in registers between its sums of squares
-// and its outputs, 8 neighbouring values a thread. Groups of up to 512 values
-// are 8 to 64 lanes of one wave, so their sums need no barrier; wider ones a
+// and its outputs, 8 neighbouring values a thread. Groups of up to 256 values
+// are 1 to 32 lanes of one wave, so their sums need no barrier; wider ones a
 // workgroup, of as many threads as give each 8 values (up to 8192), then 16 or 32.
 // Bound by bytes at many rows, else by two loads' and one reduction's latency:
 // 32 x 5120 bf16 with a residual 4.3 us; 512 x 5120 fp32 with one 9.9 us for 36.7 MB
-// (3.7 TB/s); 192 x 48 heads of 128 with gates 4.6 us. One wave against a workgroup:
-// 192 x 48 of 128 4.0 us / 6.5, 512 x 16 of 256 4.9 / 6.4, 512 x 8 of 512 5.0 / 4.7.
+// (3.7 TB/s); 192 x 48 heads of 128 with gates 4.6 us. A part of a wave
+// against a workgroup, rows x groups: 192 x 48 of 128 4.1 us / 6.5, 512 x 16 of 256 5.0 /
+// 6.5, 192 x 48 of 256 5.5 / 6.9, 32 x 1 of 256 3.3 / 3.1, 32 x 1 of 512 3.5 / 3.1, 512 x 8
+// of 512 5.0 / 4.7, 192 x 48 of 512 8.6 / 7.6.
 #include "delta_internal.h"
 #include "w12_device.h"
 
 namespace w12 {
 namespace {
 
-constexpr int kNarrow = 512;         // widest group of one wave
+constexpr int kNarrow = 256;         // widest group of a part of a wave
 constexpr int kNarrowThreads = 256;  // of a workgroup of such groups
 constexpr int kMostThreads = 1024;
 
@@ -162,7 +164,7 @@ __device__ __forceinline__ void norm_group(const NormArgs& a, int64_t row, int g
     if (n[k] > 0) store8<Vec>(a.out, 0, at + c + k * step, n[k], t[k]);
 }
 
-// Groups of up to 512 values: `lanes` (a power of two) neighbouring lanes each.
+// Groups of up to 256 values: `lanes` (a power of two) neighbouring lanes each.
 template <bool Vec>
 __global__ __launch_bounds__(kNarrowThreads) void norm_narrow_kernel(NormArgs a, int lanes) {
   const int per = kNarrowThreads / lanes, mine = threadIdx.x / lanes, c = (threadIdx.x & (lanes - 1)) * 8;
