@@ -108,3 +108,12 @@ def test_commit_counts_over_what_it_reads(w12):
 def test_commit_states_over_what_it_reads(w12):
     call, reads = commit(w12)
     refused(w12, call, AT, {n: CACHE[n] for n in ("state", "conv")}, reads)
+
+
+@pytest.mark.parametrize("off", [1, 2, 3])
+def test_misaligned_step_arrays(w12, off):
+    """The arrays of 32-bit numbers, as the header's conventions say."""
+    for make, names in ((append(w12), STEP_READS), (rule(w12, 0), STEP_READS), (rule(w12, 1), ("slot", "row_off")),
+                        (commit(w12), ("slot", "row_off", "accept_len", "path", "kept"))):
+        for n in names:
+            assert make[0]({**AT, n: AT[n] + off}) == w12.W12_EINVAL, n

@@ -53,9 +53,10 @@ w12::DeltaArgs args_of(const w12_delta_cache* c) {
   return a;
 }
 
-bool step_ok(const w12_delta_cache* c, int32_t num_seq, const int32_t* row_off, int32_t total_rows) {
+bool step_ok(const w12_delta_cache* c, int32_t num_seq, const int32_t* slot, const int32_t* row_off, int32_t total_rows,
+             const int32_t* parent) {
   return num_seq >= 1 && num_seq <= w12::kStepRows && total_rows >= 1 && total_rows <= w12::kStepRows &&
-         total_rows <= c->step_rows && row_off;
+         total_rows <= c->step_rows && row_off && aligned(row_off, 4) && aligned(slot, 4) && aligned(parent, 4);
 }
 
 // Bytes from the first value of `rows` rows of `values`, `stride` values apart, to behind the last.
@@ -95,7 +96,7 @@ w12_status w12_delta_append(const w12_delta_cache* cache, int32_t layer, int32_t
                             int64_t qkv_stride, const void* ba, int64_t ba_stride, int type, const float* conv_weight,
                             const float* conv_bias, const float* a_log, const float* dt_bias, uint16_t* q,
                             hipStream_t stream) {
-  if (!cache_ok(cache) || layer < 0 || layer >= cache->layers || !step_ok(cache, num_seq, row_off, total_rows))
+  if (!cache_ok(cache) || layer < 0 || layer >= cache->layers || !step_ok(cache, num_seq, slot, row_off, total_rows, parent))
     return W12_EINVAL;
   if (!qkv || !ba || !conv_weight || !a_log || !dt_bias || !q || !ydtype(type)) return W12_EINVAL;
   w12::DeltaAppendArgs a{};
@@ -143,7 +144,7 @@ w12_status w12_delta_append(const w12_delta_cache* cache, int32_t layer, int32_t
 w12_status w12_delta_rule(const w12_delta_cache* cache, int32_t layer, int32_t num_seq, const int32_t* slot,
                           const int32_t* row_off, int32_t total_rows, const int32_t* parent, const uint16_t* q,
                           float scale, int32_t keep, uint16_t* out, hipStream_t stream) {
-  if (!cache_ok(cache) || layer < 0 || layer >= cache->layers || !step_ok(cache, num_seq, row_off, total_rows))
+  if (!cache_ok(cache) || layer < 0 || layer >= cache->layers || !step_ok(cache, num_seq, slot, row_off, total_rows, parent))
     return W12_EINVAL;
   if (!q || !out || !finite(scale) || (keep && parent)) return W12_EINVAL;
   if (!aligned(q, 16) || !aligned(out, 16)) return W12_EINVAL;
@@ -173,7 +174,9 @@ w12_status w12_delta_rule(const w12_delta_cache* cache, int32_t layer, int32_t n
 w12_status w12_delta_commit(const w12_delta_cache* cache, int32_t num_seq, const int32_t* slot, const int32_t* row_off,
                             int32_t total_rows, const int32_t* accept_len, const int32_t* path, int32_t* kept,
                             hipStream_t stream) {
-  if (!cache_ok(cache) || !step_ok(cache, num_seq, row_off, total_rows) || !accept_len || !kept) return W12_EINVAL;
+  if (!cache_ok(cache) || !step_ok(cache, num_seq, slot, row_off, total_rows, nullptr) || !accept_len || !kept ||
+      !aligned(accept_len, 4) || !aligned(path, 4) || !aligned(kept, 4))
+    return W12_EINVAL;
   w12::DeltaCommitArgs a{};
   a.c = args_of(cache);
   const size_t nb = (size_t)num_seq * 4, slots = (size_t)a.c.layers * a.c.slots;
