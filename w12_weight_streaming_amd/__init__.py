@@ -807,19 +807,20 @@ def w12_delta_append(cache: DeltaCache, layer: int, qkv: torch.Tensor, ba: torch
         raise ValueError("qkv and ba differ in type or rows")
     at_off = _get(row_off, _I32, "row_off", 1, index)
     seqs = row_off.shape[0] - 1
+    at_w = _get(conv_weight, _F32, "conv_weight", 2, index)
     if conv_weight.shape != (cache.channels, cache.conv_width):
         raise ValueError(f"conv_weight must be [{cache.channels}, {cache.conv_width}]")
-    at_w = _get(conv_weight, _F32, "conv_weight", 2, index)
     at_c = 0 if conv_bias is None else _get(conv_bias, _F32, "conv_bias", 1, index, cache.channels)
     at_a, at_d = _get(a_log, _F32, "a_log", 1, index, hv), _get(dt_bias, _F32, "dt_bias", 1, index, hv)
     if out is None:
         out = torch.empty(rows, hk, kd, dtype=_BF16, device=qkv.device)
-    elif out.numel() < rows * hk * kd:
+    at_out = _get(out, _BF16, "out", None, index)
+    if out.numel() < rows * hk * kd:
         raise ValueError("out must hold [rows, key_heads, key_dim]")
     _run(index, "w12_delta_append", cache._ref, layer, seqs,
          0 if slot is None else _get(slot, _I32, "slot", 1, index, seqs), at_off, rows,
          0 if parent is None else _get(parent, _I32, "parent", 1, index, rows), at_x, step_x, at_b, step_b, kind, at_w,
-         at_c, at_a, at_d, _get(out, _BF16, "out", None, index))
+         at_c, at_a, at_d, at_out)
     return out
 
 
@@ -842,12 +843,13 @@ def w12_delta_rule(cache: DeltaCache, layer: int, q: torch.Tensor, row_off: torc
     wide = cache.value_heads * cache.value_dim
     if out is None:
         out = torch.empty(rows, wide, dtype=_BF16, device=q.device)
-    elif out.numel() < rows * wide:
+    at_out = _get(out, _BF16, "out", None, index)
+    if out.numel() < rows * wide:
         raise ValueError("out must hold [rows, value_heads * value_dim]")
     _run(index, "w12_delta_rule", cache._ref, layer, seqs,
          0 if slot is None else _get(slot, _I32, "slot", 1, index, seqs), at_off, rows,
          0 if parent is None else _get(parent, _I32, "parent", 1, index, rows), at_q,
-         kd ** -0.5 if scale is None else scale, 1 if keep else 0, _get(out, _BF16, "out", None, index))
+         kd ** -0.5 if scale is None else scale, 1 if keep else 0, at_out)
     return out
 
 
@@ -898,7 +900,7 @@ def w12_norm(y: torch.Tensor | None, weight: torch.Tensor | None = None, post_we
     at_g = none if gate is None else _rows_of(gate, "gate", wide, index)
     at_h, kind_h = 0, W12_Y_F32
     if h is not None:
-        if h.dtype not in (_F32, _BF16):
+        if not isinstance(h, torch.Tensor) or h.dtype not in (_F32, _BF16):
             raise TypeError("h must be a float32 or bfloat16 tensor")
         at_h, kind_h = _get(h, h.dtype, "h", 2, index), W12_Y_F32 if h.dtype is _F32 else W12_Y_BF16
     if (gate is not None and gate.shape[0] != rows) or (h is not None and h is not first and h.shape != first.shape):
@@ -907,8 +909,9 @@ def w12_norm(y: torch.Tensor | None, weight: torch.Tensor | None = None, post_we
     at_w = 0 if weight is None else _get(weight, _F32, "weight", 1, index, width)
     if out is None:
         out = torch.empty(rows, wide, dtype=_BF16, device=first.device)
-    elif out.numel() < rows * wide:
+    at_out = _get(out, _BF16, "out", None, index)
+    if out.numel() < rows * wide:
         raise ValueError("out must hold [rows, groups * width]")
     _run(index, "w12_norm", rows, groups, width, at_y[0], at_y[2], at_y[1], at_p, at_g[0], at_g[2], at_g[1], scale, at_h,
-         kind_h, at_w, eps, _get(out, _BF16, "out", None, index))
+         kind_h, at_w, eps, at_out)
     return out
