@@ -534,7 +534,8 @@ typedef struct w12_delta_cache {
  *   conv_weight [channels][conv_width] fp32, the row's own tap last;
  *   conv_bias [channels] fp32 or NULL; a_log, dt_bias [value_heads] fp32;
  *   q    [total_rows][key_heads][key_dim] bf16 out, apart from the cache's
- *        arrays and all that the call reads.
+ *        arrays and all that the call reads;
+ * qkv, conv_weight, conv_bias and q 16-byte aligned.
  * Writes raw, kv and gates of its rows, which lie apart from all that the call
  * reads; state and conv are read at most.
  * Device-detected, reported as NaN queries with nothing staged: an invalid
@@ -564,7 +565,7 @@ w12_status w12_delta_append(const w12_delta_cache *cache, int32_t layer, int32_t
  * products beyond 2^100 may come out as infinities or NaN in the whole sequence.
  *   q    [total_rows][key_heads][key_dim] bf16 (w12_delta_append's output);
  *   out  [total_rows][value_heads * value_dim] bf16, apart from the cache's
- *        arrays and all that the call reads;
+ *        arrays and all that the call reads; q and out 16-byte aligned;
  *   keep 0: writes the rows' delta; state and conv stay, and w12_delta_commit
  *        keeps the accepted rows. Not 0 (parent NULL only: prompts, plain
  *        decoding): every row is kept, state and conv become those behind the
@@ -573,6 +574,10 @@ w12_status w12_delta_append(const w12_delta_cache *cache, int32_t layer, int32_t
  * Device-detected, reported as NaN outputs of the sequence with nothing else
  * written: what w12_delta_append lists, and with keep a slot of an earlier
  * sequence of the call. Results are bitwise reproducible.
+ * The kernel's form goes by the mean rows of a sequence, empty ones counted: a
+ * step of single rows and long sequences is faster as two calls, each over its
+ * own part of slot and row_off, the single rows first and the first call's
+ * total_rows theirs alone.
  */
 w12_status w12_delta_rule(const w12_delta_cache *cache, int32_t layer, int32_t num_seq, const int32_t *slot,
                           const int32_t *row_off, int32_t total_rows, const int32_t *parent, const uint16_t *q,

@@ -830,7 +830,8 @@ def w12_delta_rule(cache: DeltaCache, layer: int, q: torch.Tensor, row_off: torc
     """The gated delta rule over the step's staged rows, q [rows, key_heads,
     key_dim] bf16; returns [rows, value_heads * value_dim] bf16. scale defaults
     to key_dim ** -0.5. keep (chains only: prompts, plain decoding): every row
-    joins the state and the window, and w12_delta_commit is not called."""
+    joins the state and the window, and w12_delta_commit is not called. A step of
+    single rows and long sequences is faster as two calls (include/w12.h)."""
     index = cache.index
     at_q = _get(q, _BF16, "q", 3, index)
     rows, hk, kd = q.shape

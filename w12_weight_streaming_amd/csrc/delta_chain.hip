@@ -8,9 +8,10 @@
 // the new one, 16 value dims a wave: the two fill each other's waits. Blocks of
 // 32 rows rather than 64 let both halves of the buffers fit (82 KB), and leave
 // two steps of the triangular system. 512 rows of 16 key and 48 value heads of
-// 128 x 128: 48 us, 3.0 a block, of which the takers' products with the state take
-// 1.2 and the system, the new state and the outputs 1.6 (3.7 GFLOP at 77 TFLOP/s;
-// the way from state to state bounds it, not a rate). Makers need 2.2 of it.
+// 128 x 128: 46 us, 2.9 a block, of which the takers' products with the state take
+// 1.2 and the system, the new state and the outputs 1.6 (the way from state to
+// state bounds it, not a rate: the rule's own 6 operations a row and entry of the
+// state are 2.4 GFLOP, at 53 TFLOP/s). Makers need at most 2.2 of it.
 #include "delta_rule.h"
 
 namespace w12 {
@@ -132,6 +133,7 @@ __device__ __forceinline__ void tile(const Shared<KD>& s, Block<KD>& o, int firs
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
     const int over = u == 2 ? 1 : col - (4 * g + r);  // how far row i lies behind row j
+    // (__expf: off by about |f| 2^-23 of itself, as much as f's own rounding to fp32)
     x[r] = (of_low ? over > 0 : over >= 0) ? (of_low ? beta * x[r] : x[r]) * __expf(f[r]) : 0.0f;
   }
   (of_low ? o.low : o.see)[u][lane] = x;
@@ -348,7 +350,8 @@ void go(const DeltaRuleArgs& a, hipStream_t s) {
 template <int KD, int VD>
 hipError_t launch(const DeltaRuleArgs& a, hipStream_t s) {
   // two takers where that leaves a CU for each workgroup, as fewer waves share a
-  // SIMD: 1 x 512 rows 47 us against 53; 2 x 256 51 against 32
+  // SIMD: 1 x 512 rows 46 us against 50, 1 x 32 8.5 against 9.0; 2 x 256 50 against
+  // 31, 2 x 64 20.3 against 12.5
   if (a.c.value_heads * (VD / 32) * a.st.num_seq <= 256)
     go<KD, VD, 2>(a, s);
   else

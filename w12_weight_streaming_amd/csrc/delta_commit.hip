@@ -7,9 +7,10 @@
 // the state's bytes, read and written once: a workgroup holds one head's state
 // in registers and adds 32 rows at a time on the matrix cores (most paths are
 // one turn), keys as they are (bf16), weighted deltas in three bf16 pieces. 48
-// layers of 48 heads of 128 x 128, one sequence: 63 us for 303 MB (4.8 TB/s);
-// 12 layers of 24 sequences 332 us for 1.83 GB (5.5 TB/s). With the states' traffic
-// through the caches 77 and 389.
+// layers of 48 heads of 128 x 128, one sequence: 64 us for 313 MB of states,
+// windows and rows (4.9 TB/s); 12 layers of 24 sequences 330 us for 1.87 GB (5.7
+// TB/s, where 4 GiB rewritten in place past the caches reach 5.9). With the
+// states' traffic through the caches 77 and 389.
 #include "delta_mfma.h"
 
 namespace w12 {
@@ -115,7 +116,7 @@ f32x4 add = {0, 0, 0, 0};
 #pragma unroll
         for (int p = 2; p >= 0; --p) add = mfma_bf16(f, piece[c][p], add);
         join_state(S[t][c], keep, add);
-        asm volatile("" : "+v"(S[t][c]));  // keeps its place among the products: else 157 registers, 354 us below
+        asm volatile("" : "+v"(S[t][c]));  // keeps its place among the products: else 157 registers and 354 us for 12 x 24
       }
     }
   }

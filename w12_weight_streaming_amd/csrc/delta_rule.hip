@@ -28,7 +28,8 @@
 // and 48 value heads of 128 x 128, 24.5 us for 85 MB (3.5 TB/s), 32 x 1 41 us for 202 MB
 // read and written (4.9 TB/s); by latency where there are few: one 32-row tree
 // takes 9.0 us, about 1.5 of them until a sequence's rows and slot are there,
-// 2 for the loads behind those, 2.5 for tiles and inverses, 1 for the products.
+// 2 for the loads behind those, 2.5 for tiles and inverses, 1 for the products;
+// 2 are not told apart (start and end, outputs, instructions fetched for the first time).
 // A workgroup's code runs once, so its instructions are fetched as it goes:
 // loops of few instructions beat unrolled ones outside the state's registers.
 #include "delta_mfma.h"
@@ -256,6 +257,7 @@ __global__ __launch_bounds__(64 * kWaves, RT == 1 ? 4 : RT == 2 ? 2 : 1) void de
       for (int r = 0; r < 4; ++r) {
         const int j = 16 * bj + 4 * g + r;
         const bool on = i < n && ((in >> j) & 1) && !(of_low && i == j);
+        // (__expf: off by about |x| 2^-23 of itself, as much as its argument's rounding to fp32)
         x[r] = on ? f * __expf((float)(gi - s.sum[base + j])) * x[r] : 0.0f;
       }
       (of_low ? s.low : s.see)[bi * RT + bj][lane] = x;
@@ -437,7 +439,9 @@ __global__ __launch_bounds__(64 * kWaves, RT == 1 ? 4 : RT == 2 ? 2 : 1) void de
   }
 }
 
-// Plain decoding: as many rows as sequences, chains.
+// Plain decoding: as many rows as sequences, chains. Two dims a lane of 128 x 128
+// spill 8 registers at four waves a SIMD, none at three: 32 x 1 42.2 us against 41.8,
+// 8 x 1 14.0 / 13.7, 64 x 1 76.8 / 77.0.
 constexpr int kDecodeThreads = 256;
 template <int KD, int VD, int NC>
 __global__ __launch_bounds__(kDecodeThreads, 4) void delta_decode_kernel(DeltaRuleArgs a) {
@@ -457,15 +461,25 @@ __global__ __launch_bounds__(kDecodeThreads, 4) void delta_decode_kernel(DeltaRu
 
 // Which form: by the rows a sequence has on average (their numbers are on the
 // device) and by the workgroups there are. In us, 16 key and 48 value heads of
-// 128 x 128, sequences x rows, states rotated past the caches for single rows:
+// 128 x 128 (other heads and dims go by their workgroups, not measured on both
+// sides), sequences x rows, states rotated past the caches for single rows:
 //   single rows, 32 value dims a wave (past the caches) against 16: 1 x 1 7.6 / 6.6,
 //     2 x 1 7.8 / 7.1, 3 x 1 8.1 / 9.7, 8 x 1 14.0 / 17.8, 32 x 1 42.3 / 52.0.
 //   trees, blocks of 16 / 32 / 64 rows: 24 x 8 24.0 / 38.2 / 99.9, 1 x 16 7.9 / 8.1 /
 //     13.2, 1 x 24 13.9 / 8.5 / 13.5, 6 x 32 20.0 / 17.1 / 37.7, 1 x 64 32.9 / 17.7 / 15.2,
 //     3 x 64 33.4 / 20.7 / 27.1 (a CU holds one workgroup of the last).
-//   chains, delta_chain.hip against blocks of 16: 1 x 16 9.0 / 10.0, 8 x 8 27.3 / 14.6,
-//     1 x 64 11.2 / 27.3, 4 x 32 17.5 / 17.5, 6 x 32 26.0 / 23.4, 8 x 48 38.3 / 32.9, 8 x 64
-//     37.7 / 39.6, 4 x 128 35.0 / 52.7, 16 x 32 58.2 / 40.7.
+//   kept chains, delta_chain.hip against blocks of 16: 1 x 32 8.7 / 15.9, 1 x 64 10.8 /
+//     27.0, 4 x 32 17.5 / 17.3, 6 x 32 25.7 / 22.7, 8 x 48 38.0 / 32.3, 8 x 64 37.1 / 39.8,
+//     4 x 128 34.6 / 52.9, 16 x 32 57.7 / 40.5. Up to 16 rows all go in blocks of 16, for
+//     two or fewer sequences the slower side: 1 x 8 8.9 / 9.2, 1 x 16 8.8 / 10.0, 2 x 16
+//     9.9 / 10.6, but 3 x 16 17.7 / 10.9, 8 x 8 27.0 / 15.0, 8 x 16 28.0 / 16.2. Not kept:
+//     1 x 32 6.8 / 13.4, 24 x 8 55.3 / 24.0, 8 x 48 30.0 / 28.8.
+// A step's sequences need not be alike, and a long one among short ones is then
+// in a form of the short ones' (right, and slow): 32 single kept rows and 480 of one
+// sequence 185 to 210 us, where alone they take 40 and 44; 64 rows among 63 empty
+// sequences 91 against 11, 512 among 511 empty ones 750 against 47; a tree of 400
+// rows alone 271, with 24 single rows 303 to 337, with 40 of them 580. In two calls, the short
+// sequences' rows first, they take 86 (chains), 291 and 298 (trees).
 template <int KD, int VD>
 hipError_t launch(const DeltaRuleArgs& a, hipStream_t s) {
   const int rows = (a.st.total + a.st.num_seq - 1) / a.st.num_seq;

@@ -10,7 +10,8 @@
 // (3.7 TB/s); 192 x 48 heads of 128 with gates 4.6 us. A part of a wave
 // against a workgroup, rows x groups: 192 x 48 of 128 4.1 us / 6.5, 512 x 16 of 256 5.0 /
 // 6.5, 192 x 48 of 256 5.5 / 6.9, 32 x 1 of 256 3.3 / 3.1, 32 x 1 of 512 3.5 / 3.1, 512 x 8
-// of 512 5.0 / 4.7, 192 x 48 of 512 8.6 / 7.6.
+// of 512 5.0 / 4.7, 192 x 48 of 512 8.6 / 7.6. Widths above 16384 (32 values a thread of
+// 1024, at most 128 registers) spill 11 to 16 registers.
 #include "delta_internal.h"
 #include "w12_device.h"
 
